@@ -152,7 +152,7 @@ def _inputs(case, seed, dev):
         s["ys"] = (normal(T, D) * rows.flip(0) * 3.0).to(DTYPES[c["y"]])
         s["w_post"] = 1.0 + normal(D, scale=0.1)
         s["w_pre"] = 1.0 + normal(D, scale=0.1)
-        shape = {"none": None, "channel": (D,), "row": (T,), "full": (T, D)}[c["gate"]]
+        shape = {"none": None, "channel": (D,), "row": (T, 1), "full": (T, D)}[c["gate"]]
         s["gates"] = None if shape is None else torch.rand(shape, generator=g, device=dev) + 0.25
         s["scale"] = 0.875
         if op == "norm_bwd":
@@ -209,13 +209,6 @@ def _act_slope(v, act):
         + v * torch.exp(v * v * -0.5) * (1.0 / math.sqrt(2.0 * math.pi))
 
 
-def _gate_of(s):
-    g = s["gates"]
-    if g is None:
-        return None
-    return g[:, None] if s["gate"] == "row" else g
-
-
 def _kept(x):
     """What the 8-bit checkpoint of x (T x K) stands for: in each run of 32 rows of
     a column, whole multiples (-127..127) of the smallest power of two (at least
@@ -246,7 +239,7 @@ def _plain(s):
         return _act(v, s["act"]).to(DTYPES[s["out"]])
     if op in ("norm", "norm_bwd"):
         x, y, a = s["xs"].float(), s["ys"].float(), s["scale"]
-        g = _gate_of(s)
+        g = s["gates"]
         r2 = torch.rsqrt((y * y).mean(1, keepdim=True) + EPS)
         n = y * r2
         p = n * s["w_post"]
@@ -264,7 +257,7 @@ def _plain(s):
                "dw_post": (dp * n).sum(0), "dw_pre": (dh * u * r1).sum(0)}
         if g is not None:
             dg = du * p
-            out["dgate"] = {"channel": lambda: dg.sum(0), "row": lambda: dg.sum(1),
+            out["dgate"] = {"channel": lambda: dg.sum(0), "row": lambda: dg.sum(1, keepdim=True),
                             "full": lambda: dg}[s["gate"]]()
         return out
     if op == "ckpt_act":
@@ -350,7 +343,7 @@ def exact(case, seed):
         D = s["D"]
         x, y = s["xs"].double(), s["ys"].double()
         w2, w1, a = s["w_post"].double(), s["w_pre"].double(), s["scale"]
-        g = 1.0 if s["gates"] is None else _gate_of(s).double()
+        g = 1.0 if s["gates"] is None else s["gates"].double()
         rms_y = ((y ** 2).sum(1, keepdim=True) / D + EPS).sqrt()
         p = y / rms_y * w2
         u = a * x + g * p
@@ -368,7 +361,7 @@ def exact(case, seed):
         if s["gates"] is not None:
             dg = du * p
             out["dgate"] = dg.sum(0) if s["gate"] == "channel" else \
-                dg.sum(1) if s["gate"] == "row" else dg
+                dg.sum(1, keepdim=True) if s["gate"] == "row" else dg
         return out
     if op == "ckpt_act":
         z, k = s["zs"].double(), _kept64(s["zs"])
