@@ -11,25 +11,37 @@ missing or unloadable library is an error, never a fallback.
     C = g7.gemm_bf16_f32acc(A_bf16, B_bf16)   # A: MxK, B: KxN, CUDA tensors
     C = g7.gemm_f32(A_f32, B_f32)
 
+Beside the GEMM stand the operators of a transformer layer around it: products
+with 4-bit weights (``gemm_w4``), norms with gate and residual
+(``gemm_norm_gate``) and 8-bit activation checkpoints (``gemm_ckpt8_*``);
+``layer_example`` runs them together.
+
 The raw ctypes entry points (integer addresses) are in ``dense_gemm_07_gb300.abi``.
 """
 from __future__ import annotations
 
 from . import _abi as abi
 from ._build import build
+from ._errors import GemmError
+
+# The layer operators import torch; they are loaded on first use.
+_LAYER = ("gemm_w4", "w4_pack", "w4_quantize", "w4_unpack",
+          "gemm_norm_gate", "gemm_norm_gate_bwd", "NormGateGrads",
+          "gemm_ckpt8_pack", "gemm_ckpt8_unpack", "gemm_ckpt8_act_grad",
+          "gemm_ckpt8_wgrad", "Ckpt8")
 
 __all__ = ["abi", "build", "GemmError", "gemm_f32", "gemm_bf16_f32acc", "gemm_f32_ladder",
            "gemm_f32_ex", "gemm_bf16_f32acc_ex",
            "gemm_f32_host", "gemm_bf16_f32acc_host", "gemm_get_device_status",
-           "gemm_status_string", "plan"]
+           "gemm_status_string", "plan", *_LAYER]
 
 
-class GemmError(RuntimeError):
-    """A nonzero gemm_status_t from the library."""
-
-    def __init__(self, status: int, where: str):
-        self.status = status
-        super().__init__(f"{where}: {abi.gemm_status_string(status)} (status {status})")
+def __getattr__(name):
+    if name in _LAYER:
+        from . import layer
+        globals().update({n: getattr(layer, n) for n in _LAYER})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def gemm_status_string(status: int) -> str:

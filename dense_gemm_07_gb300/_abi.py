@@ -46,6 +46,37 @@ class GemmEpilogue(ctypes.Structure):
                 ("bias", ctypes.c_void_p), ("activation", ctypes.c_int32)]
 
 
+class GemmW4(ctypes.Structure):
+    _fields_ = [("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("ld_scales", ctypes.c_int64), ("zeros", ctypes.c_void_p),
+                ("ld_zeros", ctypes.c_int64), ("group", ctypes.c_int32)]
+
+
+class GemmNormGateArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_type", ctypes.c_int32),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("y_type", ctypes.c_int32),
+                ("w_post", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("ld_gate", ctypes.c_int64), ("gate_mode", ctypes.c_int32),
+                ("w_pre", ctypes.c_void_p), ("alpha", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class GemmNormGateGrads(ctypes.Structure):
+    _fields_ = [("d_x_out", ctypes.c_void_p), ("ld_d_x_out", ctypes.c_int64),
+                ("dh", ctypes.c_void_p), ("ld_dh", ctypes.c_int64), ("dh_type", ctypes.c_int32),
+                ("dx", ctypes.c_void_p), ("ld_dx", ctypes.c_int64),
+                ("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64),
+                ("dgate", ctypes.c_void_p), ("dw_post", ctypes.c_void_p),
+                ("dw_pre", ctypes.c_void_p)]
+
+
+TYPE_F32 = 0
+TYPE_BF16 = 1
+GATE_NONE = 0
+GATE_CHANNEL = 1
+GATE_ROW = 2
+GATE_FULL = 3
+NORM_MAX_WIDTH = 16384
 ACT_NONE = 0
 ACT_RELU = 1
 ACT_GELU = 2
@@ -78,6 +109,24 @@ SIGNATURES = [
     ("gemm_pair_units", _i64, [_i64, _i64, _i64, _i32, _i32, _i32, _vp, _i64]),
     ("gemm_set_bf16_schedule", _i32, [_i32]),
     ("gemm_set_bf16_small_limit", _i64, [_i64]),
+    ("gemm_w4_packed_bytes", _i64, [_i64, _i64]),
+    ("gemm_w4", _i32, [_i64, _i64, _i64, _vp, _i64, ctypes.POINTER(GemmW4), _vp, _i64,
+                       ctypes.c_int32, ctypes.POINTER(GemmEpilogue), _vp]),
+    ("gemm_w4_pack", _i32, [_i64, _i64, _vp, _i64, _vp, _vp]),
+    ("gemm_w4_quantize", _i32, [_i64, _i64, ctypes.c_int32, _vp, _i64, ctypes.c_int32, _vp,
+                                _vp, _i64, _vp, _i64, _vp]),
+    ("gemm_w4_unpack", _i32, [_i64, _i64, ctypes.POINTER(GemmW4), _vp, _i64, _vp]),
+    ("gemm_norm_gate", _i32, [ctypes.POINTER(GemmNormGateArgs), _vp, _i64, _vp, _i64, _vp]),
+    ("gemm_norm_gate_bwd", _i32, [ctypes.POINTER(GemmNormGateArgs),
+                                  ctypes.POINTER(GemmNormGateGrads), _vp]),
+    ("gemm_ckpt8_bytes", _i64, [_i64, _i64]),
+    ("gemm_ckpt8_pack", _i32, [_i64, _i64, _vp, _i64, ctypes.c_int32, _vp, _vp,
+                               ctypes.c_int32, _vp, _i64, _vp]),
+    ("gemm_ckpt8_unpack", _i32, [_i64, _i64, _vp, _vp, _vp, _i64, ctypes.c_int32, _vp]),
+    ("gemm_ckpt8_act_grad", _i32, [_i64, _i64, _vp, _i64, ctypes.c_int32, _vp, _vp,
+                                   ctypes.c_int32, _vp, _i64, _vp, _vp]),
+    ("gemm_ckpt8_wgrad", _i32, [_i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i64,
+                                ctypes.c_float, _vp]),
 ]
 
 
@@ -221,3 +270,58 @@ def gemm_pair_units(M, N, K, max_pairs, pair, schedule=SCHEDULE_AUTO):
     n2 = lib().gemm_pair_units(M, N, K, max_pairs, schedule, pair, buf, n)
     assert n2 == n
     return [tuple(buf[9 * i:9 * i + 9]) for i in range(n)]
+
+
+def gemm_w4_packed_bytes(K, N):
+    return lib().gemm_w4_packed_bytes(K, N)
+
+
+def gemm_w4(M, N, K, A, lda, w, C, ldc, c_type, epilogue, stream):
+    """w: a GemmW4; epilogue: a GemmEpilogue or None."""
+    return lib().gemm_w4(M, N, K, A, lda, _epi(w), C, ldc, c_type, _epi(epilogue), stream)
+
+
+def gemm_w4_pack(K, N, codes, ld, packed, stream):
+    return lib().gemm_w4_pack(K, N, codes, ld, packed, stream)
+
+
+def gemm_w4_quantize(K, N, group, B, ldb, b_type, packed, scales, ld_scales, zeros, ld_zeros,
+                     stream):
+    return lib().gemm_w4_quantize(K, N, group, B, ldb, b_type, packed, scales, ld_scales,
+                                  zeros, ld_zeros, stream)
+
+
+def gemm_w4_unpack(K, N, w, B, ldb, stream):
+    return lib().gemm_w4_unpack(K, N, _epi(w), B, ldb, stream)
+
+
+def gemm_norm_gate(args, x_out, ld_x_out, h, ldh, stream):
+    """args: a GemmNormGateArgs."""
+    return lib().gemm_norm_gate(_epi(args), x_out, ld_x_out, h, ldh, stream)
+
+
+def gemm_norm_gate_bwd(args, grads, stream):
+    """args: a GemmNormGateArgs; grads: a GemmNormGateGrads."""
+    return lib().gemm_norm_gate_bwd(_epi(args), _epi(grads), stream)
+
+
+def gemm_ckpt8_bytes(T, N):
+    return lib().gemm_ckpt8_bytes(T, N)
+
+
+def gemm_ckpt8_pack(T, N, X, ldx, x_type, q, scales, activation, act_out, ld_act, stream):
+    return lib().gemm_ckpt8_pack(T, N, X, ldx, x_type, q, scales, activation, act_out, ld_act,
+                                 stream)
+
+
+def gemm_ckpt8_unpack(T, N, q, scales, out, ld, out_type, stream):
+    return lib().gemm_ckpt8_unpack(T, N, q, scales, out, ld, out_type, stream)
+
+
+def gemm_ckpt8_act_grad(T, N, G, ldg, g_type, q, scales, activation, dZ, ld_dz, dbias, stream):
+    return lib().gemm_ckpt8_act_grad(T, N, G, ldg, g_type, q, scales, activation, dZ, ld_dz,
+                                     dbias, stream)
+
+
+def gemm_ckpt8_wgrad(T, K, N, q, scales, dY, ld_dy, dW, ldw, beta, stream):
+    return lib().gemm_ckpt8_wgrad(T, K, N, q, scales, dY, ld_dy, dW, ldw, beta, stream)

@@ -11,6 +11,7 @@
 
 #include "../../include/gemm07.h"
 #include "kernels.h"
+#include "layer.h"
 #include "tile_order.cuh"
 
 namespace g07 {
@@ -48,7 +49,8 @@ enum ScratchUse {
   kScratchSplitK = 1,   // FP32 split-K counters (kept zero) + partial sums
   kScratchPack = 2,     // BF16 operands copied to aligned rows
   kScratchSmall = 3,    // BF16 small problems: counters (kept zero) + partial tiles
-  kScratchUses = 4
+  kScratchLayer = 4,  // column sums and operand copies of the layer operators
+  kScratchUses = 5
 };
 struct StreamScratch {
   cudaStream_t stream = nullptr;
@@ -1018,6 +1020,42 @@ gemm_status_t run_bf16_noalloc(int64_t M, int64_t N, int64_t K,
 }
 
 }  // namespace
+
+// ---- services for the layer operators' entry points (layer.h)
+
+gemm_status_t layer_device(LayerDevice* out) {
+  DeviceState* d = nullptr;
+  const gemm_status_t s = device_state(&d);
+  if (s != GEMM_OK) return s;
+  out->sms = d->sms;
+  out->status = d->status;
+  return GEMM_OK;
+}
+
+gemm_status_t layer_scratch(cudaStream_t stream, int64_t bytes, LayerScratch* out) {
+  DeviceState* d = nullptr;
+  const gemm_status_t s = device_state(&d);
+  if (s != GEMM_OK) return s;
+  bool fresh = false;
+  return call_scratch(d, stream, kScratchLayer, bytes, &out->ptr, &fresh, &out->owned);
+}
+
+void layer_scratch_done(const LayerScratch& s, cudaStream_t stream) {
+  if (s.owned) pool_free(s.ptr, stream);
+}
+
+gemm_status_t layer_epilogue(const gemm_epilogue_t* e, EpiParams* out) { return to_epi(e, out); }
+
+gemm_status_t layer_from_cuda(cudaError_t e) { return from_cuda(e); }
+
+gemm_status_t layer_gemm_bf16(int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda,
+                              const uint16_t* B, int64_t ldb, float* C, int64_t ldc, float beta,
+                              cudaStream_t stream) {
+  EpiParams epi = epi_identity();
+  epi.beta = beta;
+  return run_bf16(M, N, K, A, lda, B, ldb, C, ldc, stream, epi);
+}
+
 }  // namespace g07
 
 using namespace g07;

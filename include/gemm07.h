@@ -431,6 +431,204 @@ GEMM07_API gemm_status_t gemm_plan_f32(int64_t M, int64_t N, int64_t K,
                             const void *B, int64_t ldb,
                             const void *C, int64_t ldc, gemm_plan_t *plan);
 
+/* ------------------------------------------------------------------------
+ * Operators of a transformer layer around the GEMM.  They share its
+ * conventions (sizes, device pointers, streams, determinism, thread safety,
+ * graph capture, errors).  BF16 arrays are passed as their 16-bit patterns.
+ * ------------------------------------------------------------------------ */
+
+typedef enum gemm_type {
+    GEMM_TYPE_F32 = 0,
+    GEMM_TYPE_BF16 = 1
+} gemm_type_t;
+
+/*
+ * 4-bit weights: a K x N matrix
+ *   W[k][n] = (q[k][n] - z[g][n]) * s[g][n],   g = k / group,
+ * with codes q and zero points z whole numbers 0..15 and s BF16.
+ *   packed: gemm_w4_packed_bytes(K, N) bytes, 16-byte aligned: tiles of 16
+ *           columns by 128 rows, 1 KB each, tile (n / 16, k / 128) at index
+ *           (n / 16) * ceil(K / 128) + k / 128.  In a tile, 32-bit word
+ *           ((n % 16) * 4 + (k % 32) / 8) * 4 + (k % 128) / 32 holds the rows
+ *           k .. k + 7 of column n (k a multiple of 8): row k + e at bits
+ *           4 * (e / 2 + 4 * (e % 2)).  Codes past K or N may hold anything.
+ *   scales: ceil(K / group) x N, row stride ld_scales.
+ *   zeros:  ceil(K / group) x N bytes, row stride ld_zeros, or NULL: z = 8.
+ *   group:  32, 64 or 128.
+ */
+typedef struct gemm_w4 {
+    const void *packed;
+    const uint16_t *scales;
+    int64_t ld_scales;
+    const uint8_t *zeros;
+    int64_t ld_zeros;
+    int32_t group;
+} gemm_w4_t;
+
+/* Bytes of a packed K x N matrix; -1 for a size out of range. */
+GEMM07_API int64_t gemm_w4_packed_bytes(int64_t K, int64_t N);
+
+/*
+ * gemm_w4 -- C := act(alpha * A * W + beta * C + bias), A M x K BF16, C M x N
+ * of type c_type, epilogue as for gemm_bf16_f32acc_ex (NULL: the product).
+ *   Meant for the few rows of a decode step: the weights are read once for
+ *   every 16 rows of A.  For a prompt, write W out once with gemm_w4_unpack
+ *   and use gemm_bf16_f32acc.
+ *   Arithmetic: q - z times A exactly, summed in FP32 over a group, times the
+ *   group's scale in FP32; C is rounded once.
+ *   Any alignment of A and C is accepted; A on 16 bytes with lda a multiple of
+ *   8 is read 16 bytes at a time.
+ */
+GEMM07_API gemm_status_t gemm_w4(int64_t M, int64_t N, int64_t K,
+                                 const uint16_t *A, int64_t lda, const gemm_w4_t *W,
+                                 void *C, int64_t ldc, int32_t c_type,
+                                 const gemm_epilogue_t *epilogue, void *stream);
+
+/* Codes (K x N bytes, the low four bits of each) into the packed order. */
+GEMM07_API gemm_status_t gemm_w4_pack(int64_t K, int64_t N, const uint8_t *codes,
+                                      int64_t ld, void *packed, void *stream);
+
+/*
+ * Quantise B (K x N, b_type) to the nearest codes, group by group: packed,
+ * scales and, when zeros is not NULL, zero points are written.
+ *   zeros NULL: s = max|w| / 7, codes 1..15 around 8.
+ *   zeros set:  s = (hi - lo) / 15 over the group's range widened to hold 0.
+ * s is rounded to BF16 before the codes are taken.  A group with a value that
+ * is not finite gets a NaN scale.
+ */
+GEMM07_API gemm_status_t gemm_w4_quantize(int64_t K, int64_t N, int32_t group,
+                                          const void *B, int64_t ldb, int32_t b_type,
+                                          void *packed, uint16_t *scales, int64_t ld_scales,
+                                          uint8_t *zeros, int64_t ld_zeros, void *stream);
+
+/* W as a K x N BF16 matrix, each (q - z) * s rounded once. */
+GEMM07_API gemm_status_t gemm_w4_unpack(int64_t K, int64_t N, const gemm_w4_t *W,
+                                        uint16_t *B, int64_t ldb, void *stream);
+
+/*
+ * gemm_norm_gate -- the step between two blocks of a residual network, for
+ * each of T rows (tokens) of width D <= 16384: RMS norm of the block's output
+ * y, its gate, the scaled residual, and the RMS norm before the next block:
+ *   p = y / rms(y) * w_post          (p = y when w_post is NULL)
+ *   u = alpha * x + gate * p         -> x_out, in x's type
+ *   h = u / rms(u) * w_pre           -> h, BF16: the next GEMM's A
+ * with rms(v) = sqrt(mean(v^2) + eps), in FP32 from the values as loaded; h is
+ * taken from u before x_out's rounding.
+ *   x: T x D of type x_type; y: T x D of type y_type, or NULL (u = alpha * x;
+ *   w_post and gate are then NULL too).  gemm_bf16_f32acc's FP32 C is a y.
+ *   gate: FP32, gate_mode GEMM_GATE_NONE (NULL), _CHANNEL (D values), _ROW (T
+ *   values) or _FULL (T x D, row stride ld_gate).
+ *   w_post, w_pre: D floats or NULL.  x_out may be NULL, and may be x.  h is
+ *   NULL if and only if w_pre is.
+ *   Strides are in elements, at least D.  Rows on 16 bytes with strides and D
+ *   multiples of 8 are read 16 bytes at a time, others element by element.
+ */
+typedef enum gemm_gate_mode {
+    GEMM_GATE_NONE = 0,
+    GEMM_GATE_CHANNEL = 1,
+    GEMM_GATE_ROW = 2,
+    GEMM_GATE_FULL = 3
+} gemm_gate_mode_t;
+
+typedef struct gemm_norm_gate_args {
+    int64_t T, D;
+    const void *x;
+    int64_t ldx;
+    int32_t x_type;
+    const void *y;
+    int64_t ldy;
+    int32_t y_type;
+    const float *w_post;
+    const float *gate;
+    int64_t ld_gate;
+    int32_t gate_mode;
+    const float *w_pre;
+    float alpha, eps;
+} gemm_norm_gate_args_t;
+
+GEMM07_API gemm_status_t gemm_norm_gate(const gemm_norm_gate_args_t *args,
+                                        void *x_out, int64_t ld_x_out,
+                                        uint16_t *h, int64_t ldh, void *stream);
+
+/*
+ * gemm_norm_gate_bwd -- the gradient of gemm_norm_gate, from the same x, y,
+ * weights and gate (nothing has to be kept from the forward call):
+ *   d_x_out: T x D in x's type, the gradient of x_out, or NULL (zero);
+ *   dh:      T x D of type dh_type, the gradient of h; NULL iff w_pre is.
+ * Outputs: dx in x's type; dy BF16 (the next gradient GEMMs' operand; NULL iff
+ * y is); dgate FP32 in gate's layout with the row stride ld_gate; dw_post and
+ * dw_pre, D floats.  dgate, dw_post and dw_pre are NULL iff their inputs are.
+ * Sums over rows are FP32 in a fixed order.  dx may be d_x_out or x.
+ */
+typedef struct gemm_norm_gate_grads {
+    const void *d_x_out;
+    int64_t ld_d_x_out;
+    const void *dh;
+    int64_t ld_dh;
+    int32_t dh_type;
+    void *dx;
+    int64_t ld_dx;
+    uint16_t *dy;
+    int64_t ld_dy;
+    float *dgate;
+    float *dw_post;
+    float *dw_pre;
+} gemm_norm_gate_grads_t;
+
+GEMM07_API gemm_status_t gemm_norm_gate_bwd(const gemm_norm_gate_args_t *args,
+                                            const gemm_norm_gate_grads_t *grads,
+                                            void *stream);
+
+/*
+ * 8-bit checkpoints: a T x N matrix of activations kept for the backward pass.
+ * Each run of 32 rows of a column (rows 32 p .. 32 p + 31) shares the step
+ * 2^e, the smallest power of two (-126 <= e <= 121) with max|x| <= 127 * 2^e,
+ * and keeps round(x / 2^e), ties to even (magnitudes past 127 * 2^121 as that).
+ * A run with a value that is not finite is kept as NaN.
+ *   q: gemm_ckpt8_bytes(T, N) bytes, 16-byte aligned: the value of row t,
+ *      column n at ((t / 16) * N + n) * 16 + t % 16, rows past T as zeros up
+ *      to a multiple of 32.
+ *   scales: ceil(T / 32) x N bytes, e + 127, or 255 for NaN.
+ */
+GEMM07_API int64_t gemm_ckpt8_bytes(int64_t T, int64_t N);
+
+/* Keep X (T x N, x_type).  With act_out not NULL, also write act(X) there in
+ * BF16 (activation: a gemm_activation_t), the next GEMM's A. */
+GEMM07_API gemm_status_t gemm_ckpt8_pack(int64_t T, int64_t N, const void *X, int64_t ldx,
+                                         int32_t x_type, void *q, uint8_t *scales,
+                                         int32_t activation, uint16_t *act_out,
+                                         int64_t ld_act, void *stream);
+
+/* The values kept, T x N of type out_type (exact in both). */
+GEMM07_API gemm_status_t gemm_ckpt8_unpack(int64_t T, int64_t N, const void *q,
+                                           const uint8_t *scales, void *out, int64_t ld,
+                                           int32_t out_type, void *stream);
+
+/*
+ * The gradient through an activation whose input Z was kept:
+ *   dZ = G * act'(Z kept)  (T x N, BF16),   dbias[n] = sum over rows of dZ,
+ * G of type g_type; dbias (N floats, or NULL) sums dZ before its rounding, in
+ * FP32 and a fixed order.  ReLU's slope at 0 is 0; a value kept as NaN gives
+ * NaN.
+ */
+GEMM07_API gemm_status_t gemm_ckpt8_act_grad(int64_t T, int64_t N, const void *G, int64_t ldg,
+                                             int32_t g_type, const void *q,
+                                             const uint8_t *scales, int32_t activation,
+                                             uint16_t *dZ, int64_t ld_dz, float *dbias,
+                                             void *stream);
+
+/*
+ * The weight gradient of a layer whose input X (T x K) was kept:
+ *   dW := (X kept)^T * dY + beta * dW,   dY T x N BF16, dW K x N FP32.
+ * The values kept are exact BF16 numbers, multiplied exactly and summed in
+ * FP32.  beta == 0: the prior contents of dW are not read.  T == 0: dW :=
+ * beta * dW.
+ */
+GEMM07_API gemm_status_t gemm_ckpt8_wgrad(int64_t T, int64_t K, int64_t N, const void *q,
+                                          const uint8_t *scales, const uint16_t *dY,
+                                          int64_t ld_dy, float *dW, int64_t ldw, float beta,
+                                          void *stream);
+
 #ifdef __cplusplus
 }
 #endif
