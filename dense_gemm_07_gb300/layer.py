@@ -25,16 +25,19 @@ _F32 = (torch.float32,)
 
 def _matrix(t, name, dtypes, device, shape=None):
     """Row stride of a 2-D tensor, after its checks."""
-    if t.dim() != 2:
+    size = t.shape
+    if len(size) != 2:
         raise ValueError(f"{name} must be 2-D")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    rows, cols = t.shape
-    if shape is not None and (rows, cols) != shape:
+    rows, cols = size
+    if shape is not None and size != shape:
         raise ValueError(f"{name} must be {shape[0]} x {shape[1]}, not {rows} x {cols}")
     r, c = t.stride()
+    if c == 1 and r >= cols > 0:
+        return r
     if cols > 1 and c != 1:
         raise ValueError(f"{name}: rows must be contiguous (stride(1) == 1)")
     if rows > 1 and cols > 0 and r < cols:
@@ -50,7 +53,7 @@ def _vector(t, name, dtype, device, n):
 
 
 def _cuda(t, name):
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return t.device
 
@@ -64,26 +67,38 @@ def _bytes16(t, name, numel, device):
 
 
 def _act(activation):
-    if activation not in _ACTS:
+    act = _ACTS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of {sorted(_ACTS)}")
-    return _ACTS[activation]
+    return act
 
 
 def _ptr(t):
-    return t.data_ptr() if t is not None and t.numel() else None
+    """Address of a tensor's elements (0 when it has none), None for no tensor."""
+    return None if t is None else t.data_ptr()
 
 
-def _run(fn, device, stream, *args):
+@functools.lru_cache(maxsize=None)
+def _entry(name):
+    return getattr(abi.lib(), name)
+
+
+# The handle of a device's current stream, without a Stream object around it
+# (0.1 us where torch.cuda.current_stream takes 2 us).
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _run(name, device, stream, *args):
     """Calls a C entry point with the device current and the stream last."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if torch.cuda.current_device() == device.index:
-        s = fn(*args, stream.cuda_stream)
+    index = device.index
+    handle = _current_stream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        s = _entry(name)(*args, handle)
     else:
         with torch.cuda.device(device):
-            s = fn(*args, stream.cuda_stream)
-    if s != abi.GEMM_OK:
-        raise GemmError(s, fn.__name__)
+            s = _entry(name)(*args, handle)
+    if s:
+        raise GemmError(s, name)
 
 
 def _output(out, name, shape, dtype, device):
@@ -138,7 +153,7 @@ def gemm_w4(A, packed, scales, zeros=None, group=128, out=None, alpha=1.0, beta=
     if bias is not None:
         _vector(bias, "bias", torch.float32, device, N)
     epi = abi.GemmEpilogue(alpha, beta, _ptr(bias), _act(activation))
-    _run(abi.gemm_w4, device, stream, M, N, K, _ptr(A), lda, w, _ptr(out), ldc,
+    _run("gemm_w4", device, stream, M, N, K, _ptr(A), lda, w, _ptr(out), ldc,
          _TYPES[out_dtype], epi)
     return out
 
@@ -150,7 +165,7 @@ def w4_pack(codes, stream=None):
     ld = _matrix(codes, "codes", (torch.uint8,), device)
     K, N = codes.shape
     packed = torch.empty(_packed_bytes(K, N), dtype=torch.uint8, device=device)
-    _run(abi.gemm_w4_pack, device, stream, K, N, _ptr(codes), ld, _ptr(packed))
+    _run("gemm_w4_pack", device, stream, K, N, _ptr(codes), ld, _ptr(packed))
     return packed
 
 
@@ -167,7 +182,7 @@ def w4_quantize(B, group=128, symmetric=True, stream=None):
     scales = torch.empty((G, N), dtype=torch.bfloat16, device=device)
     zeros = None if symmetric else torch.empty((G, N), dtype=torch.uint8, device=device)
     ld = max(N, 1)
-    _run(abi.gemm_w4_quantize, device, stream, K, N, group, _ptr(B), ldb, _TYPES[B.dtype],
+    _run("gemm_w4_quantize", device, stream, K, N, group, _ptr(B), ldb, _TYPES[B.dtype],
          _ptr(packed), _ptr(scales), ld, _ptr(zeros), ld)
     return packed, scales, zeros
 
@@ -181,7 +196,7 @@ def w4_unpack(packed, scales, zeros=None, group=128, K=None, stream=None):
     K = scales.shape[0] * group if K is None else K
     N, w = _w4(packed, scales, zeros, group, K, device)
     out = torch.empty((K, N), dtype=torch.bfloat16, device=device)
-    _run(abi.gemm_w4_unpack, device, stream, K, N, w, _ptr(out), max(N, 1))
+    _run("gemm_w4_unpack", device, stream, K, N, w, _ptr(out), max(N, 1))
     return out
 
 
@@ -239,7 +254,7 @@ def gemm_norm_gate(x, y=None, weight_post=None, gate=None, weight_pre=None,
         h, ldh = _output(h, "h", (T, D), torch.bfloat16, device)
     elif h is not None:
         raise ValueError("h needs weight_pre")
-    _run(abi.gemm_norm_gate, device, stream, args, _ptr(x_out), ld_o, _ptr(h), ldh)
+    _run("gemm_norm_gate", device, stream, args, _ptr(x_out), ld_o, _ptr(h), ldh)
     return x_out, h
 
 
@@ -274,7 +289,7 @@ def gemm_norm_gate_bwd(x, y=None, d_x_out=None, d_h=None, weight_post=None, gate
     dgate = None if gate is None else empty(gate.shape, dtype=torch.float32)
     grads = abi.GemmNormGateGrads(_ptr(d_x_out), ld_o, _ptr(d_h), ldh, h_type, _ptr(dx), D,
                                   _ptr(dy), D, _ptr(dgate), _ptr(dw_post), _ptr(dw_pre))
-    _run(abi.gemm_norm_gate_bwd, device, stream, args, grads)
+    _run("gemm_norm_gate_bwd", device, stream, args, grads)
     return NormGateGrads(dx, dy, dw_post, dgate, dw_pre)
 
 
@@ -311,12 +326,12 @@ def gemm_ckpt8_pack(X, activation=None, act_out=None, stream=None):
     if activation is None:
         if act_out is not None:
             raise ValueError("act_out needs an activation")
-        _run(abi.gemm_ckpt8_pack, device, stream, T, N, _ptr(X), ldx, _TYPES[X.dtype],
+        _run("gemm_ckpt8_pack", device, stream, T, N, _ptr(X), ldx, _TYPES[X.dtype],
              _ptr(q), _ptr(scales), abi.ACT_NONE, None, max(N, 1))
         return kept
     act = _act(activation)
     act_out, ld = _output(act_out, "act_out", (T, N), torch.bfloat16, device)
-    _run(abi.gemm_ckpt8_pack, device, stream, T, N, _ptr(X), ldx, _TYPES[X.dtype],
+    _run("gemm_ckpt8_pack", device, stream, T, N, _ptr(X), ldx, _TYPES[X.dtype],
          _ptr(q), _ptr(scales), act, _ptr(act_out), ld)
     return kept, act_out
 
@@ -327,7 +342,7 @@ def gemm_ckpt8_unpack(kept, dtype=torch.bfloat16, stream=None):
     if dtype not in _TYPES:
         raise TypeError("dtype must be torch.float32 or torch.bfloat16")
     out = torch.empty((T, N), dtype=dtype, device=device)
-    _run(abi.gemm_ckpt8_unpack, device, stream, T, N, _ptr(kept.q), _ptr(kept.scales),
+    _run("gemm_ckpt8_unpack", device, stream, T, N, _ptr(kept.q), _ptr(kept.scales),
          _ptr(out), max(N, 1), _TYPES[dtype])
     return out
 
@@ -340,7 +355,7 @@ def gemm_ckpt8_act_grad(grad, kept, activation, bias_grad=True, out=None, stream
     act = _act(activation)
     out, ld = _output(out, "out", (T, N), torch.bfloat16, device)
     dbias = torch.empty(N, dtype=torch.float32, device=device) if bias_grad else None
-    _run(abi.gemm_ckpt8_act_grad, device, stream, T, N, _ptr(grad), ldg, _TYPES[grad.dtype],
+    _run("gemm_ckpt8_act_grad", device, stream, T, N, _ptr(grad), ldg, _TYPES[grad.dtype],
          _ptr(kept.q), _ptr(kept.scales), act, _ptr(out), ld, _ptr(dbias))
     return out, dbias
 
@@ -356,6 +371,6 @@ def gemm_ckpt8_wgrad(kept, dY, out=None, beta=0.0, stream=None):
     if beta != 0.0 and out is None:
         raise ValueError("beta != 0 reads dW: pass its prior contents as `out`")
     out, ldw = _output(out, "out", (K, N), torch.float32, device)
-    _run(abi.gemm_ckpt8_wgrad, device, stream, T, K, N, _ptr(kept.q), _ptr(kept.scales),
+    _run("gemm_ckpt8_wgrad", device, stream, T, K, N, _ptr(kept.q), _ptr(kept.scales),
          _ptr(dY), ld, _ptr(out), ldw, beta)
     return out
