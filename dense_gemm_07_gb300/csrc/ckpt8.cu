@@ -24,69 +24,160 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// x * Phi(x) as the GEMM's epilogue computes it, and its slope
-// Phi(x) + x phi(x).
-__device__ __forceinline__ float act_value(float v, int act) {
-  return epi_apply(EpiParams{1.0f, 0.0f, nullptr, act}, v, 0.0f, 0.0f);
+// Phi(-|x|), the lower tail of the normal distribution, times 2, and
+// exp(-x^2 / 2): Abramowitz and Stegun, "Handbook of Mathematical Functions",
+// 7.1.26, erfc(z) = (a1 t + .. + a5 t^5) exp(-z^2), t = 1 / (1 + p z), at
+// z = |x| / sqrt 2, within 1.5e-7 absolute.  GELU and its slope share the
+// exponential; 12 instructions where erff and expf take about 50, which bound
+// these kernels (2048 x 11008 pack and gradient: 185 us).
+__device__ __forceinline__ float normal_tail2(float x, float* exp_part) {
+  const float t = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678f, fabsf(x), 1.0f));
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * x * -0.72134752f));  // log2(e) / 2
+  float p = fmaf(t, 1.061405429f, -1.453152027f);
+  p = fmaf(t, p, 1.421413741f);
+  p = fmaf(t, p, -0.284496736f);
+  p = fmaf(t, p, 0.254829592f);
+  *exp_part = e;
+  return p * t * e;
 }
-__device__ __forceinline__ float act_slope(float v, int act) {
-  if (act == 1) return v > 0.0f ? 1.0f : (v == v ? 0.0f : v);
-  if (act == 2)
-    return 0.5f * (1.0f + erff(v * 0.70710678118654752f)) +
-           v * expf(-0.5f * v * v) * 0.39894228040143268f;
+// x Phi(x), and its slope Phi(x) + x phi(x).
+template <int ACT>
+__device__ __forceinline__ float act_value(float v) {
+  if (ACT == 1) return fmaxf(v, 0.0f);
+  if (ACT == 2) {
+    float e;
+    const float tail = 0.5f * normal_tail2(v, &e);
+    return v * (v > 0.0f ? 1.0f - tail : tail);
+  }
+  return v;
+}
+template <int ACT>
+__device__ __forceinline__ float act_slope(float v) {
+  if (ACT == 1) return v > 0.0f ? 1.0f : (v == v ? 0.0f : v);
+  if (ACT == 2) {
+    float e;
+    const float tail = 0.5f * normal_tail2(v, &e);
+    return fmaf(v * 0.39894228f, e, v > 0.0f ? 1.0f - tail : tail);
+  }
   return 1.0f;
 }
 
-template <typename X>
+// C adjacent elements (C = 1, or 2 on a boundary of two) of a row.
+template <int C>
+__device__ __forceinline__ void load_cols(const float* p, float (&v)[C]) {
+  if constexpr (C == 2) {
+    const float2 a = *reinterpret_cast<const float2*>(p);
+    v[0] = a.x;
+    v[1] = a.y;
+  } else {
+    v[0] = *p;
+  }
+}
+template <int C>
+__device__ __forceinline__ void load_cols(const __nv_bfloat16* p, float (&v)[C]) {
+  if constexpr (C == 2) {
+    const uint32_t a = *reinterpret_cast<const uint32_t*>(p);
+    v[0] = bf16_lo(a);
+    v[1] = bf16_hi(a);
+  } else {
+    v[0] = __bfloat162float(*p);
+  }
+}
+template <int C>
+__device__ __forceinline__ void store_cols(__nv_bfloat16* p, const float (&v)[C]) {
+  if constexpr (C == 2)
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16(v[0], v[1]);
+  else
+    *p = __float2bfloat16_rn(v[0]);
+}
+
+// The low byte of the FP32 bits of v + 1.5 * 2^23 is round(v), ties to even, in
+// two's complement (|v| <= 127).
+__device__ __forceinline__ uint32_t round_byte(float v, float inverse_step) {
+  return __float_as_uint(fmaf(v, inverse_step, 12582912.0f));
+}
+__device__ __forceinline__ uint32_t four_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// A thread owns C adjacent columns of a panel; a warp's loads of a row are
+// contiguous.  OUT: also write act(x).
+template <typename X, int C, int ACT, bool OUT>
 __global__ void __launch_bounds__(kThreads) ckpt8_pack_kernel(CkptArgs p) {
   grid_dependency_wait();
   grid_dependents_go();
-  const int c = blockIdx.x * kThreads + threadIdx.x;
+  const int c = (blockIdx.x * kThreads + threadIdx.x) * C;
   if (c >= p.N) return;
   const int panels = (p.T + kCkptRun - 1) / kCkptRun;
   for (int panel = blockIdx.y; panel < panels; panel += gridDim.y) {
     const int t0 = panel * kCkptRun;
     const int rows = min(kCkptRun, p.T - t0);
     const X* x = static_cast<const X*>(p.x) + t0 * p.ldx + c;
-    float v[kCkptRun];
+    float v[kCkptRun][C];
+    if (rows == kCkptRun) {
 #pragma unroll
-    for (int i = 0; i < kCkptRun; ++i) v[i] = i < rows ? to_f32(x[i * p.ldx]) : 0.0f;
-    uint32_t top = 0;  // magnitudes compare as integers; above 0x7F800000: NaN
+      for (int i = 0; i < kCkptRun; ++i) load_cols<C>(x + i * p.ldx, v[i]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kCkptRun; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    const uint32_t code = ckpt8_code(top);
-    const float inv = ckpt8_inverse_step(code);
-    uint32_t w[8];
+      for (int i = 0; i < kCkptRun; ++i) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[i] = 0;
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        w[i] |= (static_cast<uint32_t>(ckpt8_round(v[4 * i + b], inv)) & 0xFFu) << (8 * b);
+        for (int j = 0; j < C; ++j) v[i][j] = 0.0f;
+        if (i < rows) load_cols<C>(x + i * p.ldx, v[i]);
+      }
     }
-    uint4* q = reinterpret_cast<uint4*>(p.q) + (static_cast<int64_t>(panel) * 2) * p.N + c;
-    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    q[p.N] = make_uint4(w[4], w[5], w[6], w[7]);
-    p.scales[static_cast<int64_t>(panel) * p.N + c] = static_cast<uint8_t>(code);
-    if (p.out) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      uint32_t top = 0;  // magnitudes compare as integers; above 0x7F800000: NaN
+#pragma unroll
+      for (int i = 0; i < kCkptRun; ++i) top = max(top, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
+      const uint32_t code = ckpt8_code(top);
+      const float inv = ckpt8_inverse_step(code);
+      uint32_t w[8];
+      if (code < 248u) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          w[i] = four_bytes(round_byte(v[4 * i][j], inv), round_byte(v[4 * i + 1][j], inv),
+                            round_byte(v[4 * i + 2][j], inv), round_byte(v[4 * i + 3][j], inv));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          w[i] = four_bytes(ckpt8_round(v[4 * i][j], inv), ckpt8_round(v[4 * i + 1][j], inv),
+                            ckpt8_round(v[4 * i + 2][j], inv), ckpt8_round(v[4 * i + 3][j], inv));
+      }
+      uint4* q = reinterpret_cast<uint4*>(p.q) + (static_cast<int64_t>(panel) * 2) * p.N + c + j;
+      q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      q[p.N] = make_uint4(w[4], w[5], w[6], w[7]);
+      p.scales[static_cast<int64_t>(panel) * p.N + c + j] = static_cast<uint8_t>(code);
+    }
+    if constexpr (OUT) {
       __nv_bfloat16* o = p.out + t0 * p.ld_out + c;
 #pragma unroll
       for (int i = 0; i < kCkptRun; ++i)
-        if (i < rows) o[i * p.ld_out] = __float2bfloat16_rn(act_value(v[i], p.act));
+        if (i < rows) {
+          float a[C];
+#pragma unroll
+          for (int j = 0; j < C; ++j) a[j] = act_value<ACT>(v[i][j]);
+          store_cols<C>(o + i * p.ld_out, a);
+        }
     }
   }
 }
 
-// A column's run of 32 kept values.
-__device__ __forceinline__ void load_run(const uint8_t* q, const uint8_t* scales, int panel, int N,
-                                         int c, float (&v)[kCkptRun]) {
+// A column's run of 32 kept values: words and step.
+struct Run {
+  uint32_t w[8];
+  float step;
+  __device__ __forceinline__ float at(int i) const {
+    return static_cast<float>(static_cast<int8_t>(w[i / 4] >> (8 * (i % 4)))) * step;
+  }
+};
+__device__ __forceinline__ Run load_run(const uint8_t* q, const uint8_t* scales, int panel, int N,
+                                        int c) {
   const uint4* src = reinterpret_cast<const uint4*>(q) + (static_cast<int64_t>(panel) * 2) * N + c;
   const uint4 a = src[0], b = src[N];
-  const float step = ckpt8_step(scales[static_cast<int64_t>(panel) * N + c]);
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < kCkptRun; ++i)
-    v[i] = static_cast<float>(static_cast<int8_t>(w[i / 4] >> (8 * (i % 4)))) * step;
+  return Run{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w},
+             ckpt8_step(scales[static_cast<int64_t>(panel) * N + c])};
 }
 
 template <typename O>
@@ -99,43 +190,60 @@ ckpt8_unpack_kernel(int T, int N, const uint8_t* __restrict__ q,
   if (c >= N) return;
   const int panels = (T + kCkptRun - 1) / kCkptRun;
   for (int panel = blockIdx.y; panel < panels; panel += gridDim.y) {
-    float v[kCkptRun];
-    load_run(q, scales, panel, N, c, v);
+    const Run r = load_run(q, scales, panel, N, c);
     O* o = out + static_cast<int64_t>(panel) * kCkptRun * ld + c;
 #pragma unroll
     for (int i = 0; i < kCkptRun; ++i)
-      if (panel * kCkptRun + i < T) o[i * ld] = from_f32<O>(v[i]);
+      if (panel * kCkptRun + i < T) o[i * ld] = from_f32<O>(r.at(i));
   }
 }
 
 // dz = g * act'(kept z) and the block's column sums of dz (before rounding),
 // to partial[blockIdx.y][N].
-template <typename X>
+template <typename X, int C, int ACT>
 __global__ void __launch_bounds__(kThreads) ckpt8_act_grad_kernel(CkptArgs p, float* partial) {
   grid_dependency_wait();
   grid_dependents_go();
-  const int c = blockIdx.x * kThreads + threadIdx.x;
+  const int c = (blockIdx.x * kThreads + threadIdx.x) * C;
   if (c >= p.N) return;
   const int panels = (p.T + kCkptRun - 1) / kCkptRun;
-  float sum = 0.0f;
+  float sum[C] = {};
   for (int panel = blockIdx.y; panel < panels; panel += gridDim.y) {
     const int t0 = panel * kCkptRun;
     const int rows = min(kCkptRun, p.T - t0);
     const X* x = static_cast<const X*>(p.x) + t0 * p.ldx + c;
-    float g[kCkptRun], v[kCkptRun];
+    float g[kCkptRun][C];
+    if (rows == kCkptRun) {
 #pragma unroll
-    for (int i = 0; i < kCkptRun; ++i) g[i] = i < rows ? to_f32(x[i * p.ldx]) : 0.0f;
-    load_run(p.q, p.scales, panel, p.N, c, v);
+      for (int i = 0; i < kCkptRun; ++i) load_cols<C>(x + i * p.ldx, g[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCkptRun; ++i) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) g[i][j] = 0.0f;
+        if (i < rows) load_cols<C>(x + i * p.ldx, g[i]);
+      }
+    }
+    Run r[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) r[j] = load_run(p.q, p.scales, panel, p.N, c + j);
     __nv_bfloat16* o = p.out + t0 * p.ld_out + c;
 #pragma unroll
     for (int i = 0; i < kCkptRun; ++i)
       if (i < rows) {
-        const float dz = g[i] * act_slope(v[i], p.act);
-        sum += dz;
-        o[i * p.ld_out] = __float2bfloat16_rn(dz);
+        float dz[C];
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          dz[j] = g[i][j] * act_slope<ACT>(r[j].at(i));
+          sum[j] += dz[j];
+        }
+        store_cols<C>(o + i * p.ld_out, dz);
       }
   }
-  if (partial) partial[static_cast<int64_t>(blockIdx.y) * p.N + c] = sum;
+  if (partial) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) partial[static_cast<int64_t>(blockIdx.y) * p.N + c + j] = sum[j];
+  }
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -148,14 +256,14 @@ ckpt8_transposed_kernel(int T, int N, const uint8_t* __restrict__ q,
   if (c >= N) return;
   const int panels = (T + kCkptRun - 1) / kCkptRun;
   for (int panel = blockIdx.y; panel < panels; panel += gridDim.y) {
-    float v[kCkptRun];
-    load_run(q, scales, panel, N, c, v);
+    const Run r = load_run(q, scales, panel, N, c);
     uint4* o = reinterpret_cast<uint4*>(out + c * ld + panel * kCkptRun);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      o[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                        pack_bf16(v[8 * i + 4], v[8 * i + 5]),
-                        pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+      o[i] = make_uint4(pack_bf16(r.at(8 * i), r.at(8 * i + 1)),
+                        pack_bf16(r.at(8 * i + 2), r.at(8 * i + 3)),
+                        pack_bf16(r.at(8 * i + 4), r.at(8 * i + 5)),
+                        pack_bf16(r.at(8 * i + 6), r.at(8 * i + 7)));
   }
 }
 
@@ -166,11 +274,41 @@ dim3 panel_grid(int T, int N) {
 
 }  // namespace
 
+// Two columns a thread when every row starts on a boundary of two elements
+// (8-byte loads of FP32, 4-byte loads and stores of BF16), else one.
+static bool pairs_ok(const CkptArgs& a) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.x), o = reinterpret_cast<uintptr_t>(a.out);
+  return a.N % 2 == 0 && a.ldx % 2 == 0 && x % (a.x_bf16 ? 4 : 8) == 0 &&
+         (a.out == nullptr || (a.ld_out % 2 == 0 && o % 4 == 0));
+}
+static unsigned column_blocks(int N, int columns) {
+  return static_cast<unsigned>((N + kThreads * columns - 1) / (kThreads * columns));
+}
+
+template <typename X, int C>
+static cudaError_t pack(const CkptArgs& a, cudaStream_t st) {
+  const dim3 grid(column_blocks(a.N, C), panel_grid(a.T, a.N).y), block(kThreads);
+  if (a.out == nullptr) return launch_pdl(ckpt8_pack_kernel<X, C, 0, false>, grid, block, 0, st, a);
+  if (a.act == 0) return launch_pdl(ckpt8_pack_kernel<X, C, 0, true>, grid, block, 0, st, a);
+  if (a.act == 1) return launch_pdl(ckpt8_pack_kernel<X, C, 1, true>, grid, block, 0, st, a);
+  return launch_pdl(ckpt8_pack_kernel<X, C, 2, true>, grid, block, 0, st, a);
+}
+
+template <typename X, int C>
+static cudaError_t act_grad(const CkptArgs& a, int slots, float* partial, cudaStream_t st) {
+  const dim3 grid(column_blocks(a.N, C), slots), block(kThreads);
+  if (a.act == 0)
+    return launch_pdl(ckpt8_act_grad_kernel<X, C, 0>, grid, block, 0, st, a, partial);
+  if (a.act == 1)
+    return launch_pdl(ckpt8_act_grad_kernel<X, C, 1>, grid, block, 0, st, a, partial);
+  return launch_pdl(ckpt8_act_grad_kernel<X, C, 2>, grid, block, 0, st, a, partial);
+}
+
 cudaError_t launch_ckpt8_pack(const CkptArgs& a, cudaStream_t stream) {
-  const dim3 grid = panel_grid(a.T, a.N), block(kThreads);
-  const cudaError_t e =
-      a.x_bf16 ? launch_pdl(ckpt8_pack_kernel<__nv_bfloat16>, grid, block, 0, stream, a)
-               : launch_pdl(ckpt8_pack_kernel<float>, grid, block, 0, stream, a);
+  using B = __nv_bfloat16;
+  const bool two = pairs_ok(a);
+  const cudaError_t e = a.x_bf16 ? (two ? pack<B, 2>(a, stream) : pack<B, 1>(a, stream))
+                                 : (two ? pack<float, 2>(a, stream) : pack<float, 1>(a, stream));
   if (e == cudaSuccess) note_launches(1);
   return e;
 }
@@ -189,18 +327,20 @@ cudaError_t launch_ckpt8_unpack(int T, int N, const uint8_t* q, const uint8_t* s
 
 int ckpt8_act_grad_slots(int T, int N, const LayerDevice& dev) {
   const int64_t panels = (T + kCkptRun - 1) / kCkptRun;
-  const int64_t cols = (N + kThreads - 1) / kThreads;
-  int64_t s = (static_cast<int64_t>(dev.sms) * 16 + cols - 1) / cols;
+  const int64_t cols = column_blocks(N, 2);
+  int64_t s = (static_cast<int64_t>(dev.sms) * 8 + cols - 1) / cols;
   if (s > panels) s = panels;
   return static_cast<int>(s < 1 ? 1 : s);
 }
 
 cudaError_t launch_ckpt8_act_grad(const CkptArgs& a, int slots, float* partial,
                                   cudaStream_t stream) {
-  const dim3 grid((a.N + kThreads - 1) / kThreads, slots), block(kThreads);
-  const cudaError_t e =
-      a.x_bf16 ? launch_pdl(ckpt8_act_grad_kernel<__nv_bfloat16>, grid, block, 0, stream, a, partial)
-               : launch_pdl(ckpt8_act_grad_kernel<float>, grid, block, 0, stream, a, partial);
+  using B = __nv_bfloat16;
+  const bool two = pairs_ok(a);
+  const cudaError_t e = a.x_bf16 ? (two ? act_grad<B, 2>(a, slots, partial, stream)
+                                        : act_grad<B, 1>(a, slots, partial, stream))
+                                 : (two ? act_grad<float, 2>(a, slots, partial, stream)
+                                        : act_grad<float, 1>(a, slots, partial, stream));
   if (e == cudaSuccess) note_launches(1);
   return e;
 }
