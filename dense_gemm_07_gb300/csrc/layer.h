@@ -96,6 +96,31 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[N])
   }
 }
 
+// ---- asynchronous copies global -> shared of one thread.  The thread that
+// issues a copy is the one that reads it, after cp_async_wait: no barrier.
+__device__ __forceinline__ uint32_t shared_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes, both addresses on 16 bytes; only the first `bytes` are read, the
+// rest of the 16 are zeros.
+__device__ __forceinline__ void cp_async_16(void* dst, const void* src, uint32_t bytes = 16) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(shared_u32(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(shared_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// At most N of this thread's groups are still on their way.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ---- 4-bit weights (w4.cu)
 constexpr int kW4TileN = 16;    // columns of a packed tile
 constexpr int kW4TileK = 128;   // rows of a packed tile
