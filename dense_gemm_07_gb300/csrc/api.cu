@@ -50,7 +50,8 @@ enum ScratchUse {
   kScratchPack = 2,     // BF16 operands copied to aligned rows
   kScratchSmall = 3,    // BF16 small problems: counters (kept zero) + partial tiles
   kScratchLayer = 4,  // column sums and operand copies of the layer operators
-  kScratchUses = 5
+  kScratchWgrad = 5,  // weight gradients: counters (kept zero) + segments' sums
+  kScratchUses = 6
 };
 struct StreamScratch {
   cudaStream_t stream = nullptr;
@@ -1048,12 +1049,57 @@ gemm_status_t layer_epilogue(const gemm_epilogue_t* e, EpiParams* out) { return 
 
 gemm_status_t layer_from_cuda(cudaError_t e) { return from_cuda(e); }
 
-gemm_status_t layer_gemm_bf16(int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda,
-                              const uint16_t* B, int64_t ldb, float* C, int64_t ldc, float beta,
-                              cudaStream_t stream) {
-  EpiParams epi = epi_identity();
-  epi.beta = beta;
-  return run_bf16(M, N, K, A, lda, B, ldb, C, ldc, stream, epi);
+gemm_status_t layer_ckpt8_wgrad(int64_t T, int64_t K, int64_t N, const uint8_t* q,
+                                const uint8_t* scales, const uint16_t* dY, int64_t ld_dy,
+                                float* dW, int64_t ldw, float beta, cudaStream_t stream) {
+  DeviceState* d = nullptr;
+  gemm_status_t s = device_state(&d);
+  if (s != GEMM_OK) return s;
+  const int max_pairs = ckpt8_wgrad_pairs();
+  if (max_pairs <= 0) return GEMM_ERR_LAUNCH;
+  if ((K + 255) / 256 * ((N + 255) / 256) > kMaxDim) return GEMM_ERR_INVALID_ARG;
+  const PairSchedule ps = ckpt8_wgrad_schedule(T, K, N, max_pairs);
+  // dY is copied to aligned rows when the copy engine cannot read it in place
+  // (as gemm_bf16_f32acc's B).
+  const bool pack = !aligned16(dY) || (ld_dy % 8 != 0 && T > 1);
+  const int64_t ld_op = pack ? round_up(N, 8) : round_up(ld_dy, 8);
+  const uint16_t* y = dY;
+  void* packed = nullptr;
+  bool fresh = false, packed_owned = false;
+  if (pack) {
+    s = call_scratch(d, stream, kScratchPack, round_up(T * ld_op * 2, 256), &packed, &fresh,
+                     &packed_owned);
+    if (s != GEMM_OK) return s;
+    y = static_cast<const uint16_t*>(packed);
+    const PackJob job = {dY, ld_dy, static_cast<uint16_t*>(packed), ld_op, static_cast<int>(T),
+                         static_cast<int>(N)};
+    s = from_cuda(launch_pack_u16(&job, 1, stream));
+  }
+  // Counters first, in an area of fixed size (zero when new; each launch puts
+  // its own back), then the segments' sums.
+  constexpr int64_t kCounterBytes = 64 << 10;
+  void* ws = nullptr;
+  bool owned = false;
+  if (s == GEMM_OK && ps.sk_tiles > 0) {
+    if (ckpt8_wgrad_counters(ps) * 4 > kCounterBytes) s = GEMM_ERR_INTERNAL;
+    if (s == GEMM_OK)
+      s = call_scratch(d, stream, kScratchWgrad, kCounterBytes + ckpt8_wgrad_partial_bytes(ps),
+                       &ws, &fresh, &owned);
+    if (s == GEMM_OK && fresh) s = from_cuda(cudaMemsetAsync(ws, 0, kCounterBytes, stream));
+  }
+  CUtensorMap tmY, tmW;
+  if (s == GEMM_OK) s = make_map(&tmY, y, N, T, ld_op, 64, kCkptStageRows);
+  if (s == GEMM_OK) {
+    const bool tma_w = tma_store_ok(dW, N, ldw) && make_map_c(&tmW, dW, K, N, ldw) == GEMM_OK;
+    s = from_cuda(launch_ckpt8_wgrad(
+        tmY, tma_w ? &tmW : nullptr, ps, static_cast<int>(T), static_cast<int>(K),
+        static_cast<int>(N), q, scales, dW, ldw, beta,
+        ws ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes) : nullptr,
+        static_cast<unsigned int*>(ws), d->status, stream));
+  }
+  if (packed_owned) pool_free(packed, stream);
+  if (owned) pool_free(ws, stream);
+  return s;
 }
 
 }  // namespace g07

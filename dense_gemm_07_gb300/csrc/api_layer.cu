@@ -351,22 +351,8 @@ gemm_status_t gemm_ckpt8_wgrad(int64_t T, int64_t K, int64_t N, const void* q,
     return layer_from_cuda(launch_zero_fill_f32(dW, ldw, static_cast<int>(K),
                                                 static_cast<int>(N), epi, st));
   }
-  // The values kept, transposed to K x ld BF16, then GEMMs over runs of rows
-  // that add up in dW: a tensor-core sum rounds toward zero at every step, so
-  // its error grows with its length, and runs of 512 keep it near FP32's.
-  const int64_t ld = (T + kCkptRun - 1) / kCkptRun * kCkptRun;
-  LayerScratch ws;
-  s = layer_scratch(st, K * ld * 2, &ws);
-  if (s != GEMM_OK) return s;
-  uint16_t* xt = static_cast<uint16_t*>(ws.ptr);
-  s = layer_from_cuda(launch_ckpt8_transposed(static_cast<int>(T), static_cast<int>(K),
-                                              static_cast<const uint8_t*>(q), scales,
-                                              as_bf16(xt), ld, st));
-  for (int64_t t = 0; t < T && s == GEMM_OK; t += 512)
-    s = layer_gemm_bf16(K, N, T - t < 512 ? T - t : 512, xt + t, ld, dY + t * ld_dy, ld_dy, dW,
-                        ldw, t == 0 ? beta : 1.0f, st);
-  layer_scratch_done(ws, st);
-  return s;
+  return layer_ckpt8_wgrad(T, K, N, static_cast<const uint8_t*>(q), scales, dY, ld_dy, dW, ldw,
+                           beta, st);
 }
 
 }  // extern "C"

@@ -246,27 +246,6 @@ __global__ void __launch_bounds__(kThreads) ckpt8_act_grad_kernel(CkptArgs p, fl
   }
 }
 
-__global__ void __launch_bounds__(kThreads)
-ckpt8_transposed_kernel(int T, int N, const uint8_t* __restrict__ q,
-                        const uint8_t* __restrict__ scales, __nv_bfloat16* __restrict__ out,
-                        int64_t ld) {
-  grid_dependency_wait();
-  grid_dependents_go();
-  const int c = blockIdx.x * kThreads + threadIdx.x;
-  if (c >= N) return;
-  const int panels = (T + kCkptRun - 1) / kCkptRun;
-  for (int panel = blockIdx.y; panel < panels; panel += gridDim.y) {
-    const Run r = load_run(q, scales, panel, N, c);
-    uint4* o = reinterpret_cast<uint4*>(out + c * ld + panel * kCkptRun);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = make_uint4(pack_bf16(r.at(8 * i), r.at(8 * i + 1)),
-                        pack_bf16(r.at(8 * i + 2), r.at(8 * i + 3)),
-                        pack_bf16(r.at(8 * i + 4), r.at(8 * i + 5)),
-                        pack_bf16(r.at(8 * i + 6), r.at(8 * i + 7)));
-  }
-}
-
 dim3 panel_grid(int T, int N) {
   const int panels = (T + kCkptRun - 1) / kCkptRun;
   return dim3((N + kThreads - 1) / kThreads, panels < 65535 ? panels : 65535);
@@ -341,14 +320,6 @@ cudaError_t launch_ckpt8_act_grad(const CkptArgs& a, int slots, float* partial,
                                         : act_grad<B, 1>(a, slots, partial, stream))
                                  : (two ? act_grad<float, 2>(a, slots, partial, stream)
                                         : act_grad<float, 1>(a, slots, partial, stream));
-  if (e == cudaSuccess) note_launches(1);
-  return e;
-}
-
-cudaError_t launch_ckpt8_transposed(int T, int N, const uint8_t* q, const uint8_t* scales,
-                                    __nv_bfloat16* out, int64_t ld, cudaStream_t stream) {
-  const cudaError_t e = launch_pdl(ckpt8_transposed_kernel, panel_grid(T, N), dim3(kThreads), 0,
-                                   stream, T, N, q, scales, out, ld);
   if (e == cudaSuccess) note_launches(1);
   return e;
 }

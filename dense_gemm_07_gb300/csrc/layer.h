@@ -5,11 +5,13 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "../../include/gemm07.h"
 #include "epilogue.cuh"
+#include "stream_k.cuh"
 
 namespace g07 {
 
@@ -31,10 +33,10 @@ gemm_status_t layer_scratch(cudaStream_t stream, int64_t bytes, LayerScratch* ou
 void layer_scratch_done(const LayerScratch& s, cudaStream_t stream);
 gemm_status_t layer_epilogue(const gemm_epilogue_t* e, EpiParams* out);
 gemm_status_t layer_from_cuda(cudaError_t e);
-// gemm_bf16_f32acc with C := A * B + beta * C.
-gemm_status_t layer_gemm_bf16(int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_t lda,
-                              const uint16_t* B, int64_t ldb, float* C, int64_t ldc, float beta,
-                              cudaStream_t stream);
+// dW := X^T dY + beta dW with X kept in 8 bits (T > 0, sizes checked).
+gemm_status_t layer_ckpt8_wgrad(int64_t T, int64_t K, int64_t N, const uint8_t* q,
+                                const uint8_t* scales, const uint16_t* dY, int64_t ld_dy,
+                                float* dW, int64_t ldw, float beta, cudaStream_t stream);
 
 // ---- element access shared by the kernels
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -222,8 +224,21 @@ cudaError_t launch_ckpt8_unpack(int T, int N, const uint8_t* q, const uint8_t* s
 int ckpt8_act_grad_slots(int T, int N, const LayerDevice& dev);
 cudaError_t launch_ckpt8_act_grad(const CkptArgs& a, int slots, float* partial,
                                   cudaStream_t stream);
-// The checkpoint's values transposed, N x ld BF16 (exact), zero past T.
-cudaError_t launch_ckpt8_transposed(int T, int N, const uint8_t* q, const uint8_t* scales,
-                                    __nv_bfloat16* out, int64_t ld, cudaStream_t stream);
+
+// ---- weight gradient from an 8-bit checkpoint (ckpt8_wgrad.cu)
+// SM pairs that can be resident at once (0: the kernel cannot run here).
+int ckpt8_wgrad_pairs();
+PairSchedule ckpt8_wgrad_schedule(int64_t T, int64_t K, int64_t N, int max_pairs);
+int64_t ckpt8_wgrad_partial_bytes(const PairSchedule& s);
+int64_t ckpt8_wgrad_counters(const PairSchedule& s);
+constexpr int kCkptStageRows = 128;  // rows of X and dY per stage
+// tmY: dY, box {64, kCkptStageRows}, 128-byte swizzle; tmW: dW as FP32 boxes {32, 32},
+// 128-byte swizzle, or null to store rows; counters: ckpt8_wgrad_counters(s)
+// words, zero before and after; partial: ckpt8_wgrad_partial_bytes(s).
+cudaError_t launch_ckpt8_wgrad(const CUtensorMap& tmY, const CUtensorMap* tmW,
+                               const PairSchedule& s, int T, int K, int N, const uint8_t* q,
+                               const uint8_t* scales, float* dW, int64_t ldw, float beta,
+                               float* partial, unsigned int* counters, unsigned int* status,
+                               cudaStream_t stream);
 
 }  // namespace g07
