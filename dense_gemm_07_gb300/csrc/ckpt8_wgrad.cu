@@ -15,7 +15,7 @@
 // cta_group::2, M = 256, N = 256, K = 16, accumulators of 256 columns, two of
 // them taking turns).  Both operands are staged per 128 rows of X and dY in a
 // ring of 3 stages; CTA r owns rows 128 r .. of the tile (columns of X) and
-// stages 128 columns of dY.  Roles, 512 threads per CTA:
+// stages 128 columns of dY.  Roles, 640 threads per CTA:
 //   warp 0       copies dY boxes by TMA (64 columns x 128 rows, N-major);
 //   warp 1       issues the MMAs (even CTA);
 //   warps 2, 3   of the odd CTA tell the even one that a stage of X is decoded,
@@ -23,13 +23,13 @@
 //                stage and waits for the loads its thread has in flight: done
 //                by the decoding warps it emptied their read-ahead at every
 //                stage, 732 us at 4096 x 4096 x 11008; done by one warp, 520.)
-//   warps 4-7    load X as kept (16 rows of one column are 16 bytes, so a
-//                thread owns a row of X^T and reads its 128 values of a stage as
-//                eight 16-byte loads, one stage ahead), turn them into BF16 and
+//   warps 4-11   load X as kept (16 rows of one column are 16 bytes, so a
+//                thread owns a row of X^T and reads its 64 values of a stage as
+//                four 16-byte loads, one stage ahead), turn them into BF16 and
 //                store them K-major in the swizzle the MMA reads.  Nothing is
 //                written back to memory in 16 bits, and 8 bits of X are read
 //                per 256 columns of dW;
-//   warps 8-15   add each finished accumulator to 128 sums a thread, and write
+//   warps 12-19  add each finished accumulator to 128 sums a thread, and write
 //                the tile.
 // 8 bits to BF16, per two values: a byte permutation sets the bytes under the
 // exponent of 128, two masks split the sign bit off (128 + low 7 bits, and 128
@@ -65,19 +65,21 @@ constexpr int B_BYTES = BK * CTA_N * 2;          // 32 KB
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int CHUNK = 4;                         // stages per sum in tensor memory
 constexpr int TMEM_COLS = 2 * TILE;
-constexpr int THREADS = 512;
+constexpr int THREADS = 640;
+constexpr int DECODE_WARPS = 8;
 constexpr int EPI_WARPS = 8;
 constexpr int BOX_BYTES = 32 * 32 * 4;
 constexpr int EPI_BYTES = EPI_WARPS * BOX_BYTES;
 constexpr int GROUP = 8;
-// Registers per thread of the roles (setmaxnreg): together at most the 512 x
-// 128 that the block is launched with.
-constexpr int kRegsCopy = 56, kRegsDecode = 104, kRegsSum = 176;
-static_assert(128 * kRegsCopy + 128 * kRegsDecode + 256 * kRegsSum <= 512 * 128, "register split");
+// Registers per thread of the roles (setmaxnreg): together at most the 640 x
+// 96 that the block is launched with.
+constexpr int kRegsCopy = 32, kRegsDecode = 56, kRegsSum = 168;
+constexpr int kRegsBlock = 128 * kRegsCopy + 256 * kRegsDecode + 256 * kRegsSum;
+static_assert(kRegsBlock <= THREADS * 96, "register split");
 
 struct alignas(8) Control {
   uint64_t full[STAGES];  // even CTA: dY bytes and decoded X of both CTAs
-  uint64_t decoded[STAGES];  // odd CTA: its 4 decoding warps
+  uint64_t decoded[STAGES];  // odd CTA: its decoding warps
   uint64_t empty[STAGES];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];  // even CTA: 8 warps of both CTAs
@@ -206,8 +208,8 @@ ckpt8_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constan
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&ctl->full[s], 1 + 4 + 1);  // the copying thread; X: 4 warps, the odd CTA
-      mbar_init(&ctl->decoded[s], 4);
+      mbar_init(&ctl->full[s], 1 + DECODE_WARPS + 1);  // dY's copier; X; the odd CTA's X
+      mbar_init(&ctl->decoded[s], DECODE_WARPS);
       mbar_init(&ctl->empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -337,10 +339,11 @@ ckpt8_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constan
         if (!mbar_wait(&ctl->drain, 0u, &never, limit)) give_up(abort, peer_abort, p.status);
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < 4 + DECODE_WARPS) {
     // ------------------------------------------------- X: 8 bits to BF16
     regs_dec<kRegsDecode>();
-    const int m = static_cast<int>(threadIdx.x) - 128;  // row of this CTA's part of the tile
+    const int m = static_cast<int>(threadIdx.x) & 127;  // row of this CTA's part of the tile
+    const int part = (warp - 4) / 4;                     // which 64 of a stage's rows of X
     const int blocks = (p.T + kCkptRun - 1) / kCkptRun * 2;  // 16-row pieces kept
     Ring ring;
     StageWalk sw;
@@ -356,9 +359,10 @@ ckpt8_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constan
       if (!sw.any) return;
       const int row = sw.tc.m * TILE + static_cast<int>(rank) * CTA_M + m;
       if (row >= p.K) return;
-      src = reinterpret_cast<const uint4*>(p.q) + row + static_cast<int64_t>(sw.kb) * 8 * p.K;
-      codes = p.scales + row + static_cast<int64_t>(sw.kb) * 4 * p.K;
-      left = blocks - sw.kb * 8;
+      const int64_t first = sw.kb * 8 + part * 4;
+      src = reinterpret_cast<const uint4*>(p.q) + row + first * p.K;
+      codes = p.scales + row + first / 2 * p.K;
+      left = blocks - static_cast<int>(first);
     };
     auto next = [&]() {
       src += 8 * static_cast<int64_t>(p.K);
@@ -366,8 +370,8 @@ ckpt8_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constan
       left -= 8;
       if (sw.advance(sched, pairs)) place();
     };
-    uint4 v[8];        // 16 values each
-    uint32_t code[4];  // a run's scale byte each
+    uint4 v[4];        // 16 values each
+    uint32_t code[2];  // a run's scale byte each
     auto piece = [&](int i) {
       v[i] = i < left ? __ldg(src + static_cast<int64_t>(i) * p.K) : make_uint4(0u, 0u, 0u, 0u);
     };
@@ -376,28 +380,26 @@ ckpt8_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constan
     };
     place();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) piece(i);
+    for (int i = 0; i < 4; ++i) piece(i);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) scale(i);
+    for (int i = 0; i < 2; ++i) scale(i);
     uint64_t* done = rank == 0 ? ctl->full : ctl->decoded;
     while (sw.any) {
       ok = __all_sync(0xFFFFFFFFu,
                       mbar_wait(&ctl->empty[ring.stage], ring.phase ^ 1u, abort, limit));
       if (!ok) break;
       next();
-      uint8_t* a = smem + ring.stage * STAGE_BYTES + m * 128;
+      uint8_t* a = smem + ring.stage * STAGE_BYTES + part * A_PART_BYTES + m * 128;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         // 16 values to two 16-byte pieces; the next stage's take their place
         const uint32_t st = step_pair(code[i / 2]);
         const uint2 x = values(v[i].x, st), y = values(v[i].y, st);
         const uint2 z = values(v[i].z, st), w = values(v[i].w, st);
         piece(i);
         if (i % 2 == 1) scale(i / 2);
-        uint8_t* part = a + i / 4 * A_PART_BYTES;
-        const int c = 2 * (i % 4);
-        *reinterpret_cast<uint4*>(part + ((c ^ (m & 7)) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
-        *reinterpret_cast<uint4*>(part + (((c + 1) ^ (m & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(a + (((2 * i) ^ (m & 7)) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
+        *reinterpret_cast<uint4*>(a + (((2 * i + 1) ^ (m & 7)) << 4)) =
             make_uint4(z.x, z.y, w.x, w.y);
       }
       fence_proxy_async_smem();
@@ -409,9 +411,9 @@ ckpt8_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constan
   } else {
     // ------------------------------------------------------ sums and output
     regs_inc<kRegsSum>();
-    const int ew = warp - 8;           // 0..7
-    const int quad = warp & 3;         // the tensor-memory lanes of this warp
-    const int half = ew >> 2;          // its 128 columns of the tile
+    const int ew = warp - 4 - DECODE_WARPS;  // 0..7
+    const int quad = warp & 3;               // the tensor-memory lanes of this warp
+    const int half = ew >> 2;                // its 128 columns of the tile
     uint8_t* box = boxes + ew * BOX_BYTES;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) +
                            static_cast<uint32_t>(half * 128);
@@ -582,7 +584,7 @@ int ckpt8_wgrad_pairs() {
   // The role's register shares are drawn from what the block is launched with.
   cudaFuncAttributes fa;
   if (cudaFuncGetAttributes(&fa, ckpt8_wgrad_kernel) != cudaSuccess ||
-      fa.numRegs * THREADS < 128 * kRegsCopy + 128 * kRegsDecode + 256 * kRegsSum)
+      fa.numRegs * THREADS < kRegsBlock)
     return 0;
   if (cudaFuncSetAttribute(ckpt8_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(kSmemBytes)) != cudaSuccess)
