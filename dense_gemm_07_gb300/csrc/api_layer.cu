@@ -93,7 +93,7 @@ gemm_status_t gemm_w4(int64_t M, int64_t N, int64_t K, const uint16_t* A, int64_
                       const gemm_w4_t* W, void* C, int64_t ldc, int32_t c_type,
                       const gemm_epilogue_t* epilogue, void* stream) {
   W4Args a;
-  if (!size_ok(M) || !size_ok(N) || !size_ok(K) || !matrix_ok(M, K, lda) ||
+  if (!size_ok(M) || M > kW4MaxRows || !size_ok(N) || !size_ok(K) || !matrix_ok(M, K, lda) ||
       !matrix_ok(M, N, ldc) || !type_ok(c_type) || !w4_ok(K, N, W))
     return GEMM_ERR_INVALID_ARG;
   gemm_status_t s = layer_epilogue(epilogue, &a.epi);

@@ -127,6 +127,7 @@ __device__ __forceinline__ void cp_async_wait() {
 constexpr int kW4TileN = 16;    // columns of a packed tile
 constexpr int kW4TileK = 128;   // rows of a packed tile
 constexpr int kW4TileBytes = 1024;
+constexpr int kW4MaxRows = 65535 * 8;  // grid rows of 8 rows of A at least
 struct W4Args {
   int M = 0, N = 0, K = 0;
   const __nv_bfloat16* A = nullptr;

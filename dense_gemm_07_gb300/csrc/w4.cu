@@ -17,6 +17,7 @@
 
 #include "kernels.h"
 #include "layer.h"
+#include "sm103_ptx.cuh"
 
 namespace g07 {
 namespace {
@@ -53,7 +54,7 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 
 // Eight consecutive elements of a row of A from k, zero past K.
 __device__ __forceinline__ uint4 load_a8(const __nv_bfloat16* row, int k, int K, bool vec) {
-  if (vec && k + 8 <= K) return *reinterpret_cast<const uint4*>(row + k);
+  if (vec && k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -66,79 +67,147 @@ __device__ __forceinline__ uint4 load_a8(const __nv_bfloat16* row, int k, int K,
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One block: CT tiles of 16 columns by up to 8 * NT rows of A.  Its warps take
-// the 128-row tiles of K in turn and add their sums in warp order.
-template <int CT, int NT>
-__global__ void __launch_bounds__(kThreads) w4_kernel(W4Args p, int vec_a) {
-  __shared__ float red[kWarps][CT * 16][8 * NT + 1];
+// One cluster computes CT tiles of 16 columns by up to 8 * NT rows of A; the
+// 128-row tiles of K go round over the warps of its blocks.  A warp copies the
+// packed tiles of its next steps into a ring in shared memory (cp.async; each
+// lane copies the 16-byte pieces that it decodes, so no barrier is needed), STAGES
+// - 1 steps ahead.  Every step's groups (GPT of them in 128 rows) come as one
+// 32-bit word per column, scale above 128 + z, held by one lane and handed
+// round by shuffles.  The warps' sums are added in warp order, the blocks' in
+// rank order.
+template <int CT, int NT, int GPT, int STAGES>
+__global__ void __launch_bounds__(kThreads, 2) w4_kernel(W4Args p, int vec_a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int RED = 8 * NT + 1;             // row of the sums' exchange
+  constexpr int MREGS = GPT == 4 ? 2 : 1;     // two groups of 16 columns a register
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int KT = (p.K + kW4TileK - 1) / kW4TileK;
   const int NTILES = (p.N + kW4TileN - 1) / kW4TileN;
+  const int G = (p.K + p.group - 1) / p.group;
+  const int blocks = static_cast<int>(gridDim.z), rank = static_cast<int>(blockIdx.z);
   const int nt0 = blockIdx.x * CT;
   const int m0 = blockIdx.y * 8 * NT;
-  const int G = (p.K + p.group - 1) / p.group;
-  const int per = p.group / 32;  // 32-row blocks of a group: 1, 2 or 4
+  const int first = rank * kWarps + warp, step = blocks * kWarps;
   grid_dependency_wait();
   grid_dependents_go();
 
-  float acc[CT][NT][4] = {};
-  for (int kt = warp; kt < KT; kt += kWarps) {
-    uint4 a[NT][4];
+  uint8_t* ring = smem + warp * (STAGES * CT * kW4TileBytes) + lane * 16;
+  const uint8_t* tiles =
+      p.packed + static_cast<int64_t>(nt0) * KT * kW4TileBytes + lane * 16;
+  auto issue = [&](int kt, int s) {
+    if (kt < KT) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+        if (c == 0 || nt0 + c < NTILES) {
+          const uint8_t* src = tiles + (static_cast<int64_t>(c) * KT + kt) * kW4TileBytes;
+          uint8_t* dst = ring + (s * CT + c) * kW4TileBytes;
+          cp_async_16(dst, src);
+          cp_async_16(dst + 512, src + 512);
+        }
+    }
+    cp_async_commit();
+  };
+  // This lane's group word of each tile for step kt: column lane % 16, group
+  // lane / 16 (+ 2).
+  auto load_meta = [&](int kt, uint32_t (&m)[CT][MREGS]) {
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int r = 0; r < MREGS; ++r) {
+        const int grp = kt * GPT + (lane >> 4) + 2 * r;
+        const int n = (nt0 + c) * 16 + (lane & 15);
+        uint32_t v = 0x4308u;
+        if (kt < KT && grp < G && n < p.N && (GPT > 1 || lane < 16)) {
+          const uint32_t z = p.zeros ? p.zeros[grp * p.ld_zeros + n] : 8u;
+          v = 0x4300u | z |
+              (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(
+                   p.scales + grp * p.ld_scales + n))
+               << 16);
+        }
+        m[c][r] = v;
+      }
+  };
+  auto load_a = [&](int kt, uint4 (&a)[NT][4]) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int m = m0 + i * 8 + g;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        a[i][j] = m < p.M ? load_a8(p.A + m * p.lda, kt * 128 + j * 32 + t * 8, p.K, vec_a)
-                          : make_uint4(0u, 0u, 0u, 0u);
+        a[i][j] = m < p.M && kt < KT
+                      ? load_a8(p.A + m * p.lda, kt * 128 + j * 32 + t * 8, p.K, vec_a)
+                      : make_uint4(0u, 0u, 0u, 0u);
     }
+  };
+
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) issue(first + s * step, s);
+  uint32_t meta[CT][MREGS];
+  uint4 a[NT][4];
+  load_meta(first, meta);
+  load_a(first, a);
+
+  float acc[CT][NT][4] = {};
+  int s = 0;
+  for (int kt = first; kt < KT; kt += step) {
+    issue(kt + (STAGES - 1) * step, s == 0 ? STAGES - 1 : s - 1);
+    cp_async_wait<STAGES - 1>();
+    uint32_t mine[CT][MREGS];
+    uint4 x[NT][4];
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int r = 0; r < MREGS; ++r) mine[c][r] = meta[c][r];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[i][j] = a[i][j];
+    load_meta(kt + step, meta);
+    if (NT == 1) load_a(kt + step, a);
+    const uint8_t* st = ring + s * CT * kW4TileBytes;
+    if (++s == STAGES) s = 0;
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
-      if (nt0 + c >= NTILES) break;
-      const uint4* tile = reinterpret_cast<const uint4*>(
-          p.packed + (static_cast<int64_t>(nt0 + c) * KT + kt) * kW4TileBytes);
-      const uint4 h0 = tile[lane], h1 = tile[32 + lane];
+      if (c > 0 && nt0 + c >= NTILES) break;
+      const uint4 h0 = *reinterpret_cast<const uint4*>(st + c * kW4TileBytes);
+      const uint4 h1 = *reinterpret_cast<const uint4*>(st + c * kW4TileBytes + 512);
       const uint32_t w0[4] = {h0.x, h0.y, h0.z, h0.w};
       const uint32_t w1[4] = {h1.x, h1.y, h1.z, h1.w};
-      const int n_lo = min((nt0 + c) * 16 + g, p.N - 1), n_hi = min((nt0 + c) * 16 + 8 + g, p.N - 1);
-      float part[NT][4] = {};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int grp = min((kt * 128 + j * 32) / p.group, G - 1);
-        uint32_t z0 = 8, z1 = 8;
-        if (p.zeros != nullptr) {
-          z0 = p.zeros[grp * p.ld_zeros + n_lo];
-          z1 = p.zeros[grp * p.ld_zeros + n_hi];
-        }
-        z0 = (z0 | (z0 << 16)) | 0x43004300u;  // 128 + z, twice
-        z1 = (z1 | (z1 << 16)) | 0x43004300u;
-        uint32_t v0[4], v1[4];
+      for (int grp = 0; grp < GPT; ++grp) {
+        const uint32_t g0 = __shfl_sync(0xFFFFFFFFu, mine[c][grp / 2], (grp % 2) * 16 + g);
+        const uint32_t g1 = __shfl_sync(0xFFFFFFFFu, mine[c][grp / 2], (grp % 2) * 16 + 8 + g);
+        const uint32_t z0 = __byte_perm(g0, 0, 0x1010), z1 = __byte_perm(g1, 0, 0x1010);
+        float part[NT][4] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v0[i] = sub_bf16x2(decode_pair(w0[j], i), z0);
-          v1[i] = sub_bf16x2(decode_pair(w1[j], i), z1);
-        }
+        for (int j = grp * (4 / GPT); j < (grp + 1) * (4 / GPT); ++j) {
+          uint32_t v0[4], v1[4];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          mma_bf16(part[i], v0[0], v1[0], v0[1], v1[1], a[i][j].x, a[i][j].y);
-          mma_bf16(part[i], v0[2], v1[2], v0[3], v1[3], a[i][j].z, a[i][j].w);
-        }
-        if ((j + 1) % per == 0) {
-          const float s0 = __bfloat162float(p.scales[grp * p.ld_scales + n_lo]);
-          const float s1 = __bfloat162float(p.scales[grp * p.ld_scales + n_hi]);
+          for (int i = 0; i < 4; ++i) {
+            v0[i] = sub_bf16x2(decode_pair(w0[j], i), z0);
+            v1[i] = sub_bf16x2(decode_pair(w1[j], i), z1);
+          }
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
-            acc[c][i][0] = fmaf(s0, part[i][0], acc[c][i][0]);
-            acc[c][i][1] = fmaf(s0, part[i][1], acc[c][i][1]);
-            acc[c][i][2] = fmaf(s1, part[i][2], acc[c][i][2]);
-            acc[c][i][3] = fmaf(s1, part[i][3], acc[c][i][3]);
-            part[i][0] = part[i][1] = part[i][2] = part[i][3] = 0.0f;
+            mma_bf16(part[i], v0[0], v1[0], v0[1], v1[1], x[i][j].x, x[i][j].y);
+            mma_bf16(part[i], v0[2], v1[2], v0[3], v1[3], x[i][j].z, x[i][j].w);
           }
+        }
+        const float s0 = bf16_hi(g0), s1 = bf16_hi(g1);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          acc[c][i][0] = fmaf(s0, part[i][0], acc[c][i][0]);
+          acc[c][i][1] = fmaf(s0, part[i][1], acc[c][i][1]);
+          acc[c][i][2] = fmaf(s1, part[i][2], acc[c][i][2]);
+          acc[c][i][3] = fmaf(s1, part[i][3], acc[c][i][3]);
         }
       }
     }
+    if (NT > 1) load_a(kt + step, a);
   }
+  cp_async_wait<0>();
+  __syncthreads();  // every copy of the block has landed: the ring becomes the exchange
+  float(*red)[CT * 16][RED] = reinterpret_cast<float(*)[CT * 16][RED]>(smem);
 #pragma unroll
   for (int c = 0; c < CT; ++c)
 #pragma unroll
@@ -149,13 +218,30 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(W4Args p, int vec_a) {
       red[warp][c * 16 + 8 + g][i * 8 + 2 * t + 1] = acc[c][i][3];
     }
   __syncthreads();
-  for (int i = threadIdx.x; i < CT * 16 * 8 * NT; i += kThreads) {
+  constexpr int OUT = CT * 16 * 8 * NT;
+  if (blocks > 1) {
+    // this block's sums, in its first warp's place, then all blocks' by rank
+    for (int i = threadIdx.x; i < OUT; i += kThreads) {
+      const int col = i % (CT * 16), row = i / (CT * 16);
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v += red[w][col][row];
+      red[0][col][row] = v;
+    }
+    cluster_sync();
+  }
+  for (int i = threadIdx.x + rank * kThreads; i < OUT; i += kThreads * blocks) {
     const int col = i % (CT * 16), row = i / (CT * 16);
     const int n = nt0 * 16 + col, m = m0 + row;
     if (n >= p.N || m >= p.M) continue;
     float v = 0.0f;
+    if (blocks > 1) {
+      const uint32_t at = smem_u32(&red[0][col][row]);
+      for (int r = 0; r < blocks; ++r) v += ld_cluster_f32(map_to_rank(at, r));
+    } else {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += red[w][col][row];
+      for (int w = 0; w < kWarps; ++w) v += red[w][col][row];
+    }
     const float bias = p.epi.bias != nullptr ? p.epi.bias[n] : 0.0f;
     if (p.c_bf16) {
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.C) + m * p.ldc + n;
@@ -166,6 +252,7 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(W4Args p, int vec_a) {
       *o = epi_apply(p.epi, v, p.epi.beta != 0.0f ? *o : 0.0f, bias);
     }
   }
+  if (blocks > 1) cluster_sync();  // no block leaves while others read its sums
 }
 
 // Position of code (k, n) in the packed matrix: word index and shift.
@@ -280,21 +367,68 @@ int blocks_for(int64_t total, int threads) {
   return static_cast<int>(b < 8192 ? (b > 0 ? b : 1) : 8192);
 }
 
+template <int CT, int NT, int GPT>
+cudaError_t launch_tile(const W4Args& a, bool vec_a, int blocks, cudaStream_t stream) {
+  constexpr int STAGES = CT == 4 ? 3 : 4;
+  constexpr size_t kRing = static_cast<size_t>(kWarps) * STAGES * CT * kW4TileBytes;
+  constexpr size_t kExchange = sizeof(float) * kWarps * CT * 16 * (8 * NT + 1);
+  constexpr size_t kSmem = kRing > kExchange ? kRing : kExchange;
+  const auto kernel = w4_kernel<CT, NT, GPT, STAGES>;
+  if (kSmem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    if (e != cudaSuccess) return e;
+  }
+  const int ntiles = (a.N + kW4TileN - 1) / kW4TileN;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0] = pdl_attribute();
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = static_cast<unsigned>(blocks);
+  cfg.gridDim = dim3(static_cast<unsigned>((ntiles + CT - 1) / CT),
+                     static_cast<unsigned>((a.M + 8 * NT - 1) / (8 * NT)),
+                     static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = blocks > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, vec_a ? 1 : 0);
+}
+
 template <int CT, int NT>
-cudaError_t launch_tile(const W4Args& a, bool vec_a, cudaStream_t stream) {
-  const int64_t ntiles = (a.N + kW4TileN - 1) / kW4TileN;
-  const dim3 grid(static_cast<unsigned>((ntiles + CT - 1) / CT),
-                  static_cast<unsigned>((a.M + 8 * NT - 1) / (8 * NT)));
-  return launch_pdl(w4_kernel<CT, NT>, grid, dim3(kThreads), 0, stream, a, vec_a ? 1 : 0);
+cudaError_t launch_groups(const W4Args& a, bool vec_a, int blocks, cudaStream_t stream) {
+  if (a.group == 128) return launch_tile<CT, NT, 1>(a, vec_a, blocks, stream);
+  if (a.group == 64) return launch_tile<CT, NT, 2>(a, vec_a, blocks, stream);
+  return launch_tile<CT, NT, 4>(a, vec_a, blocks, stream);
+}
+
+template <int NT>
+cudaError_t launch_columns(int ct, const W4Args& a, bool vec_a, int blocks, cudaStream_t stream) {
+  if (ct == 4) return launch_groups<4, NT>(a, vec_a, blocks, stream);
+  if (ct == 2) return launch_groups<2, NT>(a, vec_a, blocks, stream);
+  return launch_groups<1, NT>(a, vec_a, blocks, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_w4(const W4Args& a, const LayerDevice& dev, cudaStream_t stream) {
-  (void)dev;
   const bool vec_a = (reinterpret_cast<uintptr_t>(a.A) & 15u) == 0 && (a.lda % 8 == 0 || a.M == 1);
-  const cudaError_t e = a.M <= 8 ? launch_tile<1, 1>(a, vec_a, stream)
-                                 : launch_tile<1, 2>(a, vec_a, stream);
+  const int ntiles = (a.N + kW4TileN - 1) / kW4TileN, kts = (a.K + kW4TileK - 1) / kW4TileK;
+  // A is read once per CT tiles of columns: wide where that would be more than
+  // the weights (M of 3 and up), as long as every SM still gets a block.
+  int ct = a.M > 4 ? 4 : a.M > 2 ? 2 : 1;
+  while (ct > 1 && ntiles < ct * dev.sms) ct /= 2;
+  // Few columns: K is shared by the blocks of a cluster too, at least two
+  // steps to a warp.
+  int blocks = 1;
+  while (blocks < 8 && (ntiles + ct - 1) / ct * blocks * 2 <= 2 * dev.sms &&
+         kts >= 4 * kWarps * blocks)
+    blocks *= 2;
+  const cudaError_t e = a.M <= 8 ? launch_columns<1>(ct, a, vec_a, blocks, stream)
+                                 : launch_columns<2>(ct, a, vec_a, blocks, stream);
   if (e == cudaSuccess) note_launches(1);
   return e;
 }

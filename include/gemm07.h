@@ -475,7 +475,7 @@ GEMM07_API int64_t gemm_w4_packed_bytes(int64_t K, int64_t N);
  *   every 16 rows of A.  For a prompt, write W out once with gemm_w4_unpack
  *   and use gemm_bf16_f32acc.
  *   Arithmetic: q - z times A exactly, summed in FP32 over a group, times the
- *   group's scale in FP32; C is rounded once.
+ *   group's scale in FP32; C is rounded once.  M is at most 524280.
  *   Any alignment of A and C is accepted; A on 16 bytes with lda a multiple of
  *   8 is read 16 bytes at a time.
  */

@@ -37,7 +37,7 @@ def test_sizes():
 
 
 @pytest.mark.parametrize("change", [
-    dict(M=-1), dict(N=2 ** 31), dict(K=-5), dict(lda=127), dict(ldc=63), dict(A=None),
+    dict(M=-1), dict(M=524281), dict(N=2 ** 31), dict(K=-5), dict(lda=127), dict(ldc=63), dict(A=None),
     dict(C=None), dict(c_type=2), dict(w=None), dict(w=_w4(group=96)), dict(w=_w4(packed=None)),
     dict(w=_w4(packed=P + 8)), dict(w=_w4(scales=None)), dict(w=_w4(ld_scales=63)),
     dict(w=_w4(zeros=P, ld_zeros=1)), dict(epi=_abi.GemmEpilogue(1.0, 0.0, None, 9)),
