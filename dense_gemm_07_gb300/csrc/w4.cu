@@ -35,14 +35,28 @@ __host__ __device__ __forceinline__ int nibble_shift(int e) { return 4 * (e / 2 
 
 // The codes at pair i of a word, as two BF16 whole numbers 128 + q: the bits
 // 0x4300 | q are exactly 128 + q.
+// One three-input logic operation for both (written as & and | it became two).
 __device__ __forceinline__ uint32_t decode_pair(uint32_t w, int i) {
-  return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;"  // (a & b) | c
+      : "=r"(d)
+      : "r"(w >> (4 * i)), "r"(0x000F000Fu), "r"(0x43004300u));
+  return d;
 }
 // Exact: both operands are whole numbers of at most 8 bits.
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
+}
+// The same with a sum that starts here.
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1,
+                                               uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -52,148 +66,144 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Eight consecutive elements of a row of A from k, zero past K.
-__device__ __forceinline__ uint4 load_a8(const __nv_bfloat16* row, int k, int K, bool vec) {
-  if (vec && k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
-  uint32_t w[4];
+// ---------------------------------------------------- one warp's share of W
+//
+// Per step a warp takes CT packed tiles (16 columns each) of one 128-row block
+// of K with their GPT = 128 / group groups.  Both come through a ring in shared
+// memory by asynchronous copies: a lane copies the 16-byte pieces of the tiles
+// that it decodes itself, and pieces of the groups' scales and zero points,
+// whose rows start anywhere: the 16-byte granules that hold a tile's 16 scales
+// (3 at most) and 16 zero points (2) are copied and read from an offset.
+constexpr int kMetaBytes = 80;    // a group's granules: 48 of scales, 32 of zero points
+constexpr int kMetaPieces = 5;
+
+template <int CT, int GPT>
+struct WarpWeights {
+  static constexpr int kStageBytes = CT * (kW4TileBytes + GPT * kMetaBytes);
+  static constexpr int kMetaJobs = (CT * GPT * kMetaPieces + 31) / 32;
+
+  const int lane, tiles, KT, G;
+  const bool zeros;
+  const uint8_t* src;     // this lane's piece of tile (nt0, 0)
+  int64_t tile_stride;    // from a tile to the next 16 columns
+  // What a step costs besides its weights is kept small by working out here
+  // what does not change from step to step.  Jobs: the granules that this lane
+  // copies (job i * 32 + lane; row 0 of its array, bytes from row to row).
+  uintptr_t row0[kMetaJobs];
+  int64_t row_bytes[kMetaJobs];
+  int job_grp[kMetaJobs];   // group of the step, or past all groups: no job
+  int job_to[kMetaJobs];    // offset in the stage
+  int job_skip[kMetaJobs];  // granules between the row's first and the job's
+  int job_len[kMetaJobs];   // bytes wanted from the row
+  // Low address bits of the arrays' first rows: where in its granules a row
+  // starts (tiles are 32 and 16 bytes apart, so all of them start alike).
+  uint32_t scale_low, zero_low, scale_row, zero_row;
+
+  __device__ __forceinline__ WarpWeights(const W4Args& p, int nt0)
+      : lane(threadIdx.x & 31), tiles((p.N + kW4TileN - 1) / kW4TileN - nt0),
+        KT((p.K + kW4TileK - 1) / kW4TileK), G((p.K + p.group - 1) / p.group),
+        zeros(p.zeros != nullptr),
+        src(p.packed + static_cast<int64_t>(nt0) * KT * kW4TileBytes + lane * 16),
+        tile_stride(static_cast<int64_t>(KT) * kW4TileBytes) {
+    const uintptr_t scale0 = reinterpret_cast<uintptr_t>(p.scales + nt0 * kW4TileN);
+    const uintptr_t zero0 = reinterpret_cast<uintptr_t>(p.zeros + nt0 * kW4TileN);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo =
-        k + 2 * i < K ? *reinterpret_cast<const uint16_t*>(row + k + 2 * i) : 0u;
-    const uint32_t hi =
-        k + 2 * i + 1 < K ? *reinterpret_cast<const uint16_t*>(row + k + 2 * i + 1) : 0u;
-    w[i] = lo | (hi << 16);
+    for (int i = 0; i < kMetaJobs; ++i) {
+      const int job = i * 32 + lane, cg = job / kMetaPieces, piece = job % kMetaPieces;
+      const int c = cg / GPT;
+      const bool scale = piece < 3;
+      const int cols = min(kW4TileN, p.N - (nt0 + c) * kW4TileN);
+      const bool live = cg < CT * GPT && c < tiles && (scale || zeros);
+      row0[i] = scale ? scale0 + c * 32 : zero0 + c * 16;
+      row_bytes[i] = scale ? p.ld_scales * 2 : p.ld_zeros;
+      job_grp[i] = live ? cg % GPT : 0x40000000;
+      job_to[i] = CT * kW4TileBytes + cg * kMetaBytes + piece * 16;
+      job_skip[i] = (scale ? piece : piece - 3) * 16;
+      job_len[i] = scale ? cols * 2 : cols;
+    }
+    scale_row = static_cast<uint32_t>(p.ld_scales * 2);
+    zero_row = static_cast<uint32_t>(p.ld_zeros);
+    scale_low = static_cast<uint32_t>(scale0);
+    zero_low = static_cast<uint32_t>(zero0);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
-// One cluster computes CT tiles of 16 columns by up to 8 * NT rows of A; the
-// 128-row tiles of K go round over the warps of its blocks.  A warp copies the
-// packed tiles of its next steps into a ring in shared memory (cp.async; each
-// lane copies the 16-byte pieces that it decodes, so no barrier is needed), STAGES
-// - 1 steps ahead.  Every step's groups (GPT of them in 128 rows) come as one
-// 32-bit word per column, scale above 128 + z, held by one lane and handed
-// round by shuffles.  The warps' sums are added in warp order, the blocks' in
-// rank order.
-template <int CT, int NT, int GPT, int STAGES>
-__global__ void __launch_bounds__(kThreads, 2) w4_kernel(W4Args p, int vec_a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int RED = 8 * NT + 1;             // row of the sums' exchange
-  constexpr int MREGS = GPT == 4 ? 2 : 1;     // two groups of 16 columns a register
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const int KT = (p.K + kW4TileK - 1) / kW4TileK;
-  const int NTILES = (p.N + kW4TileN - 1) / kW4TileN;
-  const int G = (p.K + p.group - 1) / p.group;
-  const int blocks = static_cast<int>(gridDim.z), rank = static_cast<int>(blockIdx.z);
-  const int nt0 = blockIdx.x * CT;
-  const int m0 = blockIdx.y * 8 * NT;
-  const int first = rank * kWarps + warp, step = blocks * kWarps;
-  grid_dependency_wait();
-  grid_dependents_go();
+  // Zeroes the group words of this warp's stages: a group past the matrix is
+  // then multiplied by 0 or by an earlier group's scale of the column, never by
+  // what shared memory held before (its products are 0: A is 0 past K).
+  __device__ __forceinline__ void clear(uint8_t* ring, int stages, int stage_bytes) const {
+    for (int s = 0; s < stages; ++s)
+      for (int i = lane; i < CT * GPT * kMetaBytes / 16; i += 32)
+        *reinterpret_cast<uint4*>(ring + s * stage_bytes + CT * kW4TileBytes + i * 16) =
+            make_uint4(0u, 0u, 0u, 0u);
+    __syncwarp();
+  }
 
-  uint8_t* ring = smem + warp * (STAGES * CT * kW4TileBytes) + lane * 16;
-  const uint8_t* tiles =
-      p.packed + static_cast<int64_t>(nt0) * KT * kW4TileBytes + lane * 16;
-  auto issue = [&](int kt, int s) {
-    if (kt < KT) {
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-        if (c == 0 || nt0 + c < NTILES) {
-          const uint8_t* src = tiles + (static_cast<int64_t>(c) * KT + kt) * kW4TileBytes;
-          uint8_t* dst = ring + (s * CT + c) * kW4TileBytes;
-          cp_async_16(dst, src);
-          cp_async_16(dst + 512, src + 512);
-        }
-    }
-    cp_async_commit();
-  };
-  // This lane's group word of each tile for step kt: column lane % 16, group
-  // lane / 16 (+ 2).
-  auto load_meta = [&](int kt, uint32_t (&m)[CT][MREGS]) {
+  // Starts the copies of step kt into a stage; the caller commits.
+  __device__ __forceinline__ void copy(uint8_t* stage, int kt) const {
+    const uint8_t* from = src + static_cast<int64_t>(kt) * kW4TileBytes;
+    uint8_t* to = stage + lane * 16;
 #pragma unroll
     for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int r = 0; r < MREGS; ++r) {
-        const int grp = kt * GPT + (lane >> 4) + 2 * r;
-        const int n = (nt0 + c) * 16 + (lane & 15);
-        uint32_t v = 0x4308u;
-        if (kt < KT && grp < G && n < p.N && (GPT > 1 || lane < 16)) {
-          const uint32_t z = p.zeros ? p.zeros[grp * p.ld_zeros + n] : 8u;
-          v = 0x4300u | z |
-              (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(
-                   p.scales + grp * p.ld_scales + n))
-               << 16);
-        }
-        m[c][r] = v;
+      if (c < tiles) {
+        cp_async_16(to + c * kW4TileBytes, from + c * tile_stride);
+        cp_async_16(to + c * kW4TileBytes + 512, from + c * tile_stride + 512);
       }
-  };
-  auto load_a = [&](int kt, uint4 (&a)[NT][4]) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int m = m0 + i * 8 + g;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        a[i][j] = m < p.M && kt < KT
-                      ? load_a8(p.A + m * p.lda, kt * 128 + j * 32 + t * 8, p.K, vec_a)
-                      : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < kMetaJobs; ++i) {
+      const int grp = kt * GPT + job_grp[i];
+      const uintptr_t at = row0[i] + grp * row_bytes[i];
+      const int skip = job_skip[i] - static_cast<int>(at & 15u);
+      if (grp < G && skip < job_len[i])
+        cp_async_16(stage + job_to[i], reinterpret_cast<const void*>(at + skip));
     }
-  };
+  }
 
+  // Adds the step's products to acc: x holds this lane's pieces of A (row 8 i +
+  // lane / 4, 8 values of each 32-row block).
+  template <int NT>
+  __device__ __forceinline__ void multiply(const uint8_t* stage, int kt, const uint4 (&x)[NT][4],
+                                           float (&acc)[CT][NT][4]) const {
+    // Tiles past the matrix are decoded too, from whatever the stage holds: their
+    // sums are never written, and without a branch the tiles' work interleaves.
+    const uint8_t* words = stage + CT * kW4TileBytes + (lane >> 2) * 2;
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) issue(first + s * step, s);
-  uint32_t meta[CT][MREGS];
-  uint4 a[NT][4];
-  load_meta(first, meta);
-  load_a(first, a);
-
-  float acc[CT][NT][4] = {};
-  int s = 0;
-  for (int kt = first; kt < KT; kt += step) {
-    issue(kt + (STAGES - 1) * step, s == 0 ? STAGES - 1 : s - 1);
-    cp_async_wait<STAGES - 1>();
-    uint32_t mine[CT][MREGS];
-    uint4 x[NT][4];
+    for (int grp = 0; grp < GPT; ++grp) {
+      const uint32_t row = kt * GPT + grp;
+      const uint32_t s_off = (scale_low + row * scale_row) & 15u;
+      const uint32_t z_off = 48 + ((zero_low + row * zero_row) & 15u);
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
+      for (int c = 0; c < CT; ++c) {
+        // scales and zero points of columns lane / 4 and 8 + lane / 4
+        const uint8_t* m = words + (c * GPT + grp) * kMetaBytes;
+        const uint16_t* sc = reinterpret_cast<const uint16_t*>(m + s_off);
+        const float s0 = __uint_as_float(sc[0] * 65536u), s1 = __uint_as_float(sc[8] * 65536u);
+        uint32_t z0 = 0x43084308u, z1 = 0x43084308u;  // 128 + z, twice
+        if (zeros) {
+          const uint8_t* zp = m + z_off - (lane >> 2);
+          z0 = zp[0] * 0x00010001u + 0x43004300u;
+          z1 = zp[8] * 0x00010001u + 0x43004300u;
+        }
+        const uint8_t* tile = stage + c * kW4TileBytes + lane * 16;
+        float part[NT][4];
 #pragma unroll
-      for (int r = 0; r < MREGS; ++r) mine[c][r] = meta[c][r];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[i][j] = a[i][j];
-    load_meta(kt + step, meta);
-    if (NT == 1) load_a(kt + step, a);
-    const uint8_t* st = ring + s * CT * kW4TileBytes;
-    if (++s == STAGES) s = 0;
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      if (c > 0 && nt0 + c >= NTILES) break;
-      const uint4 h0 = *reinterpret_cast<const uint4*>(st + c * kW4TileBytes);
-      const uint4 h1 = *reinterpret_cast<const uint4*>(st + c * kW4TileBytes + 512);
-      const uint32_t w0[4] = {h0.x, h0.y, h0.z, h0.w};
-      const uint32_t w1[4] = {h1.x, h1.y, h1.z, h1.w};
-#pragma unroll
-      for (int grp = 0; grp < GPT; ++grp) {
-        const uint32_t g0 = __shfl_sync(0xFFFFFFFFu, mine[c][grp / 2], (grp % 2) * 16 + g);
-        const uint32_t g1 = __shfl_sync(0xFFFFFFFFu, mine[c][grp / 2], (grp % 2) * 16 + 8 + g);
-        const uint32_t z0 = __byte_perm(g0, 0, 0x1010), z1 = __byte_perm(g1, 0, 0x1010);
-        float part[NT][4] = {};
-#pragma unroll
-        for (int j = grp * (4 / GPT); j < (grp + 1) * (4 / GPT); ++j) {
+        for (int jj = 0; jj < 4 / GPT; ++jj) {
+          const int j = grp * (4 / GPT) + jj;
+          const uint32_t w0 = word(tile, j), w1 = word(tile + 512, j);
           uint32_t v0[4], v1[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            v0[i] = sub_bf16x2(decode_pair(w0[j], i), z0);
-            v1[i] = sub_bf16x2(decode_pair(w1[j], i), z1);
+            v0[i] = sub_bf16x2(decode_pair(w0, i), z0);
+            v1[i] = sub_bf16x2(decode_pair(w1, i), z1);
           }
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
-            mma_bf16(part[i], v0[0], v1[0], v0[1], v1[1], x[i][j].x, x[i][j].y);
+            if (jj == 0)
+              mma_bf16_first(part[i], v0[0], v1[0], v0[1], v1[1], x[i][j].x, x[i][j].y);
+            else
+              mma_bf16(part[i], v0[0], v1[0], v0[1], v1[1], x[i][j].x, x[i][j].y);
             mma_bf16(part[i], v0[2], v1[2], v0[3], v1[3], x[i][j].z, x[i][j].w);
           }
         }
-        const float s0 = bf16_hi(g0), s1 = bf16_hi(g1);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           acc[c][i][0] = fmaf(s0, part[i][0], acc[c][i][0]);
@@ -203,56 +213,255 @@ __global__ void __launch_bounds__(kThreads, 2) w4_kernel(W4Args p, int vec_a) {
         }
       }
     }
-    if (NT > 1) load_a(kt + step, a);
+  }
+
+  // Word j of this lane's 16-byte piece (the four of a piece are one load).
+  static __device__ __forceinline__ uint32_t word(const uint8_t* piece, int j) {
+    const uint4 v = *reinterpret_cast<const uint4*>(piece);
+    return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+  }
+};
+
+// Elements k .. k + 7 of a row of A into 16 bytes of shared memory, zeros past
+// K; a row off the 16-byte grid goes element by element.
+__device__ __forceinline__ void copy_a8(uint8_t* to, const __nv_bfloat16* row, int k, int K,
+                                        bool vec) {
+  if (vec) {
+    const int n = K - k;
+    cp_async_16(to, n > 0 ? row + k : row, n >= 8 ? 16u : n > 0 ? 2u * n : 0u);
+    return;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo =
+        k + 2 * i < K ? *reinterpret_cast<const uint16_t*>(row + k + 2 * i) : 0u;
+    const uint32_t hi =
+        k + 2 * i + 1 < K ? *reinterpret_cast<const uint16_t*>(row + k + 2 * i + 1) : 0u;
+    w[i] = lo | (hi << 16);
+  }
+  *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void write_c(const W4Args& p, int m, int n, float v) {
+  const float bias = p.epi.bias != nullptr ? p.epi.bias[n] : 0.0f;
+  if (p.c_bf16) {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.C) + m * p.ldc + n;
+    *o = __float2bfloat16_rn(
+        epi_apply(p.epi, v, p.epi.beta != 0.0f ? __bfloat162float(*o) : 0.0f, bias));
+  } else {
+    float* o = static_cast<float*>(p.C) + m * p.ldc + n;
+    *o = epi_apply(p.epi, v, p.epi.beta != 0.0f ? *o : 0.0f, bias);
+  }
+}
+
+// The sums at red[0], one per output of the block (OUT of them at `at(i)`), added
+// over the cluster's blocks by rank, each block writing its share.
+template <typename At, typename Put>
+__device__ __forceinline__ void finish(int outs, int rank, int blocks, At at, Put put) {
+  if (blocks > 1) cluster_sync();
+  for (int i = threadIdx.x + rank * kThreads; i < outs; i += kThreads * blocks) {
+    const float* here = at(i);
+    float v = *here;
+    if (blocks > 1) {
+      v = 0.0f;
+      for (int r = 0; r < blocks; ++r) v += ld_cluster_f32(map_to_rank(smem_u32(here), r));
+    }
+    put(i, v);
+  }
+  if (blocks > 1) cluster_sync();  // no block leaves while others read its sums
+}
+
+// ------------------------------------------- few rows: K goes over the warps
+//
+// Up to 8 rows of A; a cluster takes CT tiles of columns, the 128-row blocks of
+// K go round over the warps of its blocks.  A's pieces come through the ring
+// like the weights.  The warps' sums are added in warp order.
+template <int CT, int GPT, int STAGES>
+__global__ void __launch_bounds__(kThreads, 2) w4_rows_kernel(W4Args p, int vec_a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  using Weights = WarpWeights<CT, GPT>;
+  constexpr int RED = 9;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int blocks = static_cast<int>(gridDim.z), rank = static_cast<int>(blockIdx.z);
+  const int nt0 = blockIdx.x * CT, m0 = blockIdx.y * 8;
+  const int rows = min(8, p.M - m0);
+  const int first = rank * kWarps + warp, step = blocks * kWarps;
+  const int stage_bytes = Weights::kStageBytes + rows * 256;
+  uint8_t* ring = smem + warp * STAGES * stage_bytes;
+  const bool mine = g < rows;
+  const Weights w(p, nt0);
+  w.clear(ring, STAGES, stage_bytes);
+  const __nv_bfloat16* a_row = p.A + (m0 + (mine ? g : 0)) * p.lda;
+  const int whole = p.K / kW4TileK;  // blocks of K that end inside the row
+  grid_dependency_wait();
+  grid_dependents_go();
+
+  auto issue = [&](int kt, int s) {
+    if (kt < w.KT) {
+      uint8_t* stage = ring + s * stage_bytes;
+      w.copy(stage, kt);
+      if (mine) {
+        uint8_t* to = stage + Weights::kStageBytes + g * 256 + t * 16;
+        const int k = kt * 128 + t * 8;
+        if (vec_a && kt < whole) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) cp_async_16(to + j * 64, a_row + k + j * 32);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) copy_a8(to + j * 64, a_row, k + j * 32, p.K, vec_a);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) issue(first + s * step, s);
+  float acc[CT][1][4] = {};
+  int s = 0;
+  for (int kt = first; kt < w.KT; kt += step) {
+    __syncwarp();  // every lane has read the stage that is filled next
+    issue(kt + (STAGES - 1) * step, s == 0 ? STAGES - 1 : s - 1);
+    cp_async_wait<STAGES - 1>();
+    __syncwarp();  // the group words were copied by other lanes
+    const uint8_t* stage = ring + s * stage_bytes;
+    if (++s == STAGES) s = 0;
+    uint4 x[1][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      x[0][j] = mine ? *reinterpret_cast<const uint4*>(stage + Weights::kStageBytes + g * 256 +
+                                                       j * 64 + t * 16)
+                     : make_uint4(0u, 0u, 0u, 0u);
+    w.multiply(stage, kt, x, acc);
   }
   cp_async_wait<0>();
   __syncthreads();  // every copy of the block has landed: the ring becomes the exchange
   float(*red)[CT * 16][RED] = reinterpret_cast<float(*)[CT * 16][RED]>(smem);
 #pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    red[warp][c * 16 + g][2 * t] = acc[c][0][0];
+    red[warp][c * 16 + g][2 * t + 1] = acc[c][0][1];
+    red[warp][c * 16 + 8 + g][2 * t] = acc[c][0][2];
+    red[warp][c * 16 + 8 + g][2 * t + 1] = acc[c][0][3];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < CT * 16 * rows; i += kThreads) {
+    const int col = i % (CT * 16), row = i / (CT * 16);
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) v += red[k][col][row];
+    red[0][col][row] = v;
+  }
+  // (a thread's share below is what it has just added when there is one block)
+  finish(CT * 16 * rows, rank, blocks,
+         [&](int i) { return &red[0][i % (CT * 16)][i / (CT * 16)]; },
+         [&](int i, float v) {
+           const int n = nt0 * 16 + i % (CT * 16);
+           if (n < p.N) write_c(p, m0 + i / (CT * 16), n, v);
+         });
+}
+
+// -------------------------------------- more rows: columns go over the warps
+//
+// Up to 8 * NT rows of A; each warp takes CT tiles of columns of its own and
+// all of the block's share of K (K is cut over a cluster's blocks when there are
+// few columns).  A is staged for the whole block, kPhase steps at a time in two
+// buffers, so it is read once per 128 CT columns.
+constexpr int kPhase = 4;
+constexpr int kPhaseRow = kPhase * 256 + 64;  // bytes of a staged row: 64 off a multiple of 128,
+                                              // so 8 lanes of two rows read all banks once
+
+template <int CT, int NT, int GPT, int STAGES>
+__global__ void __launch_bounds__(kThreads, 2) w4_columns_kernel(W4Args p, int vec_a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  using Weights = WarpWeights<CT, GPT>;
+  static_assert(STAGES <= kPhase + 1, "a phase of A lands before its first step");
+  constexpr int ROWS = 8 * NT;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int blocks = static_cast<int>(gridDim.z), rank = static_cast<int>(blockIdx.z);
+  const int nt0 = (blockIdx.x * kWarps + warp) * CT, m0 = blockIdx.y * ROWS;
+  const int rows = min(ROWS, p.M - m0);
+  const Weights w(p, nt0);
+  const int k0 = static_cast<int>(static_cast<int64_t>(w.KT) * rank / blocks);
+  const int k1 = static_cast<int>(static_cast<int64_t>(w.KT) * (rank + 1) / blocks);
+  uint8_t* staged = smem;  // [2][ROWS][kPhaseRow]
+  uint8_t* ring = smem + 2 * ROWS * kPhaseRow + warp * STAGES * Weights::kStageBytes;
+  w.clear(ring, STAGES, Weights::kStageBytes);
+  // rows that A does not have stay zero in both buffers
+  for (int i = threadIdx.x; i < 2 * (ROWS - rows) * (kPhaseRow / 16); i += kThreads) {
+    const int per = (ROWS - rows) * (kPhaseRow / 16);
+    const int b = i / per, at = i % per;
+    *reinterpret_cast<uint4*>(staged + (b * ROWS + rows) * kPhaseRow + at * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+  grid_dependency_wait();
+  grid_dependents_go();
+
+  auto stage_a = [&](int kt, int b) {  // steps kt .. kt + kPhase - 1
+    if (kt >= k1) return;
+    for (int i = threadIdx.x; i < rows * kPhase * 16; i += kThreads) {
+      const int row = i / (kPhase * 16), piece = i % (kPhase * 16);
+      copy_a8(staged + (b * ROWS + row) * kPhaseRow + piece * 16, p.A + (m0 + row) * p.lda,
+              kt * 128 + piece * 8, p.K, vec_a);
+    }
+  };
+  auto issue = [&](int kt, int s) {
+    if (kt < k1) w.copy(ring + s * Weights::kStageBytes, kt);
+    cp_async_commit();
+  };
+  stage_a(k0, 0);  // in the first group
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) issue(k0 + s, s);
+  float acc[CT][NT][4] = {};
+  int s = 0;
+  for (int kt = k0; kt < k1; ++kt) {
+    const int i = kt - k0;
+    if (i % kPhase == 0) {
+      // This phase of A was copied kPhase steps ago (or first of all): its
+      // group is complete once at most STAGES - 2 later ones are not.
+      cp_async_wait<STAGES - 2>();
+      __syncthreads();  // all of it has landed, and the other buffer has been read
+      stage_a(kt + kPhase, (i / kPhase + 1) & 1);
+    } else {
+      __syncwarp();  // every lane has read the stage that is filled next
+    }
+    issue(kt + STAGES - 1, s == 0 ? STAGES - 1 : s - 1);
+    cp_async_wait<STAGES - 1>();
+    __syncwarp();
+    const uint8_t* a = staged + (i / kPhase & 1) * ROWS * kPhaseRow + g * kPhaseRow +
+                       (i % kPhase) * 256 + t * 16;
+    uint4 x[NT][4];
+#pragma unroll
+    for (int r = 0; r < NT; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[r][j] = *reinterpret_cast<const uint4*>(a + r * 8 * kPhaseRow + j * 64);
+    w.multiply(ring + s * Weights::kStageBytes, kt, x, acc);
+    if (++s == STAGES) s = 0;
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+  // through shared memory for whole rows of C: [row][columns of the block + 4]
+  constexpr int COLS = kWarps * CT * 16;
+  float(*red)[COLS + 4] = reinterpret_cast<float(*)[COLS + 4]>(smem);
+#pragma unroll
   for (int c = 0; c < CT; ++c)
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      red[warp][c * 16 + g][i * 8 + 2 * t] = acc[c][i][0];
-      red[warp][c * 16 + g][i * 8 + 2 * t + 1] = acc[c][i][1];
-      red[warp][c * 16 + 8 + g][i * 8 + 2 * t] = acc[c][i][2];
-      red[warp][c * 16 + 8 + g][i * 8 + 2 * t + 1] = acc[c][i][3];
+    for (int r = 0; r < NT; ++r) {
+      const int col = (warp * CT + c) * 16 + g, row = r * 8 + 2 * t;
+      red[row][col] = acc[c][r][0];
+      red[row + 1][col] = acc[c][r][1];
+      red[row][col + 8] = acc[c][r][2];
+      red[row + 1][col + 8] = acc[c][r][3];
     }
   __syncthreads();
-  constexpr int OUT = CT * 16 * 8 * NT;
-  if (blocks > 1) {
-    // this block's sums, in its first warp's place, then all blocks' by rank
-    for (int i = threadIdx.x; i < OUT; i += kThreads) {
-      const int col = i % (CT * 16), row = i / (CT * 16);
-      float v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += red[w][col][row];
-      red[0][col][row] = v;
-    }
-    cluster_sync();
-  }
-  for (int i = threadIdx.x + rank * kThreads; i < OUT; i += kThreads * blocks) {
-    const int col = i % (CT * 16), row = i / (CT * 16);
-    const int n = nt0 * 16 + col, m = m0 + row;
-    if (n >= p.N || m >= p.M) continue;
-    float v = 0.0f;
-    if (blocks > 1) {
-      const uint32_t at = smem_u32(&red[0][col][row]);
-      for (int r = 0; r < blocks; ++r) v += ld_cluster_f32(map_to_rank(at, r));
-    } else {
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += red[w][col][row];
-    }
-    const float bias = p.epi.bias != nullptr ? p.epi.bias[n] : 0.0f;
-    if (p.c_bf16) {
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.C) + m * p.ldc + n;
-      *o = __float2bfloat16_rn(
-          epi_apply(p.epi, v, p.epi.beta != 0.0f ? __bfloat162float(*o) : 0.0f, bias));
-    } else {
-      float* o = static_cast<float*>(p.C) + m * p.ldc + n;
-      *o = epi_apply(p.epi, v, p.epi.beta != 0.0f ? *o : 0.0f, bias);
-    }
-  }
-  if (blocks > 1) cluster_sync();  // no block leaves while others read its sums
+  finish(COLS * rows, rank, blocks, [&](int i) { return &red[i / COLS][i % COLS]; },
+         [&](int i, float v) {
+           const int n = blockIdx.x * COLS + i % COLS;
+           if (n < p.N) write_c(p, m0 + i / COLS, n, v);
+         });
 }
 
 // Position of code (k, n) in the packed matrix: word index and shift.
@@ -367,19 +576,13 @@ int blocks_for(int64_t total, int threads) {
   return static_cast<int>(b < 8192 ? (b > 0 ? b : 1) : 8192);
 }
 
-template <int CT, int NT, int GPT>
-cudaError_t launch_tile(const W4Args& a, bool vec_a, int blocks, cudaStream_t stream) {
-  constexpr int STAGES = CT == 4 ? 3 : 4;
-  constexpr size_t kRing = static_cast<size_t>(kWarps) * STAGES * CT * kW4TileBytes;
-  constexpr size_t kExchange = sizeof(float) * kWarps * CT * 16 * (8 * NT + 1);
-  constexpr size_t kSmem = kRing > kExchange ? kRing : kExchange;
-  const auto kernel = w4_kernel<CT, NT, GPT, STAGES>;
-  if (kSmem > 48 * 1024) {
+cudaError_t launch_cluster(void (*kernel)(W4Args, int), const W4Args& a, bool vec_a, int gx,
+                           int gy, int blocks, size_t smem, cudaStream_t stream) {
+  if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  const int ntiles = (a.N + kW4TileN - 1) / kW4TileN;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0] = pdl_attribute();
@@ -387,48 +590,73 @@ cudaError_t launch_tile(const W4Args& a, bool vec_a, int blocks, cudaStream_t st
   attr[1].val.clusterDim.x = 1;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = static_cast<unsigned>(blocks);
-  cfg.gridDim = dim3(static_cast<unsigned>((ntiles + CT - 1) / CT),
-                     static_cast<unsigned>((a.M + 8 * NT - 1) / (8 * NT)),
+  cfg.gridDim = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy),
                      static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = blocks > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, a, vec_a ? 1 : 0);
 }
 
-template <int CT, int NT>
-cudaError_t launch_groups(const W4Args& a, bool vec_a, int blocks, cudaStream_t stream) {
-  if (a.group == 128) return launch_tile<CT, NT, 1>(a, vec_a, blocks, stream);
-  if (a.group == 64) return launch_tile<CT, NT, 2>(a, vec_a, blocks, stream);
-  return launch_tile<CT, NT, 4>(a, vec_a, blocks, stream);
+size_t larger(size_t a, size_t b) { return a > b ? a : b; }
+
+template <int CT, int GPT>
+cudaError_t launch_rows(const W4Args& a, bool vec_a, int gx, int blocks, cudaStream_t stream) {
+  constexpr int STAGES = 4;
+  const int rows = a.M < 8 ? a.M : 8;
+  const size_t smem =
+      larger(static_cast<size_t>(kWarps) * STAGES * (WarpWeights<CT, GPT>::kStageBytes + rows * 256),
+             sizeof(float) * kWarps * CT * 16 * 9);
+  return launch_cluster(w4_rows_kernel<CT, GPT, STAGES>, a, vec_a, gx, (a.M + 7) / 8, blocks,
+                        smem, stream);
 }
 
-template <int NT>
-cudaError_t launch_columns(int ct, const W4Args& a, bool vec_a, int blocks, cudaStream_t stream) {
-  if (ct == 4) return launch_groups<4, NT>(a, vec_a, blocks, stream);
-  if (ct == 2) return launch_groups<2, NT>(a, vec_a, blocks, stream);
-  return launch_groups<1, NT>(a, vec_a, blocks, stream);
+template <int CT, int NT, int GPT>
+cudaError_t launch_columns(const W4Args& a, bool vec_a, int gx, int blocks, cudaStream_t stream) {
+  constexpr int STAGES = CT == 4 ? 2 : 4;
+  const size_t smem =
+      larger(static_cast<size_t>(2) * 8 * NT * kPhaseRow +
+                 static_cast<size_t>(kWarps) * STAGES * WarpWeights<CT, GPT>::kStageBytes,
+             sizeof(float) * 8 * NT * (kWarps * CT * 16 + 4));
+  return launch_cluster(w4_columns_kernel<CT, NT, GPT, STAGES>, a, vec_a, gx,
+                        (a.M + 8 * NT - 1) / (8 * NT), blocks, smem, stream);
+}
+
+template <int GPT>
+cudaError_t launch_groups(const W4Args& a, const LayerDevice& dev, cudaStream_t stream) {
+  const bool vec_a = (reinterpret_cast<uintptr_t>(a.A) & 15u) == 0 && (a.lda % 8 == 0 || a.M == 1);
+  const int ntiles = (a.N + kW4TileN - 1) / kW4TileN, kts = (a.K + kW4TileK - 1) / kW4TileK;
+  int blocks = 1;
+  if (a.M <= 4) {
+    const bool two = ntiles >= 4 * dev.sms;
+    const int gx = two ? (ntiles + 1) / 2 : ntiles;
+    // few columns: at least two steps to a warp of each block
+    while (blocks < 8 && gx * blocks * 2 <= 2 * dev.sms && kts >= 4 * kWarps * blocks) blocks *= 2;
+    return two ? launch_rows<2, GPT>(a, vec_a, gx, blocks, stream)
+               : launch_rows<1, GPT>(a, vec_a, gx, blocks, stream);
+  }
+  // As wide as still gives every SM a block when K is cut in eight.
+  const int ct = ntiles >= 4 * dev.sms ? 4 : ntiles >= 2 * dev.sms ? 2 : 1;
+  const int gx = (ntiles + kWarps * ct - 1) / (kWarps * ct);
+  while (blocks < 8 && gx * blocks * 2 <= 2 * dev.sms && kts >= 4 * blocks) blocks *= 2;
+  if (a.M <= 8) {
+    if (ct == 4) return launch_columns<4, 1, GPT>(a, vec_a, gx, blocks, stream);
+    if (ct == 2) return launch_columns<2, 1, GPT>(a, vec_a, gx, blocks, stream);
+    return launch_columns<1, 1, GPT>(a, vec_a, gx, blocks, stream);
+  }
+  if (ct == 4) return launch_columns<4, 2, GPT>(a, vec_a, gx, blocks, stream);
+  if (ct == 2) return launch_columns<2, 2, GPT>(a, vec_a, gx, blocks, stream);
+  return launch_columns<1, 2, GPT>(a, vec_a, gx, blocks, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_w4(const W4Args& a, const LayerDevice& dev, cudaStream_t stream) {
-  const bool vec_a = (reinterpret_cast<uintptr_t>(a.A) & 15u) == 0 && (a.lda % 8 == 0 || a.M == 1);
-  const int ntiles = (a.N + kW4TileN - 1) / kW4TileN, kts = (a.K + kW4TileK - 1) / kW4TileK;
-  // A is read once per CT tiles of columns: wide where that would be more than
-  // the weights (M of 3 and up), as long as every SM still gets a block.
-  int ct = a.M > 4 ? 4 : a.M > 2 ? 2 : 1;
-  while (ct > 1 && ntiles < ct * dev.sms) ct /= 2;
-  // Few columns: K is shared by the blocks of a cluster too, at least two
-  // steps to a warp.
-  int blocks = 1;
-  while (blocks < 8 && (ntiles + ct - 1) / ct * blocks * 2 <= 2 * dev.sms &&
-         kts >= 4 * kWarps * blocks)
-    blocks *= 2;
-  const cudaError_t e = a.M <= 8 ? launch_columns<1>(ct, a, vec_a, blocks, stream)
-                                 : launch_columns<2>(ct, a, vec_a, blocks, stream);
+  const cudaError_t e = a.group == 128  ? launch_groups<1>(a, dev, stream)
+                        : a.group == 64 ? launch_groups<2>(a, dev, stream)
+                                        : launch_groups<4>(a, dev, stream);
   if (e == cudaSuccess) note_launches(1);
   return e;
 }
