@@ -272,33 +272,86 @@ __global__ void __launch_bounds__(512) norm_gate_bwd_kernel(NormArgs p, float* p
 // The gradient for rows of at most 4096 elements: one block per SM or more
 // walks the rows, and each thread copies its own 8 columns of the next rows
 // into a ring in shared memory (cp.async) while the block works on the present
-// one, so the row's three sums, each a barrier, cost no memory time.  A
-// thread's columns are its own for all its rows: their weights and their three
-// column sums stay in registers.
+// one, so the row's sums, each a barrier, cost no memory time.  Two barriers a
+// row: the last sums of a row and the first of the next one, sum(y^2), go
+// through one.  A thread's columns are its own for all its rows: their weights
+// and their three column sums stay in registers.  Arithmetic in pairs (one
+// instruction for two FP32 operations).
 
 constexpr int kRingWidth = 4096;
-constexpr int kRingStages = 3;
 constexpr int kRingBytes = 220 * 1024;
 
-// Sums over the block as block_sums, with 16 warps' entries always read (those
-// of absent warps stay zero).
-template <int N>
-__device__ __forceinline__ void block_sums16(float (&v)[N], float (*buf)[16]) {
+// Two FP32 numbers in one 64-bit register.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+  Pair d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
+__device__ __forceinline__ void unpair(Pair v, float* lo, float* hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float sum2(const Pair (&v)[2]) {
+  float a, b, c, d;
+  unpair(v[0], &a, &b);
+  unpair(v[1], &c, &d);
+  return (a + b) + (c + d);
+}
+__device__ __forceinline__ void pairs_of(const float (&v)[8], Pair (&p)[4]) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int i = 0; i < 4; ++i) p[i] = pair(v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ void floats_of(const Pair (&p)[4], float (&v)[8]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
-  if ((threadIdx.x & 31) == 0)
+  for (int i = 0; i < 4; ++i) unpair(p[i], &v[2 * i], &v[2 * i + 1]);
+}
+
+// Sums of 2 (or 4) values over the block, in every thread, in a fixed order.
+// The values share the butterfly: a step sends the half of them that the other
+// lane keeps.  buf: 32 (64) floats; entries of absent warps stay zero.
+__device__ __forceinline__ void block_sums2(float (&v)[2], float* buf) {
+  const int lane = threadIdx.x & 31;
+  float a = lane & 16 ? v[1] : v[0];
+  a += __shfl_xor_sync(0xFFFFFFFFu, lane & 16 ? v[0] : v[1], 16);
 #pragma unroll
-    for (int i = 0; i < N; ++i) buf[i][threadIdx.x >> 5] = v[i];
+  for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+  if ((lane & 15) == 0) buf[lane + (threadIdx.x >> 5)] = a;  // [value][16 warps]
   __syncthreads();
+  a = buf[lane];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float4* b = reinterpret_cast<const float4*>(buf[i]);
-    const float4 a = b[0], c = b[1], d = b[2], e = b[3];
-    v[i] = (((a.x + a.y) + (a.z + a.w)) + ((c.x + c.y) + (c.z + c.w))) +
-           (((d.x + d.y) + (d.z + d.w)) + ((e.x + e.y) + (e.z + e.w)));
-  }
+  for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+  v[0] = __shfl_sync(0xFFFFFFFFu, a, 0);
+  v[1] = __shfl_sync(0xFFFFFFFFu, a, 16);
+}
+__device__ __forceinline__ void block_sums3(float (&v)[3], float* buf) {
+  const int lane = threadIdx.x & 31;
+  float a = lane & 16 ? v[2] : v[0], b = lane & 16 ? 0.0f : v[1];
+  a += __shfl_xor_sync(0xFFFFFFFFu, lane & 16 ? v[0] : v[2], 16);
+  b += __shfl_xor_sync(0xFFFFFFFFu, lane & 16 ? v[1] : 0.0f, 16);
+  const float keep = lane & 8 ? b : a, send = lane & 8 ? a : b;
+  a = keep + __shfl_xor_sync(0xFFFFFFFFu, send, 8);  // lanes 0, 8, 16: values 0, 1, 2
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+  if ((lane & 7) == 0) buf[2 * lane + (threadIdx.x >> 5)] = a;  // [value][16 warps]
+  __syncthreads();
+  const float2 w = *reinterpret_cast<const float2*>(buf + 2 * lane);
+  a = w.x + w.y;
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+  v[0] = __shfl_sync(0xFFFFFFFFu, a, 0);
+  v[1] = __shfl_sync(0xFFFFFFFFu, a, 8);
+  v[2] = __shfl_sync(0xFFFFFFFFu, a, 16);
 }
 
 // This thread's 8 columns: adjacent (VEC, rows on 16 bytes) or blockDim.x apart.
@@ -330,204 +383,305 @@ __device__ __forceinline__ void own_store(T* row, int D, const float (&v)[8]) {
   }
 }
 
-// Whether rows of T go through the ring (2-byte elements off the 16-byte grid
-// are below the smallest asynchronous copy, and are loaded when used).
+// One operand's rows in the ring.  VEC: a thread copies what it reads itself,
+// 16-byte piece i at (i * blockDim.x + t) * 16.  Else rows start anywhere: the
+// 16-byte granules that hold the row are copied by the block and read from the
+// row's offset in its first granule (each granule holds bytes of the row).
 template <typename T, bool VEC>
-constexpr bool kRinged = VEC || sizeof(T) == 4;
+struct RingRows {
+  const T* row0;
+  const uint8_t* next;    // the next row to copy (of this thread's first piece, VEC)
+  int64_t stride;         // bytes from a row of this block to its next one
+  int slot;               // offset in a stage
+  uint32_t low, ld_low;   // low address bits of row 0, bytes from row to row
 
-// Bytes of a row in the ring.  Adjacent columns: 16-byte pieces, piece i of
-// thread t at (i * blockDim.x + t) * 16; else element e of t at
-// (e * blockDim.x + t) * 4.
-template <typename T, bool VEC>
-__host__ __device__ constexpr int ring_row_bytes(int threads) {
-  return kRinged<T, VEC> ? threads * 8 * static_cast<int>(sizeof(T)) : 0;
-}
-template <bool VEC, typename T>
-__device__ __forceinline__ void ring_copy(uint8_t* slot, const T* row, int D) {
-  if constexpr (VEC) {
-    if (own_col<VEC>(0) < D)
-#pragma unroll
-      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-        cp_async_16(slot + (i * blockDim.x + threadIdx.x) * 16,
-                    row + own_col<VEC>(0) + i * (16 / sizeof(T)));
-  } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (own_col<VEC>(e) < D)
-        cp_async_4(slot + (e * blockDim.x + threadIdx.x) * 4, row + own_col<VEC>(e));
+  static __host__ __device__ constexpr int bytes(int threads) {
+    return threads * 8 * static_cast<int>(sizeof(T)) + (VEC ? 0 : 32);
   }
-}
-template <bool VEC, typename T>
-__device__ __forceinline__ void ring_read(const uint8_t* slot, const T* row, int D,
-                                          float (&v)[8]) {
-  if constexpr (!kRinged<T, VEC>) {
-    own_load<VEC>(row, D, v);
-  } else {
+  __device__ __forceinline__ void init(const void* base, int64_t ld, int at) {
+    row0 = static_cast<const T*>(base);
+    const T* first = row0 + blockIdx.x * ld;
+    next = reinterpret_cast<const uint8_t*>(VEC ? first + own_col<true>(0) : first);
+    stride = ld * static_cast<int64_t>(sizeof(T)) * gridDim.x;
+    slot = at;
+    low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(base));
+    ld_low = static_cast<uint32_t>(ld * sizeof(T));
+  }
+  __device__ __forceinline__ void copy(uint8_t* stage, int D) const {
+    if constexpr (VEC) {
+      if (own_col<true>(0) < D) {
+        uint8_t* to = stage + slot + threadIdx.x * 16;
+        cp_async_16(to, next);
+        if constexpr (sizeof(T) == 4) cp_async_16(to + blockDim.x * 16, next + 16);
+      }
+    } else {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(next);
+      const uintptr_t end = a + D * static_cast<int>(sizeof(T));
+#pragma unroll
+      for (int i = 0; i <= static_cast<int>(sizeof(T)) / 2; ++i) {
+        const int at = (i * blockDim.x + threadIdx.x) * 16;
+        const uintptr_t from = (a & ~static_cast<uintptr_t>(15)) + at;
+        if (from < end) cp_async_16(stage + slot + at, reinterpret_cast<const void*>(from));
+      }
+    }
+  }
+  __device__ __forceinline__ void read(const uint8_t* stage, uint32_t row, int D,
+                                       Pair (&p)[4]) const {
+    float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0.0f;
     if constexpr (!VEC) {
+      const T* r = reinterpret_cast<const T*>(stage + slot + ((low + row * ld_low) & 15u));
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (own_col<VEC>(e) < D)
-          v[e] = *reinterpret_cast<const float*>(slot + (e * blockDim.x + threadIdx.x) * 4);
-    } else if (own_col<VEC>(0) < D) {
-      const uint4 a = *reinterpret_cast<const uint4*>(slot + threadIdx.x * 16);
+        if (own_col<false>(e) < D) v[e] = to_f32(r[own_col<false>(e)]);
+    } else if (own_col<true>(0) < D) {
+      const uint4 a = *reinterpret_cast<const uint4*>(stage + slot + threadIdx.x * 16);
       if constexpr (sizeof(T) == 2) {
         v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
         v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z); v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
       } else {
-        const uint4 b = *reinterpret_cast<const uint4*>(slot + (blockDim.x + threadIdx.x) * 16);
+        const uint4 b = *reinterpret_cast<const uint4*>(stage + slot +
+                                                        (blockDim.x + threadIdx.x) * 16);
         v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
         v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
         v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
         v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
       }
     }
+    pairs_of(v, p);
   }
-}
-
-// Offsets of the operands in a stage of the ring, x, y, d_x_out, dh, gate.
-struct RingLayout {
-  int y, d_x_out, dh, gate, bytes;
 };
+
 template <typename X, typename Y, typename H, bool VEC>
-__host__ __device__ RingLayout ring_layout(int threads, bool has_y, bool has_dxo, bool has_h,
-                                           bool full_gate) {
-  RingLayout l;
-  l.y = ring_row_bytes<X, VEC>(threads);
-  l.d_x_out = l.y + (has_y ? ring_row_bytes<Y, VEC>(threads) : 0);
-  l.dh = l.d_x_out + (has_dxo ? ring_row_bytes<X, VEC>(threads) : 0);
-  l.gate = l.dh + (has_h ? ring_row_bytes<H, VEC>(threads) : 0);
-  l.bytes = l.gate + (full_gate ? ring_row_bytes<float, VEC>(threads) : 0);
-  return l;
+int ring_stage_bytes(int threads, bool has_y, bool has_dxo, bool has_h, bool full_gate) {
+  return RingRows<X, VEC>::bytes(threads) * (has_dxo ? 2 : 1) +
+         (has_y ? RingRows<Y, VEC>::bytes(threads) : 0) +
+         (has_h ? RingRows<H, VEC>::bytes(threads) : 0) +
+         (full_gate ? RingRows<float, VEC>::bytes(threads) : 0);
 }
 
-template <typename X, typename Y, typename H, bool VEC, int STAGES>
+template <typename X, typename Y, typename H, bool VEC>
 __global__ void __launch_bounds__(512, 1)
-norm_gate_bwd_ring_kernel(NormArgs p, float* partial) {
+norm_gate_bwd_ring_kernel(NormArgs p, int stages, int stage_bytes, float* partial) {
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ __align__(16) float sums[2][3][2][16];  // alternate from row to row
-  const int D = p.D;
+  __shared__ __align__(16) float sums[2][32 + 64];  // alternate from row to row
+  const int D = p.D, T = p.T;
   const bool has_y = p.y != nullptr, has_h = p.dh != nullptr, has_dxo = p.d_x_out != nullptr;
   const bool row_gate = p.gate != nullptr && p.gate_col == 0;
   const bool col_gate = p.gate != nullptr && p.gate_col != 0 && p.gate_row == 0;
   const bool full_gate = p.gate != nullptr && p.gate_col != 0 && p.gate_row != 0;
-  const RingLayout lay = ring_layout<X, Y, H, VEC>(blockDim.x, has_y, has_dxo, has_h, full_gate);
-  for (int i = threadIdx.x; i < 2 * 3 * 2 * 16; i += blockDim.x) (&sums[0][0][0][0])[i] = 0.0f;
+  for (int i = threadIdx.x; i < 2 * 96; i += blockDim.x) (&sums[0][0])[i] = 0.0f;
   __syncthreads();
   grid_dependency_wait();
   grid_dependents_go();
 
-  auto x_row = [&](int64_t r) { return static_cast<const X*>(p.x) + r * p.ldx; };
-  auto y_row = [&](int64_t r) { return static_cast<const Y*>(p.y) + r * p.ldy; };
-  auto o_row = [&](int64_t r) { return static_cast<const X*>(p.d_x_out) + r * p.ld_d_x_out; };
-  auto h_row = [&](int64_t r) { return static_cast<const H*>(p.dh) + r * p.ld_dh; };
-  auto issue = [&](int64_t r, uint8_t* st) {
-    if (r < p.T) {
-      ring_copy<VEC>(st, x_row(r), D);
-      if (has_y) ring_copy<VEC>(st + lay.y, y_row(r), D);
-      if (has_dxo) ring_copy<VEC>(st + lay.d_x_out, o_row(r), D);
-      if (has_h) ring_copy<VEC>(st + lay.dh, h_row(r), D);
-      if (full_gate) ring_copy<VEC>(st + lay.gate, p.gate + r * p.gate_row, D);
+  const int threads = blockDim.x;
+  RingRows<X, VEC> rx, ro;
+  RingRows<Y, VEC> ry;
+  RingRows<H, VEC> rh;
+  RingRows<float, VEC> rg;
+  int at = 0;
+  rx.init(p.x, p.ldx, at);
+  at += rx.bytes(threads);
+  ry.init(p.y, p.ldy, at);
+  at += has_y ? ry.bytes(threads) : 0;
+  ro.init(p.d_x_out, p.ld_d_x_out, at);
+  at += has_dxo ? ro.bytes(threads) : 0;
+  rh.init(p.dh, p.ld_dh, at);
+  at += has_h ? rh.bytes(threads) : 0;
+  rg.init(p.gate, p.gate_row, at);
+
+  const int step = gridDim.x;
+  int row = blockIdx.x, ahead = row;
+  uint8_t* fill = ring;  // the stage of row `ahead`
+  uint8_t* const ring_end = ring + stages * stage_bytes;
+  // A row's copies in three parts, started at different places of an earlier
+  // row's work: all at once they fill the load queue and stop the block.
+  auto issue_block = [&]() {
+    if (ahead < T) {
+      if (has_y) ry.copy(fill, D);
+      rx.copy(fill, D);
+    }
+  };
+  auto issue_grads = [&]() {
+    if (ahead < T && has_h) rh.copy(fill, D);
+  };
+  auto issue_rest = [&]() {
+    if (ahead < T) {
+      if (has_dxo) ro.copy(fill, D);
+      if (full_gate) rg.copy(fill, D);
     }
     cp_async_commit();
+    ahead = ahead < T - step ? ahead + step : T;  // (row numbers stay in 32 bits)
+    rx.next += rx.stride;
+    ry.next += ry.stride;
+    ro.next += ro.stride;
+    rh.next += rh.stride;
+    rg.next += rg.stride;
+    fill += stage_bytes;
+    if (fill == ring_end) fill = ring;
   };
-  const int64_t step = gridDim.x;
-  int64_t row = blockIdx.x;
-#pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) issue(row + s * step, ring + s * lay.bytes);
+  for (int s = 0; s < stages - 1; ++s) {
+    issue_block();
+    issue_grads();
+    issue_rest();
+  }
 
-  float w2[8], w1[8], g[8];
+  // The gate and w_post act on a column as one factor, gw = gate * w_post.
+  // Without a gate, or with one value per column, both column sums come from
+  // sum(du n): dw_post = gate * that, dgate = w_post * that.
+  float v[8];
+  Pair w2[4], w1[4], g[4], gw[4];
+  auto weights = [&](const float* src, Pair (&w)[4]) {
+    if (src)
+      own_load<VEC>(src, D, v);
+    else
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w2[e] = w1[e] = g[e] = 1.0f;
-  if (p.w_post) own_load<VEC>(p.w_post, D, w2);
-  if (p.w_pre) own_load<VEC>(p.w_pre, D, w1);
-  if (col_gate) own_load<VEC>(p.gate, D, g);
-  float next_gate = row_gate && row < p.T ? p.gate[row * p.gate_row] : 1.0f;
-  float sum_post[8] = {}, sum_pre[8] = {}, sum_gate[8] = {};
+      for (int e = 0; e < 8; ++e) v[e] = 1.0f;
+    pairs_of(v, w);
+  };
+  weights(p.w_post, w2);
+  weights(p.w_pre, w1);
+  weights(col_gate ? p.gate : nullptr, g);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) gw[i] = mul2(g[i], w2[i]);
+  float next_gate = row_gate && row < T ? p.gate[row * p.gate_row] : 1.0f;
+  Pair sum_post[4] = {}, sum_pre[4] = {};
   const float inv_d = 1.0f / D;
-  int s = 0, odd = 0;
-  for (; row < p.T; row += step, odd ^= 1) {
-    // the stage that this thread read one row ago takes the row after the
-    // ring's others
-    issue(row + (STAGES - 1) * step, ring + (s == 0 ? STAGES - 1 : s - 1) * lay.bytes);
-    cp_async_wait<STAGES - 1>();
-    const uint8_t* st = ring + s * lay.bytes;
-    if (++s == STAGES) s = 0;
-    float y[8], u[8], du[8], h[8];
+  const Pair alpha = both(p.alpha);
+  auto squares = [&](const Pair (&q)[4]) {
+    Pair a[2] = {0, 0};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = du[e] = h[e] = 0.0f;
-    ring_read<VEC>(st, x_row(row), D, u);
-    if (has_y) ring_read<VEC>(st + lay.y, y_row(row), D, y);
-    if (has_dxo) ring_read<VEC>(st + lay.d_x_out, o_row(row), D, du);
-    if (has_h) ring_read<VEC>(st + lay.dh, h_row(row), D, h);
-    if (full_gate) ring_read<VEC>(st + lay.gate, p.gate + row * p.gate_row, D, g);
+    for (int i = 0; i < 4; ++i) a[i & 1] = fma2(q[i], q[i], a[i & 1]);
+    return sum2(a);
+  };
+  auto scale_of = [&](float sum) { return p.w_post ? rsqrtf(sum * inv_d + p.eps) : 1.0f; };
+  // The row after the present one has landed (its copies were all started one
+  // row ago or, with four stages, two).
+  auto landed = [&]() {
+    if (stages == 4)
+      cp_async_wait<1>();
+    else
+      cp_async_wait<0>();
+  };
+
+  const uint8_t* st = ring;
+  Pair y[4] = {}, y_next[4] = {};
+  landed();
+  __syncthreads();  // (other threads' copies, for rows off the 16-byte grid)
+  if (has_y) ry.read(st, row, D, y);
+  float first[2] = {squares(y), 0.0f};
+  block_sums2(first, sums[1]);
+  float r2 = scale_of(first[0]);
+
+  for (int odd = 0; row < T; odd ^= 1) {
+    // the stage of the row before this one takes the row after the ring's others
+    issue_block();
+    Pair u[4], du[4] = {}, h[4] = {};
+    rx.read(st, row, D, u);
+    if (has_h) rh.read(st, row, D, h);
+    if (full_gate) rg.read(st, row, D, g);
+    const bool more = row < T - step;
     if (row_gate) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] = next_gate;
-      if (row + step < p.T) next_gate = p.gate[(row + step) * p.gate_row];
+      for (int i = 0; i < 4; ++i) g[i] = both(next_gate);
+      if (more) next_gate = p.gate[static_cast<int64_t>(row + step) * p.gate_row];
     }
-    float r2 = 1.0f;
-    if (p.w_post) {
-      float a[1] = {0.0f};
+    if (row_gate || full_gate) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[0] = fmaf(y[e], y[e], a[0]);
-      block_sums16(a, sums[odd][0]);
-      r2 = rsqrtf(a[0] * inv_d + p.eps);
+      for (int i = 0; i < 4; ++i) gw[i] = mul2(g[i], w2[i]);
     }
-    float b[2] = {0.0f, 0.0f};
+    const Pair r2p = both(r2);
+    Pair b0[2] = {0, 0}, b1[2] = {0, 0};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      y[e] *= r2;  // n from here on
-      u[e] = has_y ? fmaf(p.alpha, u[e], g[e] * (y[e] * w2[e])) : p.alpha * u[e];
-      b[0] = fmaf(u[e], u[e], b[0]);
-      b[1] = fmaf(h[e] * w1[e], u[e], b[1]);
+    for (int i = 0; i < 4; ++i) {
+      y[i] = mul2(y[i], r2p);  // n from here on
+      u[i] = mul2(alpha, u[i]);
+      if (has_y) u[i] = fma2(gw[i], y[i], u[i]);
+      b0[i & 1] = fma2(u[i], u[i], b0[i & 1]);
+      b1[i & 1] = fma2(mul2(h[i], w1[i]), u[i], b1[i & 1]);
     }
+    if (has_dxo) ro.read(st, row, D, du);
+    landed();  // the next row, before the barrier that lets others read it
+    float b[2] = {sum2(b0), sum2(b1)};
+    block_sums2(b, sums[odd]);
+    issue_grads();
     float r1 = 0.0f, c1 = 0.0f;
     if (has_h) {
-      block_sums16(b, sums[odd][1]);
       r1 = rsqrtf(b[0] * inv_d + p.eps);
-      c1 = r1 * r1 * (b[1] * inv_d);
+      c1 = r1 * (b[1] * inv_d);
     }
-    float t[2] = {0.0f, 0.0f}, o[8], dg[8];
+    const Pair r1p = both(r1), c1p = both(-c1);
+    Pair t0[2] = {0, 0}, t1[2] = {0, 0}, o[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int i = 0; i < 4; ++i) {
       if (has_h) {
-        sum_pre[e] = fmaf(h[e] * u[e], r1, sum_pre[e]);
-        du[e] = fmaf(r1, fmaf(h[e], w1[e], -u[e] * c1), du[e]);
+        u[i] = mul2(u[i], r1p);
+        sum_pre[i] = fma2(h[i], u[i], sum_pre[i]);
+        du[i] = fma2(mul2(h[i], w1[i]), r1p, du[i]);
+        du[i] = fma2(mul2(u[i], r1p), c1p, du[i]);
       }
-      o[e] = p.alpha * du[e];
-      const float dp = g[e] * du[e];
-      sum_post[e] = fmaf(dp, y[e], sum_post[e]);
-      dg[e] = du[e] * (y[e] * w2[e]);
-      sum_gate[e] += dg[e];
-      u[e] = dp * w2[e];
-      t[0] = fmaf(u[e], y[e], t[0]);
-      t[1] += dg[e];
+      o[i] = mul2(alpha, du[i]);
+      u[i] = mul2(du[i], gw[i]);
+      t0[i & 1] = fma2(u[i], y[i], t0[i & 1]);
     }
-    own_store<VEC>(static_cast<X*>(p.dx) + row * p.ld_dx, D, o);
-    if (!has_y) continue;
-    if (full_gate) own_store<VEC>(p.dgate + row * p.gate_row, D, dg);
-    float c2 = 0.0f;
-    if (p.w_post || row_gate) {
-      block_sums16(t, sums[odd][2]);
-      if (p.w_post) c2 = t[0] * inv_d;
+    floats_of(o, v);
+    own_store<VEC>(static_cast<X*>(p.dx) + row * p.ld_dx, D, v);
+    issue_rest();
+    if (!row_gate && !full_gate) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum_post[i] = fma2(du[i], y[i], sum_post[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sum_post[i] = fma2(mul2(g[i], du[i]), y[i], sum_post[i]);
+        o[i] = mul2(du[i], mul2(y[i], w2[i]));
+        t1[i & 1] = fma2(du[i], mul2(y[i], w2[i]), t1[i & 1]);
+      }
+      if (full_gate) {
+        floats_of(o, v);
+        own_store<VEC>(p.dgate + row * p.gate_row, D, v);
+      }
+    }
+    st += stage_bytes;
+    if (st == ring_end) st = ring;
+    if (has_y && more) ry.read(st, row + step, D, y_next);
+    // always: the barrier also says that this row's stage has been read
+    float t[3] = {sum2(t0), sum2(t1), squares(y_next)};
+    block_sums3(t, sums[odd] + 32);
+    if (has_y) {
       if (row_gate && threadIdx.x == 0) p.dgate[row * p.gate_row] = t[1];
+      const Pair c2p = both(p.w_post ? -(t[0] * inv_d) * r2 : 0.0f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = fma2(y[i], c2p, mul2(u[i], r2p));
+      floats_of(o, v);
+      own_store<VEC>(p.dy + row * p.ld_dy, D, v);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = r2 * (u[e] - y[e] * c2);
-    own_store<VEC>(p.dy + row * p.ld_dy, D, o);
+    for (int i = 0; i < 4; ++i) y[i] = y_next[i];
+    r2 = scale_of(t[2]);
+    row = more ? row + step : T;
   }
   if (partial == nullptr) return;
   float* out = partial + static_cast<int64_t>(blockIdx.x) * 3 * D;
+  auto leave = [&](const Pair (&sum)[4], float* to) {
+    floats_of(sum, v);
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (own_col<VEC>(e) < D) {
-      const int c = own_col<VEC>(e);
-      out[c] = sum_post[e];
-      out[D + c] = sum_pre[e];
-      out[2 * D + c] = sum_gate[e];
+    for (int e = 0; e < 8; ++e)
+      if (own_col<VEC>(e) < D) to[own_col<VEC>(e)] = v[e];
+  };
+  leave(sum_pre, out + D);
+  if (col_gate) {
+    Pair t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t[i] = mul2(sum_post[i], w2[i]);
+      sum_post[i] = mul2(sum_post[i], g[i]);
     }
+    leave(t, out + 2 * D);
+  }
+  leave(sum_post, out);
 }
 
 // 32 columns per block; the slots are cut into 8 runs, one per warp, whose
@@ -617,31 +771,34 @@ cudaError_t backward_ring(const NormArgs& a, int slots, float* partial, cudaStre
                           int* per_sm) {
   const int threads = threads_for(a.D, 8);
   const bool full = a.gate != nullptr && a.gate_col != 0 && a.gate_row != 0;
-  const int stage = ring_layout<X, Y, H, VEC>(threads, a.y != nullptr, a.d_x_out != nullptr,
-                                              a.dh != nullptr, full).bytes;
-  // (five FP32 operands of 4096 columns take 80 KB a stage)
-  const bool three = kRingStages * stage <= kRingBytes;
-  const int smem = (three ? kRingStages : 2) * stage;
+  const int stage = ring_stage_bytes<X, Y, H, VEC>(threads, a.y != nullptr, a.d_x_out != nullptr,
+                                                   a.dh != nullptr, full);
+  const int stages = 4 * stage <= kRingBytes ? 4 : 3;
+  const int smem = stages * stage;
   if (per_sm) {
     const int by_smem = kRingBytes / (smem + 2048), by_threads = 512 / threads;
     *per_sm = by_smem < by_threads ? by_smem : by_threads;
     if (*per_sm < 1) *per_sm = 1;
     return cudaSuccess;
   }
-  void (*kernel)(NormArgs, float*) = three ? norm_gate_bwd_ring_kernel<X, Y, H, VEC, kRingStages>
-                                           : norm_gate_bwd_ring_kernel<X, Y, H, VEC, 2>;
+  const auto kernel = norm_gate_bwd_ring_kernel<X, Y, H, VEC>;
   if (smem > 40 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(kernel, dim3(slots), dim3(threads), smem, st, a, partial);
+  return launch_pdl(kernel, dim3(slots), dim3(threads), smem, st, a, stages, stage,
+                    partial);
 }
 
 template <typename X, typename Y, typename H>
 cudaError_t backward(const NormArgs& a, int slots, float* partial, cudaStream_t st, int* per_sm) {
   const Shape s = shape_for(a);
-  if (a.D <= kRingWidth)
+  // (five FP32 operands of over 3700 columns take more than three stages hold)
+  const bool full = a.gate != nullptr && a.gate_col != 0 && a.gate_row != 0;
+  const int row_bytes = (sizeof(X) + sizeof(Y) + sizeof(X) + sizeof(H) + (full ? 4 : 0)) *
+                        threads_for(a.D, 8) * 8 + 5 * 32;
+  if (a.D <= kRingWidth && 3 * row_bytes <= kRingBytes)
     return s.vec == 8 ? backward_ring<X, Y, H, true>(a, slots, partial, st, per_sm)
                       : backward_ring<X, Y, H, false>(a, slots, partial, st, per_sm);
   if (per_sm) {
@@ -649,7 +806,11 @@ cudaError_t backward(const NormArgs& a, int slots, float* partial, cudaStream_t 
     return cudaSuccess;
   }
   if (s.vec == 1)
-    return launch_bwd(norm_gate_bwd_kernel<X, Y, H, 1, 32>, a, s, slots, partial, st);
+    return s.vpt == 8
+               ? launch_bwd(norm_gate_bwd_kernel<X, Y, H, 1, 8>, a, s, slots, partial, st)
+               : launch_bwd(norm_gate_bwd_kernel<X, Y, H, 1, 32>, a, s, slots, partial, st);
+  if (s.vpt == 1)
+    return launch_bwd(norm_gate_bwd_kernel<X, Y, H, 8, 1>, a, s, slots, partial, st);
   if (s.vpt == 2)
     return launch_bwd(norm_gate_bwd_kernel<X, Y, H, 8, 2>, a, s, slots, partial, st);
   return launch_bwd(norm_gate_bwd_kernel<X, Y, H, 8, 4>, a, s, slots, partial, st);
