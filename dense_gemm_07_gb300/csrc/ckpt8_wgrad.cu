@@ -71,6 +71,8 @@ constexpr int EPI_WARPS = 8;
 constexpr int BOX_BYTES = 32 * 32 * 4;
 constexpr int EPI_BYTES = EPI_WARPS * BOX_BYTES;
 constexpr int GROUP = 8;
+// Stages (0.5 us) that a split of the last wave's tiles has to save.
+constexpr int kSplitStages = 24;
 // Registers per thread of the roles (setmaxnreg): together at most the 640 x
 // 96 that the block is launched with.
 constexpr int kRegsCopy = 32, kRegsDecode = 56, kRegsSum = 168;
@@ -475,9 +477,14 @@ ckpt8_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constan
         before = __shfl_sync(0xFFFFFFFFu, before, 0);
         __threadfence();
         if (before + 1 != static_cast<unsigned int>(st.nseg)) continue;
+        // (of two segments only the other's: a + b == b + a)
         for (int s = 0; s < st.nseg; ++s) {
           const float* other = slot(st.q_first + s);
-          if (s == 0) {
+          if (st.nseg == 2) {
+            if (st.q_first + s == pair) continue;
+#pragma unroll
+            for (int i = 0; i < 128; ++i) sum[i] += __ldcg(other + i * 32);
+          } else if (s == 0) {
 #pragma unroll
             for (int i = 0; i < 128; ++i) sum[i] = __ldcg(other + i * 32);
           } else {
@@ -610,7 +617,9 @@ PairSchedule ckpt8_wgrad_schedule(int64_t T, int64_t K, int64_t N, int max_pairs
   const int64_t tiles = static_cast<int64_t>(s.tiles_m) * s.tiles_n;
   const int64_t rest = tiles % max_pairs;
   int64_t sk = 0;
-  if (rest > 0 && s.num_kb >= 4 && rest * 8 < max_pairs * int64_t(7)) {
+  // What the split saves of the last wave, in stages, against the exchange of
+  // the segments' sums (kSplitStages).
+  if (rest > 0 && (max_pairs - rest) * s.num_kb > kSplitStages * max_pairs) {
     // the partial last wave, with the last whole one if there is one
     sk = tiles > max_pairs ? rest + max_pairs : rest;
     // runs of at least half a tile: at most kSkMaxSeg segments a tile
