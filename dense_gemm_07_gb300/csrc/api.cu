@@ -50,7 +50,7 @@ enum ScratchUse {
   kScratchPack = 2,     // BF16 operands copied to aligned rows
   kScratchSmall = 3,    // BF16 small problems: counters (kept zero) + partial tiles
   kScratchLayer = 4,  // column sums and operand copies of the layer operators
-  kScratchWgrad = 5,  // weight gradients: counters (kept zero) + segments' sums
+  kScratchCounted = 5,  // layer operators: counters (kept zero) + partial sums
   kScratchUses = 6
 };
 struct StreamScratch {
@@ -1041,6 +1041,18 @@ gemm_status_t layer_scratch(cudaStream_t stream, int64_t bytes, LayerScratch* ou
   return call_scratch(d, stream, kScratchLayer, bytes, &out->ptr, &fresh, &out->owned);
 }
 
+gemm_status_t layer_counted_scratch(cudaStream_t stream, int64_t bytes, LayerScratch* out) {
+  DeviceState* d = nullptr;
+  gemm_status_t s = device_state(&d);
+  if (s != GEMM_OK) return s;
+  bool fresh = false;
+  s = call_scratch(d, stream, kScratchCounted, kLayerCounterBytes + bytes, &out->ptr, &fresh,
+                   &out->owned);
+  if (s == GEMM_OK && fresh)
+    s = from_cuda(cudaMemsetAsync(out->ptr, 0, kLayerCounterBytes, stream));
+  return s;
+}
+
 void layer_scratch_done(const LayerScratch& s, cudaStream_t stream) {
   if (s.owned) pool_free(s.ptr, stream);
 }
@@ -1075,17 +1087,11 @@ gemm_status_t layer_ckpt8_wgrad(int64_t T, int64_t K, int64_t N, const uint8_t* 
                          static_cast<int>(N)};
     s = from_cuda(launch_pack_u16(&job, 1, stream));
   }
-  // Counters first, in an area of fixed size (zero when new; each launch puts
-  // its own back), then the segments' sums.
-  constexpr int64_t kCounterBytes = 64 << 10;
-  void* ws = nullptr;
-  bool owned = false;
+  // Counters of the split tiles, then the segments' sums.
+  LayerScratch ws;
   if (s == GEMM_OK && ps.sk_tiles > 0) {
-    if (ckpt8_wgrad_counters(ps) * 4 > kCounterBytes) s = GEMM_ERR_INTERNAL;
-    if (s == GEMM_OK)
-      s = call_scratch(d, stream, kScratchWgrad, kCounterBytes + ckpt8_wgrad_partial_bytes(ps),
-                       &ws, &fresh, &owned);
-    if (s == GEMM_OK && fresh) s = from_cuda(cudaMemsetAsync(ws, 0, kCounterBytes, stream));
+    if (ckpt8_wgrad_counters(ps) * 4 > kLayerCounterBytes) s = GEMM_ERR_INTERNAL;
+    if (s == GEMM_OK) s = layer_counted_scratch(stream, ckpt8_wgrad_partial_bytes(ps), &ws);
   }
   CUtensorMap tmY, tmW;
   if (s == GEMM_OK) s = make_map(&tmY, y, N, T, ld_op, 64, kCkptStageRows);
@@ -1094,11 +1100,12 @@ gemm_status_t layer_ckpt8_wgrad(int64_t T, int64_t K, int64_t N, const uint8_t* 
     s = from_cuda(launch_ckpt8_wgrad(
         tmY, tma_w ? &tmW : nullptr, ps, static_cast<int>(T), static_cast<int>(K),
         static_cast<int>(N), q, scales, dW, ldw, beta,
-        ws ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes) : nullptr,
-        static_cast<unsigned int*>(ws), d->status, stream));
+        ws.ptr ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws.ptr) + kLayerCounterBytes)
+               : nullptr,
+        static_cast<unsigned int*>(ws.ptr), d->status, stream));
   }
   if (packed_owned) pool_free(packed, stream);
-  if (owned) pool_free(ws, stream);
+  layer_scratch_done(ws, stream);
   return s;
 }
 

@@ -309,25 +309,26 @@ gemm_status_t gemm_ckpt8_act_grad(int64_t T, int64_t N, const void* G, int64_t l
   a.act = activation;
   a.out = as_bf16(dZ);
   a.ld_out = ld_dz;
-  const int slots = T > 0 ? ckpt8_act_grad_slots(a.T, a.N, dev) : 0;
+  if (T == 0) {  // the empty sum
+    return layer_from_cuda(launch_zero_fill_f32(dbias, N, 1, a.N, epi_identity(), st));
+  }
+  int slots = ckpt8_act_grad_slots(a.T, a.N, dev);
   LayerScratch ws;
+  ColumnTotals sums;
   if (dbias != nullptr) {
-    s = layer_scratch(st, static_cast<int64_t>(slots) * N * 4, &ws);
-    if (s != GEMM_OK) return s;
+    sums.out = dbias;
+    // (very wide rows have more column blocks than counters: one block a column
+    // block walks all rows then)
+    if (ckpt8_act_grad_counters(a.N) * 4 > kLayerCounterBytes) slots = 1;
+    if (slots > 1) {
+      s = layer_counted_scratch(st, static_cast<int64_t>(slots) * N * 4, &ws);
+      if (s != GEMM_OK) return s;
+      sums.counters = static_cast<unsigned int*>(ws.ptr);
+      sums.partial =
+          reinterpret_cast<float*>(static_cast<uint8_t*>(ws.ptr) + kLayerCounterBytes);
+    }
   }
-  if (T > 0)
-    s = layer_from_cuda(launch_ckpt8_act_grad(
-        a, slots, dbias ? static_cast<float*>(ws.ptr) : nullptr, st));
-  if (s == GEMM_OK && dbias != nullptr) {
-    ColumnSums c;
-    c.partial = static_cast<const float*>(ws.ptr);
-    c.ld = N;
-    c.slots = slots;
-    c.n = a.N;
-    c.count = 1;
-    c.out[0] = dbias;
-    s = layer_from_cuda(launch_column_sums(c, st));
-  }
+  s = layer_from_cuda(launch_ckpt8_act_grad(a, sums, slots, st));
   layer_scratch_done(ws, st);
   return s;
 }

@@ -198,15 +198,17 @@ ckpt8_unpack_kernel(int T, int N, const uint8_t* __restrict__ q,
   }
 }
 
-// dz = g * act'(kept z) and the block's column sums of dz (before rounding),
-// to partial[blockIdx.y][N].
+// dz = g * act'(kept z), and the column sums of dz before its rounding: each
+// block leaves its own in partial[blockIdx.y][N] and counts itself at its
+// columns' counter; the last one to do so adds all of them in the order of the
+// rows and puts the counter back to zero.  (A launch of its own for these sums
+// cost 4 of 21 us at 127 x 1000.)
 template <typename X, int C, int ACT>
-__global__ void __launch_bounds__(kThreads) ckpt8_act_grad_kernel(CkptArgs p, float* partial) {
+__global__ void __launch_bounds__(kThreads) ckpt8_act_grad_kernel(CkptArgs p, ColumnTotals sums) {
   grid_dependency_wait();
   grid_dependents_go();
   const int c = (blockIdx.x * kThreads + threadIdx.x) * C;
-  if (c >= p.N) return;
-  const int panels = (p.T + kCkptRun - 1) / kCkptRun;
+  const int panels = c < p.N ? (p.T + kCkptRun - 1) / kCkptRun : 0;
   float sum[C] = {};
   for (int panel = blockIdx.y; panel < panels; panel += gridDim.y) {
     const int t0 = panel * kCkptRun;
@@ -240,10 +242,36 @@ __global__ void __launch_bounds__(kThreads) ckpt8_act_grad_kernel(CkptArgs p, fl
         store_cols<C>(o + i * p.ld_out, dz);
       }
   }
-  if (partial) {
+  if (sums.out == nullptr) return;
+  if (gridDim.y == 1) {
+    if (c < p.N)
 #pragma unroll
-    for (int j = 0; j < C; ++j) partial[static_cast<int64_t>(blockIdx.y) * p.N + c + j] = sum[j];
+      for (int j = 0; j < C; ++j) sums.out[c + j] = sum[j];
+    return;
   }
+  if (c < p.N)
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      sums.partial[static_cast<int64_t>(blockIdx.y) * p.N + c + j] = sum[j];
+  __threadfence();
+  __shared__ bool last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = atomicAdd(sums.counters + blockIdx.x, 1u) + 1 == gridDim.y;
+    if (last) sums.counters[blockIdx.x] = 0u;  // for the next launch
+  }
+  __syncthreads();
+  if (!last || c >= p.N) return;
+  __threadfence();
+#pragma unroll
+  for (int j = 0; j < C; ++j) sum[j] = 0.0f;
+#pragma unroll 16
+  for (int y = 0; y < static_cast<int>(gridDim.y); ++y)
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      sum[j] += __ldcg(sums.partial + static_cast<int64_t>(y) * p.N + c + j);
+#pragma unroll
+  for (int j = 0; j < C; ++j) sums.out[c + j] = sum[j];
 }
 
 dim3 panel_grid(int T, int N) {
@@ -274,13 +302,12 @@ static cudaError_t pack(const CkptArgs& a, cudaStream_t st) {
 }
 
 template <typename X, int C>
-static cudaError_t act_grad(const CkptArgs& a, int slots, float* partial, cudaStream_t st) {
+static cudaError_t act_grad(const CkptArgs& a, const ColumnTotals& sums, int slots,
+                            cudaStream_t st) {
   const dim3 grid(column_blocks(a.N, C), slots), block(kThreads);
-  if (a.act == 0)
-    return launch_pdl(ckpt8_act_grad_kernel<X, C, 0>, grid, block, 0, st, a, partial);
-  if (a.act == 1)
-    return launch_pdl(ckpt8_act_grad_kernel<X, C, 1>, grid, block, 0, st, a, partial);
-  return launch_pdl(ckpt8_act_grad_kernel<X, C, 2>, grid, block, 0, st, a, partial);
+  if (a.act == 0) return launch_pdl(ckpt8_act_grad_kernel<X, C, 0>, grid, block, 0, st, a, sums);
+  if (a.act == 1) return launch_pdl(ckpt8_act_grad_kernel<X, C, 1>, grid, block, 0, st, a, sums);
+  return launch_pdl(ckpt8_act_grad_kernel<X, C, 2>, grid, block, 0, st, a, sums);
 }
 
 cudaError_t launch_ckpt8_pack(const CkptArgs& a, cudaStream_t stream) {
@@ -304,22 +331,24 @@ cudaError_t launch_ckpt8_unpack(int T, int N, const uint8_t* q, const uint8_t* s
   return e;
 }
 
+// The blocks of a column block: each walks the same number of panels, so that
+// about 5 blocks an SM are at work.
 int ckpt8_act_grad_slots(int T, int N, const LayerDevice& dev) {
   const int64_t panels = (T + kCkptRun - 1) / kCkptRun;
-  const int64_t cols = column_blocks(N, 2);
-  int64_t s = (static_cast<int64_t>(dev.sms) * 8 + cols - 1) / cols;
-  if (s > panels) s = panels;
-  return static_cast<int>(s < 1 ? 1 : s);
+  const int64_t each = panels * column_blocks(N, 2) / (static_cast<int64_t>(dev.sms) * 5) + 1;
+  return static_cast<int>((panels + each - 1) / each);
 }
 
-cudaError_t launch_ckpt8_act_grad(const CkptArgs& a, int slots, float* partial,
+int64_t ckpt8_act_grad_counters(int N) { return column_blocks(N, 1); }
+
+cudaError_t launch_ckpt8_act_grad(const CkptArgs& a, const ColumnTotals& sums, int slots,
                                   cudaStream_t stream) {
   using B = __nv_bfloat16;
   const bool two = pairs_ok(a);
-  const cudaError_t e = a.x_bf16 ? (two ? act_grad<B, 2>(a, slots, partial, stream)
-                                        : act_grad<B, 1>(a, slots, partial, stream))
-                                 : (two ? act_grad<float, 2>(a, slots, partial, stream)
-                                        : act_grad<float, 1>(a, slots, partial, stream));
+  const cudaError_t e = a.x_bf16 ? (two ? act_grad<B, 2>(a, sums, slots, stream)
+                                        : act_grad<B, 1>(a, sums, slots, stream))
+                                 : (two ? act_grad<float, 2>(a, sums, slots, stream)
+                                        : act_grad<float, 1>(a, sums, slots, stream));
   if (e == cudaSuccess) note_launches(1);
   return e;
 }

@@ -30,6 +30,10 @@ struct LayerScratch {
   bool owned = false;
 };
 gemm_status_t layer_scratch(cudaStream_t stream, int64_t bytes, LayerScratch* out);
+// Scratch of another kind that starts with kLayerCounterBytes of counters: zero
+// when the block is new, and put back to zero by whoever uses them.
+constexpr int64_t kLayerCounterBytes = 64 << 10;
+gemm_status_t layer_counted_scratch(cudaStream_t stream, int64_t bytes, LayerScratch* out);
 void layer_scratch_done(const LayerScratch& s, cudaStream_t stream);
 gemm_status_t layer_epilogue(const gemm_epilogue_t* e, EpiParams* out);
 gemm_status_t layer_from_cuda(cudaError_t e);
@@ -221,9 +225,16 @@ struct CkptArgs {
 cudaError_t launch_ckpt8_pack(const CkptArgs& a, cudaStream_t stream);
 cudaError_t launch_ckpt8_unpack(int T, int N, const uint8_t* q, const uint8_t* scales, void* out,
                                 int64_t ld, bool out_bf16, cudaStream_t stream);
-// Rows of the partial column sums of act_grad.
+// Where act_grad's column sums go (a null out: nowhere).  partial: slots x N
+// floats; counters: ckpt8_act_grad_counters(N), zero before and after.
+struct ColumnTotals {
+  float* out = nullptr;
+  float* partial = nullptr;
+  unsigned int* counters = nullptr;
+};
 int ckpt8_act_grad_slots(int T, int N, const LayerDevice& dev);
-cudaError_t launch_ckpt8_act_grad(const CkptArgs& a, int slots, float* partial,
+int64_t ckpt8_act_grad_counters(int N);
+cudaError_t launch_ckpt8_act_grad(const CkptArgs& a, const ColumnTotals& sums, int slots,
                                   cudaStream_t stream);
 
 // ---- weight gradient from an 8-bit checkpoint (ckpt8_wgrad.cu)
