@@ -600,3 +600,89 @@ def test_layer_refusals():
     want = g7.gemm_norm_gate(n["x"], n["y"], weight_post=off.clone(), weight_pre=off.clone())
     _close(h, want[1].double(), 2.0 ** -7 * want[1].double().abs() + 1e-9)
     assert _abi.gemm_w4_packed_bytes(-1, 4) == -1
+
+
+# ------------------------------------------------------------- together
+
+def _rel(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+def test_block_trains_and_decodes():
+    """The example block against 64 bits.  BF16 operands and outputs round by 2^-9
+    each, 8-bit checkpoints by at most half a step of 2 * max / 127 over 32 rows
+    (about 0.5 % of a normal run's values): a few of these in a chain stay below 3 %."""
+    from dense_gemm_07_gb300 import layer_example
+    T, D, H = 192, 256, 640
+    b = layer_example.Block(D, H, seed=3)
+    g = _gen(4)
+    x, dx, dh = (_randn(g, T, D, dtype=BF16), _randn(g, T, D, dtype=BF16), _randn(g, T, D))
+    x_out, h, grads = layer_example.train_step(b, x, dx, dh)
+    v = {n: getattr(b, n).double().requires_grad_() for n in ("w1", "b1", "w2", "pre", "post", "gate",
+                                                              "next_pre")}
+    v["x"] = x.double().requires_grad_()
+
+    def block(x_, w1, w2, h_=None):
+        r = lambda t: t / torch.sqrt((t ** 2).mean(1, keepdim=True) + 1e-6)  # noqa: E731
+        h_ = r(x_) * v["pre"] if h_ is None else h_
+        y = act(h_ @ w1 + v["b1"], "gelu") @ w2
+        u = b.scale * x_ + v["gate"] * (r(y) * v["post"])
+        return u, r(u) * v["next_pre"]
+
+    u, hn = block(v["x"], v["w1"], v["w2"])
+    assert _rel(x_out, u.detach()) < 0.01 and _rel(h, hn.detach()) < 0.01
+    ((u * dx.double()).sum() + (hn * dh.double()).sum()).backward()
+    for name, got in grads.items():
+        assert _rel(got, v[name].grad) < 0.03, name
+
+    rows = x[:5]
+    _, h0 = g7.gemm_norm_gate(rows, weight_pre=b.pre)
+    w1, w2 = (w4_weights(w4_layout_decode(q[0], *s).cuda(), q[1], q[2], b.group)
+              for q, s in ((b.w1_q, (D, H)), (b.w2_q, (H, D))))
+    du, dhn = layer_example.decode_step(b, rows, h0)
+    u, hn = block(rows.double(), w1, w2, h0.double())
+    assert _rel(du, u.detach()) < 0.01 and _rel(dhn, hn.detach()) < 0.01
+
+
+def test_weight_gradient_gives_up_after_a_bounded_wait():
+    """A first slice that is never copied: the wait runs out, the kernel unwinds and
+    the status says so; the next call is exact."""
+    T, K, N = 300, 300, 520
+    x = torch.full((T, K), 127.0, device="cuda")
+    dy = torch.ones((T, N), dtype=BF16, device="cuda")
+    k = g7.gemm_ckpt8_pack(x)
+    try:
+        assert _abi.gemm_debug_inject(1, 2_000_000) == _abi.GEMM_OK
+        g7.gemm_ckpt8_wgrad(k, dy)
+        assert g7.gemm_get_device_status() == _abi.GEMM_ERR_TIMEOUT
+    finally:
+        assert _abi.gemm_debug_inject(0, 0) == _abi.GEMM_OK
+    assert torch.equal(g7.gemm_ckpt8_wgrad(k, dy), torch.full((K, N), 127.0 * T, device="cuda"))
+    assert g7.gemm_get_device_status() == _abi.GEMM_OK
+
+
+def test_layer_large_offsets():
+    """Rows past 2^31 elements of a buffer: a checkpoint, a norm and a gradient of the
+    last rows of a long tensor equal those of the rows alone."""
+    T, D = 262150, 8256  # 2.16e9 elements of BF16
+    big = torch.empty((T, D), dtype=BF16, device="cuda")
+    tail = _randn(_gen(1), 70, D, dtype=BF16)
+    big[:-70] = 1.0
+    big[-70:] = tail
+    w = torch.ones(D, device="cuda")
+    _, h = g7.gemm_norm_gate(big, weight_pre=w, x_out=big)
+    _, want = g7.gemm_norm_gate(tail, weight_pre=w)
+    assert torch.equal(h[-70:], want)
+    del h
+    k = g7.gemm_ckpt8_pack(big)
+    assert int(k.q.numel()) > 2 ** 31
+    got = kept(big[-38:])
+    last = g7.gemm_ckpt8_unpack(k)[-38:]
+    first = (T - 38) % 32
+    assert first == 0 and torch.equal(last.double(), got)
+    del last
+    dy = torch.zeros((T, 8), dtype=BF16, device="cuda")
+    dy[-38:] = 1.0
+    dw = g7.gemm_ckpt8_wgrad(k, dy)
+    s = got.abs().sum(0, keepdim=True).t()
+    _close(dw, got.sum(0).view(-1, 1).expand(D, 8), 80 * EPS32 * s + 1e-30)
