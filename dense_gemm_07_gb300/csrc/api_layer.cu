@@ -218,7 +218,12 @@ gemm_status_t gemm_norm_gate_bwd(const gemm_norm_gate_args_t* args,
   const bool gate_sums = n.gate != nullptr && n.gate_col != 0 && n.gate_row == 0;
   const bool sums = n.w_post != nullptr || n.w_pre != nullptr || gate_sums;
   LayerScratch ws;
-  const int slots = n.T > 0 ? norm_gate_bwd_slots(n, dev) : 0;
+  NormBwdPlan plan;
+  if (n.T > 0) {
+    s = layer_from_cuda(norm_gate_bwd_plan(n, dev, &plan));
+    if (s != GEMM_OK) return s;
+  }
+  const int slots = plan.slots;
   ColumnSums c;
   if (sums) {
     s = layer_scratch(st, static_cast<int64_t>(slots) * 3 * n.D * 4, &ws);
@@ -233,7 +238,7 @@ gemm_status_t gemm_norm_gate_bwd(const gemm_norm_gate_args_t* args,
     c.out[2] = gate_sums ? n.dgate : nullptr;
   }
   if (n.T > 0)
-    s = layer_from_cuda(launch_norm_gate_bwd(n, slots, static_cast<float*>(ws.ptr), st));
+    s = layer_from_cuda(launch_norm_gate_bwd(n, plan, static_cast<float*>(ws.ptr), st));
   if (s == GEMM_OK && sums) s = layer_from_cuda(launch_column_sums(c, st));
   layer_scratch_done(ws, st);
   return s;

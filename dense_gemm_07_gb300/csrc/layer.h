@@ -192,10 +192,14 @@ struct NormArgs {
   float* dw_pre = nullptr;
 };
 cudaError_t launch_norm_gate(const NormArgs& a, cudaStream_t stream);
-// Slots (rows) of the partial column sums that the backward pass writes:
-// `slots` x 3 x D floats.
-int norm_gate_bwd_slots(const NormArgs& a, const LayerDevice& dev);
-cudaError_t launch_norm_gate_bwd(const NormArgs& a, int slots, float* partial,
+// How the gradient runs: `slots` clusters of `parts` blocks walk the rows, a
+// block with part_cols columns of them; its column sums leave slots x 3 x D
+// floats in `partial` (null: none are wanted).
+struct NormBwdPlan {
+  int parts = 0, part_cols = 0, threads = 0, stages = 0, stage_bytes = 0, slots = 0;
+};
+cudaError_t norm_gate_bwd_plan(const NormArgs& a, const LayerDevice& dev, NormBwdPlan* plan);
+cudaError_t launch_norm_gate_bwd(const NormArgs& a, const NormBwdPlan& plan, float* partial,
                                  cudaStream_t stream);
 
 // ---- column sums: out[c] = sum over s = 0 .. slots - 1, in that order, of

@@ -18,6 +18,7 @@
 // taken over the block while it stays there.
 #include "kernels.h"
 #include "layer.h"
+#include "sm103_ptx.cuh"
 
 namespace g07 {
 namespace {
@@ -117,168 +118,20 @@ __global__ void __launch_bounds__(512) norm_gate_kernel(NormArgs p) {
   }
 }
 
-// Blocks walk the rows; the column sums (dw_post, dw_pre, dgate) of a block's
-// rows gather in shared memory, each element by the one thread that owns its
-// column, and go to `partial` (slot blockIdx.x, 3 x D) at the end.
-template <typename X, typename Y, typename H, int VEC, int VPT>
-__global__ void __launch_bounds__(512) norm_gate_bwd_kernel(NormArgs p, float* partial) {
-  extern __shared__ float sums[];  // [3][D]
-  __shared__ float row_buf[2][3][32];  // alternate from row to row
-  const bool has_y = p.y != nullptr, has_h = p.dh != nullptr;
-  const bool row_gate = p.gate != nullptr && p.gate_col == 0;
-  const bool col_gate = p.gate != nullptr && p.gate_col != 0 && p.gate_row == 0;
-  const bool full_gate = p.gate != nullptr && p.gate_col != 0 && p.gate_row != 0;
-  for (int i = threadIdx.x; i < 3 * p.D; i += blockDim.x) sums[i] = 0.0f;
-  __syncthreads();
-  grid_dependency_wait();
-  grid_dependents_go();
-  const float inv_d = 1.0f / p.D;
-  int odd = 0;
-  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, odd ^= 1) {
-    float(*buf)[32] = row_buf[odd];
-    const X* x = static_cast<const X*>(p.x) + row * p.ldx;
-    const Y* y = static_cast<const Y*>(p.y) + row * p.ldy;
-    const X* dxo = static_cast<const X*>(p.d_x_out) + row * p.ld_d_x_out;
-    const H* dh = static_cast<const H*>(p.dh) + row * p.ld_dh;
-    float u[VPT][VEC], yv[VPT][VEC], du[VPT][VEC], hv[VPT][VEC];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int d = (i * blockDim.x + threadIdx.x) * VEC;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) u[i][e] = yv[i][e] = du[i][e] = hv[i][e] = 0.0f;
-      if (d < p.D) {
-        load_vec(x + d, u[i]);
-        if (has_y) load_vec(y + d, yv[i]);
-        if (p.d_x_out) load_vec(dxo + d, du[i]);
-        if (has_h) load_vec(dh + d, hv[i]);
-      }
-    }
-    float r2 = 1.0f;
-    if (p.w_post) {
-      float s[1] = {0.0f};
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) s[0] = fmaf(yv[i][e], yv[i][e], s[0]);
-      block_sums(s, buf[0]);
-      r2 = rsqrtf(s[0] * inv_d + p.eps);
-    }
-    auto gate_at = [&](int d, float (&g)[VEC]) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) g[e] = 1.0f;
-      if (p.gate) {
-        const float* gp = p.gate + row * p.gate_row;
-        if (p.gate_col) {
-          load_vec(gp + d, g);
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) g[e] = *gp;
-        }
-      }
-    };
-    auto vec_at = [&](const float* v, int d, float (&w)[VEC]) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) w[e] = 1.0f;
-      if (v) load_vec(v + d, w);
-    };
-    float s[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int d = (i * blockDim.x + threadIdx.x) * VEC;
-      if (d >= p.D) continue;
-      float w2[VEC], w1[VEC], g[VEC];
-      vec_at(p.w_post, d, w2);
-      vec_at(p.w_pre, d, w1);
-      gate_at(d, g);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float pe = yv[i][e] * r2 * w2[e];
-        u[i][e] = has_y ? fmaf(p.alpha, u[i][e], g[e] * pe) : p.alpha * u[i][e];
-        s[0] = fmaf(u[i][e], u[i][e], s[0]);
-        s[1] = fmaf(hv[i][e] * w1[e], u[i][e], s[1]);
-      }
-    }
-    float r1 = 0.0f, c1 = 0.0f;
-    if (has_h) {
-      block_sums(s, buf[1]);
-      r1 = rsqrtf(s[0] * inv_d + p.eps);
-      c1 = r1 * r1 * (s[1] * inv_d);
-    }
-    float t[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int d = (i * blockDim.x + threadIdx.x) * VEC;
-      if (d >= p.D) continue;
-      float w2[VEC], w1[VEC], g[VEC], o[VEC];
-      vec_at(p.w_post, d, w2);
-      vec_at(p.w_pre, d, w1);
-      gate_at(d, g);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        if (has_h) {
-          sums[p.D + d + e] += hv[i][e] * u[i][e] * r1;
-          du[i][e] = fmaf(r1, fmaf(hv[i][e], w1[e], -u[i][e] * c1), du[i][e]);
-        }
-        o[e] = p.alpha * du[i][e];
-        const float n = yv[i][e] * r2;
-        const float dp = g[e] * du[i][e];
-        if (p.w_post) sums[d + e] += dp * n;
-        if (col_gate) sums[2 * p.D + d + e] += du[i][e] * (n * w2[e]);
-        t[0] = fmaf(dp * w2[e], n, t[0]);
-        t[1] = fmaf(du[i][e], n * w2[e], t[1]);
-      }
-      store_vec(static_cast<X*>(p.dx) + row * p.ld_dx + d, o);
-      if (full_gate) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) o[e] = du[i][e] * (yv[i][e] * r2 * w2[e]);
-        store_vec(p.dgate + row * p.gate_row + d, o);
-      }
-    }
-    if (!has_y) continue;
-    float c2 = 0.0f;
-    if (p.w_post || row_gate) {
-      block_sums(t, buf[2]);
-      if (p.w_post) c2 = t[0] * inv_d;
-      if (row_gate && threadIdx.x == 0) p.dgate[row * p.gate_row] = t[1];
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int d = (i * blockDim.x + threadIdx.x) * VEC;
-      if (d >= p.D) continue;
-      float w2[VEC], g[VEC], o[VEC];
-      vec_at(p.w_post, d, w2);
-      gate_at(d, g);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        o[e] = r2 * (g[e] * du[i][e] * w2[e] - yv[i][e] * r2 * c2);
-      store_vec(p.dy + row * p.ld_dy + d, o);
-    }
-  }
-  if (partial == nullptr) return;
-  float* out = partial + static_cast<int64_t>(blockIdx.x) * 3 * p.D;
-  // every element was added to by the thread that owns its column
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int d = (i * blockDim.x + threadIdx.x) * VEC;
-    if (d >= p.D) continue;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e)
-      for (int k = 0; k < 3; ++k) out[k * p.D + d + e] = sums[k * p.D + d + e];
-  }
-}
-
 // ------------------------------------------------- gradient, rows by copies
 //
-// The gradient for rows of at most 4096 elements: one block per SM or more
-// walks the rows, and each thread copies its own 8 columns of the next rows
-// into a ring in shared memory (cp.async) while the block works on the present
-// one, so the row's sums, each a barrier, cost no memory time.  Two barriers a
-// row: the last sums of a row and the first of the next one, sum(y^2), go
-// through one.  A thread's columns are its own for all its rows: their weights
+// The gradient: one block per SM or more walks the rows, and each thread copies
+// its own 8 columns of the next rows into a ring in shared memory (cp.async)
+// while the block works on the present one, so the row's sums, each a barrier,
+// cost no memory time.  Two barriers a row: the last sums of a row and the first
+// of the next one, sum(y^2), go through one.  Rows of more than 4096 elements
+// (or of more bytes than three stages hold) are shared by the blocks of a
+// cluster, which exchange their sums through distributed shared memory.  A thread's columns are its own for all its rows: their weights
 // and their three column sums stay in registers.  Arithmetic in pairs (one
 // instruction for two FP32 operations).
 
-constexpr int kRingWidth = 4096;
+constexpr int kRingWidth = 4096;  // columns of a block
+constexpr int kMaxParts = 8;      // blocks of a cluster
 constexpr int kRingBytes = 220 * 1024;
 
 // Two FP32 numbers in one 64-bit register.
@@ -354,6 +207,25 @@ __device__ __forceinline__ void block_sums3(float (&v)[3], float* buf) {
   v[2] = __shfl_sync(0xFFFFFFFFu, a, 16);
 }
 
+// Sums of the blocks' sums over the cluster, by rank: each block leaves its own
+// in every block's `box` ([rank][4 values]).  Boxes alternate like the buffers.
+template <int N>
+__device__ __forceinline__ void cluster_sums(float (&v)[N], float* box, int parts, uint32_t rank) {
+  if (parts == 1) return;
+  if (threadIdx.x < static_cast<unsigned>(parts)) {
+    const uint32_t to = map_to_rank(smem_u32(box + rank * 4), threadIdx.x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) st_cluster_u32(to + 4 * i, __float_as_uint(v[i]));
+  }
+  __syncwarp();
+  cluster_sync();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.0f;
+  for (int r = 0; r < parts; ++r)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += box[r * 4 + i];
+}
+
 // This thread's 8 columns: adjacent (VEC, rows on 16 bytes) or blockDim.x apart.
 template <bool VEC>
 __device__ __forceinline__ int own_col(int e) {
@@ -389,7 +261,6 @@ __device__ __forceinline__ void own_store(T* row, int D, const float (&v)[8]) {
 // row's offset in its first granule (each granule holds bytes of the row).
 template <typename T, bool VEC>
 struct RingRows {
-  const T* row0;
   const uint8_t* next;    // the next row to copy (of this thread's first piece, VEC)
   int64_t stride;         // bytes from a row of this block to its next one
   int slot;               // offset in a stage
@@ -398,13 +269,15 @@ struct RingRows {
   static __host__ __device__ constexpr int bytes(int threads) {
     return threads * 8 * static_cast<int>(sizeof(T)) + (VEC ? 0 : 32);
   }
-  __device__ __forceinline__ void init(const void* base, int64_t ld, int at) {
-    row0 = static_cast<const T*>(base);
-    const T* first = row0 + blockIdx.x * ld;
-    next = reinterpret_cast<const uint8_t*>(VEC ? first + own_col<true>(0) : first);
-    stride = ld * static_cast<int64_t>(sizeof(T)) * gridDim.x;
+  // Rows first, first + step, .. of a matrix, from column col0.
+  __device__ __forceinline__ void init(const void* base, int64_t ld, int col0, int first, int step,
+                                       int at) {
+    const T* row0 = static_cast<const T*>(base) + col0;
+    const T* start = row0 + first * ld;
+    next = reinterpret_cast<const uint8_t*>(VEC ? start + own_col<true>(0) : start);
+    stride = ld * static_cast<int64_t>(sizeof(T)) * step;
     slot = at;
-    low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(base));
+    low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row0));
     ld_low = static_cast<uint32_t>(ld * sizeof(T));
   }
   __device__ __forceinline__ void copy(uint8_t* stage, int D) const {
@@ -463,37 +336,44 @@ int ring_stage_bytes(int threads, bool has_y, bool has_dxo, bool has_h, bool ful
 
 template <typename X, typename Y, typename H, bool VEC>
 __global__ void __launch_bounds__(512, 1)
-norm_gate_bwd_ring_kernel(NormArgs p, int stages, int stage_bytes, float* partial) {
+norm_gate_bwd_kernel(NormArgs p, int parts, int part_cols, int stages, int stage_bytes,
+                     float* partial) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(16) float sums[2][32 + 64];  // alternate from row to row
-  const int D = p.D, T = p.T;
+  __shared__ __align__(16) float boxes[2][2][kMaxParts * 4];
+  // this block's columns: D of them from col0
+  const uint32_t rank = parts > 1 ? cluster_ctarank() : 0u;
+  const int col0 = static_cast<int>(rank) * part_cols;
+  const int D = min(part_cols, p.D - col0), T = p.T;
+  const int slot = static_cast<int>(blockIdx.x) / parts;
   const bool has_y = p.y != nullptr, has_h = p.dh != nullptr, has_dxo = p.d_x_out != nullptr;
   const bool row_gate = p.gate != nullptr && p.gate_col == 0;
   const bool col_gate = p.gate != nullptr && p.gate_col != 0 && p.gate_row == 0;
   const bool full_gate = p.gate != nullptr && p.gate_col != 0 && p.gate_row != 0;
   for (int i = threadIdx.x; i < 2 * 96; i += blockDim.x) (&sums[0][0])[i] = 0.0f;
   __syncthreads();
+  if (parts > 1) cluster_sync();  // every block of the cluster runs
   grid_dependency_wait();
   grid_dependents_go();
 
   const int threads = blockDim.x;
+  const int step = static_cast<int>(gridDim.x) / parts;
+  int row = slot, ahead = row;
   RingRows<X, VEC> rx, ro;
   RingRows<Y, VEC> ry;
   RingRows<H, VEC> rh;
   RingRows<float, VEC> rg;
   int at = 0;
-  rx.init(p.x, p.ldx, at);
+  rx.init(p.x, p.ldx, col0, row, step, at);
   at += rx.bytes(threads);
-  ry.init(p.y, p.ldy, at);
+  ry.init(p.y, p.ldy, col0, row, step, at);
   at += has_y ? ry.bytes(threads) : 0;
-  ro.init(p.d_x_out, p.ld_d_x_out, at);
+  ro.init(p.d_x_out, p.ld_d_x_out, col0, row, step, at);
   at += has_dxo ? ro.bytes(threads) : 0;
-  rh.init(p.dh, p.ld_dh, at);
+  rh.init(p.dh, p.ld_dh, col0, row, step, at);
   at += has_h ? rh.bytes(threads) : 0;
-  rg.init(p.gate, p.gate_row, at);
+  rg.init(p.gate, p.gate_row, col0, row, step, at);
 
-  const int step = gridDim.x;
-  int row = blockIdx.x, ahead = row;
   uint8_t* fill = ring;  // the stage of row `ahead`
   uint8_t* const ring_end = ring + stages * stage_bytes;
   // A row's copies in three parts, started at different places of an earlier
@@ -541,14 +421,14 @@ norm_gate_bwd_ring_kernel(NormArgs p, int stages, int stage_bytes, float* partia
       for (int e = 0; e < 8; ++e) v[e] = 1.0f;
     pairs_of(v, w);
   };
-  weights(p.w_post, w2);
-  weights(p.w_pre, w1);
-  weights(col_gate ? p.gate : nullptr, g);
+  weights(p.w_post ? p.w_post + col0 : nullptr, w2);
+  weights(p.w_pre ? p.w_pre + col0 : nullptr, w1);
+  weights(col_gate ? p.gate + col0 : nullptr, g);
 #pragma unroll
   for (int i = 0; i < 4; ++i) gw[i] = mul2(g[i], w2[i]);
   float next_gate = row_gate && row < T ? p.gate[row * p.gate_row] : 1.0f;
   Pair sum_post[4] = {}, sum_pre[4] = {};
-  const float inv_d = 1.0f / D;
+  const float inv_d = 1.0f / p.D;
   const Pair alpha = both(p.alpha);
   auto squares = [&](const Pair (&q)[4]) {
     Pair a[2] = {0, 0};
@@ -573,6 +453,7 @@ norm_gate_bwd_ring_kernel(NormArgs p, int stages, int stage_bytes, float* partia
   if (has_y) ry.read(st, row, D, y);
   float first[2] = {squares(y), 0.0f};
   block_sums2(first, sums[1]);
+  cluster_sums(first, boxes[1][0], parts, rank);
   float r2 = scale_of(first[0]);
 
   for (int odd = 0; row < T; odd ^= 1) {
@@ -606,6 +487,7 @@ norm_gate_bwd_ring_kernel(NormArgs p, int stages, int stage_bytes, float* partia
     landed();  // the next row, before the barrier that lets others read it
     float b[2] = {sum2(b0), sum2(b1)};
     block_sums2(b, sums[odd]);
+    cluster_sums(b, boxes[odd][0], parts, rank);
     issue_grads();
     float r1 = 0.0f, c1 = 0.0f;
     if (has_h) {
@@ -627,7 +509,7 @@ norm_gate_bwd_ring_kernel(NormArgs p, int stages, int stage_bytes, float* partia
       t0[i & 1] = fma2(u[i], y[i], t0[i & 1]);
     }
     floats_of(o, v);
-    own_store<VEC>(static_cast<X*>(p.dx) + row * p.ld_dx, D, v);
+    own_store<VEC>(static_cast<X*>(p.dx) + row * p.ld_dx + col0, D, v);
     issue_rest();
     if (!row_gate && !full_gate) {
 #pragma unroll
@@ -641,7 +523,7 @@ norm_gate_bwd_ring_kernel(NormArgs p, int stages, int stage_bytes, float* partia
       }
       if (full_gate) {
         floats_of(o, v);
-        own_store<VEC>(p.dgate + row * p.gate_row, D, v);
+        own_store<VEC>(p.dgate + row * p.gate_row + col0, D, v);
       }
     }
     st += stage_bytes;
@@ -650,28 +532,30 @@ norm_gate_bwd_ring_kernel(NormArgs p, int stages, int stage_bytes, float* partia
     // always: the barrier also says that this row's stage has been read
     float t[3] = {sum2(t0), sum2(t1), squares(y_next)};
     block_sums3(t, sums[odd] + 32);
+    cluster_sums(t, boxes[odd][1], parts, rank);
     if (has_y) {
-      if (row_gate && threadIdx.x == 0) p.dgate[row * p.gate_row] = t[1];
+      if (row_gate && threadIdx.x == 0 && rank == 0) p.dgate[row * p.gate_row] = t[1];
       const Pair c2p = both(p.w_post ? -(t[0] * inv_d) * r2 : 0.0f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = fma2(y[i], c2p, mul2(u[i], r2p));
       floats_of(o, v);
-      own_store<VEC>(p.dy + row * p.ld_dy, D, v);
+      own_store<VEC>(p.dy + row * p.ld_dy + col0, D, v);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = y_next[i];
     r2 = scale_of(t[2]);
     row = more ? row + step : T;
   }
+  if (parts > 1) cluster_sync();  // no block leaves while others write its boxes
   if (partial == nullptr) return;
-  float* out = partial + static_cast<int64_t>(blockIdx.x) * 3 * D;
+  float* out = partial + static_cast<int64_t>(slot) * 3 * p.D + col0;
   auto leave = [&](const Pair (&sum)[4], float* to) {
     floats_of(sum, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (own_col<VEC>(e) < D) to[own_col<VEC>(e)] = v[e];
   };
-  leave(sum_pre, out + D);
+  leave(sum_pre, out + p.D);
   if (col_gate) {
     Pair t[4];
 #pragma unroll
@@ -679,7 +563,7 @@ norm_gate_bwd_ring_kernel(NormArgs p, int stages, int stage_bytes, float* partia
       t[i] = mul2(sum_post[i], w2[i]);
       sum_post[i] = mul2(sum_post[i], g[i]);
     }
-    leave(t, out + 2 * D);
+    leave(t, out + 2 * p.D);
   }
   leave(sum_post, out);
 }
@@ -752,83 +636,57 @@ cudaError_t forward(const NormArgs& a, cudaStream_t st) {
   return launch_pdl(norm_gate_kernel<X, Y, 8, 4>, grid, block, 0, st, a);
 }
 
-template <typename K>
-cudaError_t launch_bwd(K kernel, const NormArgs& a, const Shape& s, int slots, float* partial,
-                       cudaStream_t st) {
-  const size_t smem = 3 * sizeof(float) * a.D;
-  if (smem > 40 * 1024) {  // 48 KB with the kernel's own arrays needs the opt-in
-    const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(kernel, dim3(slots), dim3(s.threads), smem, st, a, partial);
-}
-
-// The ring kernel's launch; with `slots` null only its block count per SM is
-// taken: by shared memory, and by 512 threads an SM of at most 128 registers.
-template <typename X, typename Y, typename H, bool VEC>
-cudaError_t backward_ring(const NormArgs& a, int slots, float* partial, cudaStream_t st,
-                          int* per_sm) {
-  const int threads = threads_for(a.D, 8);
-  const bool full = a.gate != nullptr && a.gate_col != 0 && a.gate_row != 0;
-  const int stage = ring_stage_bytes<X, Y, H, VEC>(threads, a.y != nullptr, a.d_x_out != nullptr,
-                                                   a.dh != nullptr, full);
-  const int stages = 4 * stage <= kRingBytes ? 4 : 3;
-  const int smem = stages * stage;
-  if (per_sm) {
-    const int by_smem = kRingBytes / (smem + 2048), by_threads = 512 / threads;
-    *per_sm = by_smem < by_threads ? by_smem : by_threads;
-    if (*per_sm < 1) *per_sm = 1;
-    return cudaSuccess;
-  }
-  const auto kernel = norm_gate_bwd_ring_kernel<X, Y, H, VEC>;
-  if (smem > 40 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(kernel, dim3(slots), dim3(threads), smem, st, a, stages, stage,
-                    partial);
-}
-
-template <typename X, typename Y, typename H>
-cudaError_t backward(const NormArgs& a, int slots, float* partial, cudaStream_t st, int* per_sm) {
-  const Shape s = shape_for(a);
-  // (five FP32 operands of over 3700 columns take more than three stages hold)
-  const bool full = a.gate != nullptr && a.gate_col != 0 && a.gate_row != 0;
-  const int row_bytes = (sizeof(X) + sizeof(Y) + sizeof(X) + sizeof(H) + (full ? 4 : 0)) *
-                        threads_for(a.D, 8) * 8 + 5 * 32;
-  if (a.D <= kRingWidth && 3 * row_bytes <= kRingBytes)
-    return s.vec == 8 ? backward_ring<X, Y, H, true>(a, slots, partial, st, per_sm)
-                      : backward_ring<X, Y, H, false>(a, slots, partial, st, per_sm);
-  if (per_sm) {
-    *per_sm = 1;
-    return cudaSuccess;
-  }
-  if (s.vec == 1)
-    return s.vpt == 8
-               ? launch_bwd(norm_gate_bwd_kernel<X, Y, H, 1, 8>, a, s, slots, partial, st)
-               : launch_bwd(norm_gate_bwd_kernel<X, Y, H, 1, 32>, a, s, slots, partial, st);
-  if (s.vpt == 1)
-    return launch_bwd(norm_gate_bwd_kernel<X, Y, H, 8, 1>, a, s, slots, partial, st);
-  if (s.vpt == 2)
-    return launch_bwd(norm_gate_bwd_kernel<X, Y, H, 8, 2>, a, s, slots, partial, st);
-  return launch_bwd(norm_gate_bwd_kernel<X, Y, H, 8, 4>, a, s, slots, partial, st);
-}
-
-cudaError_t backward_typed(const NormArgs& a, int slots, float* partial, cudaStream_t st,
-                           int* per_sm) {
+// Calls f<X, Y, H, VEC>() for the operands' types and alignment.
+template <bool VEC, typename F>
+auto by_types(const NormArgs& a, F f) {
   using B = __nv_bfloat16;
   if (a.x_bf16)
-    return a.y_bf16 ? (a.dh_bf16 ? backward<B, B, B>(a, slots, partial, st, per_sm)
-                                 : backward<B, B, float>(a, slots, partial, st, per_sm))
-                    : (a.dh_bf16 ? backward<B, float, B>(a, slots, partial, st, per_sm)
-                                 : backward<B, float, float>(a, slots, partial, st, per_sm));
-  return a.y_bf16 ? (a.dh_bf16 ? backward<float, B, B>(a, slots, partial, st, per_sm)
-                               : backward<float, B, float>(a, slots, partial, st, per_sm))
-                  : (a.dh_bf16 ? backward<float, float, B>(a, slots, partial, st, per_sm)
-                               : backward<float, float, float>(a, slots, partial, st, per_sm));
+    return a.y_bf16 ? (a.dh_bf16 ? f.template go<B, B, B, VEC>() : f.template go<B, B, float, VEC>())
+                    : (a.dh_bf16 ? f.template go<B, float, B, VEC>()
+                                 : f.template go<B, float, float, VEC>());
+  return a.y_bf16 ? (a.dh_bf16 ? f.template go<float, B, B, VEC>()
+                               : f.template go<float, B, float, VEC>())
+                  : (a.dh_bf16 ? f.template go<float, float, B, VEC>()
+                               : f.template go<float, float, float, VEC>());
 }
+template <typename F>
+auto by_types(const NormArgs& a, F f) {
+  return vector_rows(a) ? by_types<true>(a, f) : by_types<false>(a, f);
+}
+
+void bwd_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, const NormBwdPlan& b,
+                cudaStream_t st) {
+  *cfg = cudaLaunchConfig_t{};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(b.parts);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1] = pdl_attribute();
+  cfg->gridDim = dim3(static_cast<unsigned>(b.slots * b.parts));
+  cfg->blockDim = dim3(static_cast<unsigned>(b.threads));
+  cfg->dynamicSmemBytes = static_cast<size_t>(b.stages) * b.stage_bytes;
+  cfg->stream = st;
+  cfg->attrs = attr;
+  cfg->numAttrs = 2;
+}
+
+struct BwdKernel {
+  const NormBwdPlan& b;
+  template <typename X, typename Y, typename H, bool VEC>
+  void (*go() const)(NormArgs, int, int, int, int, float*) {
+    return norm_gate_bwd_kernel<X, Y, H, VEC>;
+  }
+};
+struct BwdStage {
+  const NormArgs& a;
+  int threads;
+  template <typename X, typename Y, typename H, bool VEC>
+  int go() const {
+    const bool full = a.gate != nullptr && a.gate_col != 0 && a.gate_row != 0;
+    return ring_stage_bytes<X, Y, H, VEC>(threads, a.y != nullptr, a.d_x_out != nullptr,
+                                          a.dh != nullptr, full);
+  }
+};
 
 }  // namespace
 
@@ -841,18 +699,60 @@ cudaError_t launch_norm_gate(const NormArgs& a, cudaStream_t stream) {
   return e;
 }
 
-// As many blocks as are resident at once, so that a block's rows follow one
-// another through its ring.
-int norm_gate_bwd_slots(const NormArgs& a, const LayerDevice& dev) {
-  int per_sm = 1;
-  backward_typed(a, 0, nullptr, nullptr, &per_sm);
-  const int64_t most = static_cast<int64_t>(dev.sms) * per_sm;
-  return static_cast<int>(a.T < most ? a.T : most);
+cudaError_t norm_gate_bwd_plan(const NormArgs& a, const LayerDevice& dev, NormBwdPlan* plan) {
+  NormBwdPlan& b = *plan;
+  // The fewest blocks to a row whose columns fit their registers and whose
+  // ring holds three rows (five FP32 operands of 4096 columns take 80 KB).
+  for (int parts = (a.D + kRingWidth - 1) / kRingWidth;; ++parts) {
+    if (parts > kMaxParts) return cudaErrorInvalidValue;
+    b.part_cols = ((a.D + parts - 1) / parts + 7) / 8 * 8;
+    b.parts = (a.D + b.part_cols - 1) / b.part_cols;  // (no block without columns)
+    b.threads = threads_for(b.part_cols, 8);
+    b.stage_bytes = by_types(a, BwdStage{a, b.threads});
+    if (3 * b.stage_bytes <= kRingBytes) break;
+  }
+  b.stages = 4 * b.stage_bytes <= kRingBytes ? 4 : 3;
+  // As many as are resident at once, so that a block's rows follow one another
+  // through its ring: by shared memory, and by 512 threads an SM of at most 128
+  // registers; clusters as the occupancy calculator says.
+  const int smem = b.stages * b.stage_bytes;
+  const int by_smem = kRingBytes / (smem + 2048), by_threads = 512 / b.threads;
+  int per_sm = by_smem < by_threads ? by_smem : by_threads;
+  if (per_sm < 1) per_sm = 1;
+  int slots = dev.sms / b.parts * per_sm;
+  const auto kernel = by_types(a, BwdKernel{b});
+  if (smem > 40 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  b.slots = slots;
+  if (b.parts > 1) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    bwd_config(&cfg, attr, b, nullptr);
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (clusters < 1) return cudaErrorInvalidConfiguration;
+    if (clusters < slots) slots = clusters;
+  }
+  b.slots = a.T < slots ? a.T : slots;
+  return cudaSuccess;
 }
 
-cudaError_t launch_norm_gate_bwd(const NormArgs& a, int slots, float* partial,
+cudaError_t launch_norm_gate_bwd(const NormArgs& a, const NormBwdPlan& plan, float* partial,
                                  cudaStream_t stream) {
-  const cudaError_t e = backward_typed(a, slots, partial, stream, nullptr);
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  bwd_config(&cfg, attr, plan, stream);
+  if (plan.parts == 1) {
+    attr[0] = attr[1];  // no cluster
+    cfg.numAttrs = 1;
+  }
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, by_types(a, BwdKernel{plan}), a, plan.parts,
+                                           plan.part_cols, plan.stages, plan.stage_bytes, partial);
   if (e == cudaSuccess) note_launches(1);
   return e;
 }

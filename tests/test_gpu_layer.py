@@ -271,7 +271,8 @@ def _check_grads(got, ref, dxo, dh, xt, D):
             _close(field, w, units * size[name] + round_ * w.abs() + 1e-30, name)
 
 
-@pytest.mark.parametrize("T,D", NORM_SHAPES + [(1000, 72), (400, 4096), (1300, 4000), (1300, 2999), (9000, 40)])
+@pytest.mark.parametrize("T,D", NORM_SHAPES + [(1000, 72), (400, 4096), (1300, 4000), (1300, 2999), (9000, 40), (700, 8192),
+                                               (500, 6001), (400, 16384)])
 @pytest.mark.parametrize("xt,yt,ht", [(F32, F32, F32), (BF16, F32, F32), (BF16, BF16, BF16),
                                       (F32, BF16, BF16)])
 @pytest.mark.parametrize("gate", ["none", "channel", "row", "full"])
