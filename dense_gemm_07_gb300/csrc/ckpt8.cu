@@ -331,11 +331,11 @@ cudaError_t launch_ckpt8_unpack(int T, int N, const uint8_t* q, const uint8_t* s
   return e;
 }
 
-// The blocks of a column block: each walks the same number of panels, so that
-// about 5 blocks an SM are at work.
+// The blocks of a column block: each walks the same number of panels, with at
+// most about 8 blocks an SM.
 int ckpt8_act_grad_slots(int T, int N, const LayerDevice& dev) {
   const int64_t panels = (T + kCkptRun - 1) / kCkptRun;
-  const int64_t each = panels * column_blocks(N, 2) / (static_cast<int64_t>(dev.sms) * 5) + 1;
+  const int64_t each = panels * column_blocks(N, 2) / (static_cast<int64_t>(dev.sms) * 8) + 1;
   return static_cast<int>((panels + each - 1) / each);
 }
 

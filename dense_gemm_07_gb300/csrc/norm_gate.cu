@@ -334,7 +334,9 @@ int ring_stage_bytes(int threads, bool has_y, bool has_dxo, bool has_h, bool ful
          (full_gate ? RingRows<float, VEC>::bytes(threads) : 0);
 }
 
-template <typename X, typename Y, typename H, bool VEC>
+// ALL: every operand and both norms are there, and no gate or one value per
+// column: the row's work is then one straight piece of code.
+template <typename X, typename Y, typename H, bool VEC, bool ALL>
 __global__ void __launch_bounds__(512, 1)
 norm_gate_bwd_kernel(NormArgs p, int parts, int part_cols, int stages, int stage_bytes,
                      float* partial) {
@@ -346,10 +348,11 @@ norm_gate_bwd_kernel(NormArgs p, int parts, int part_cols, int stages, int stage
   const int col0 = static_cast<int>(rank) * part_cols;
   const int D = min(part_cols, p.D - col0), T = p.T;
   const int slot = static_cast<int>(blockIdx.x) / parts;
-  const bool has_y = p.y != nullptr, has_h = p.dh != nullptr, has_dxo = p.d_x_out != nullptr;
-  const bool row_gate = p.gate != nullptr && p.gate_col == 0;
+  const bool has_y = ALL || p.y != nullptr, has_h = ALL || p.dh != nullptr;
+  const bool has_dxo = ALL || p.d_x_out != nullptr, post = ALL || p.w_post != nullptr;
+  const bool row_gate = !ALL && p.gate != nullptr && p.gate_col == 0;
   const bool col_gate = p.gate != nullptr && p.gate_col != 0 && p.gate_row == 0;
-  const bool full_gate = p.gate != nullptr && p.gate_col != 0 && p.gate_row != 0;
+  const bool full_gate = !ALL && p.gate != nullptr && p.gate_col != 0 && p.gate_row != 0;
   for (int i = threadIdx.x; i < 2 * 96; i += blockDim.x) (&sums[0][0])[i] = 0.0f;
   __syncthreads();
   if (parts > 1) cluster_sync();  // every block of the cluster runs
@@ -436,7 +439,7 @@ norm_gate_bwd_kernel(NormArgs p, int parts, int part_cols, int stages, int stage
     for (int i = 0; i < 4; ++i) a[i & 1] = fma2(q[i], q[i], a[i & 1]);
     return sum2(a);
   };
-  auto scale_of = [&](float sum) { return p.w_post ? rsqrtf(sum * inv_d + p.eps) : 1.0f; };
+  auto scale_of = [&](float sum) { return post ? rsqrtf(sum * inv_d + p.eps) : 1.0f; };
   // The row after the present one has landed (its copies were all started one
   // row ago or, with four stages, two).
   auto landed = [&]() {
@@ -535,7 +538,7 @@ norm_gate_bwd_kernel(NormArgs p, int parts, int part_cols, int stages, int stage
     cluster_sums(t, boxes[odd][1], parts, rank);
     if (has_y) {
       if (row_gate && threadIdx.x == 0 && rank == 0) p.dgate[row * p.gate_row] = t[1];
-      const Pair c2p = both(p.w_post ? -(t[0] * inv_d) * r2 : 0.0f);
+      const Pair c2p = both(post ? -(t[0] * inv_d) * r2 : 0.0f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = fma2(y[i], c2p, mul2(u[i], r2p));
       floats_of(o, v);
@@ -671,10 +674,13 @@ void bwd_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, const NormBw
 }
 
 struct BwdKernel {
-  const NormBwdPlan& b;
+  const NormArgs& a;
   template <typename X, typename Y, typename H, bool VEC>
   void (*go() const)(NormArgs, int, int, int, int, float*) {
-    return norm_gate_bwd_kernel<X, Y, H, VEC>;
+    const bool all = a.y != nullptr && a.dh != nullptr && a.d_x_out != nullptr &&
+                     a.w_post != nullptr && (a.gate == nullptr || a.gate_row == 0);
+    if (VEC && all) return norm_gate_bwd_kernel<X, Y, H, VEC, VEC>;
+    return norm_gate_bwd_kernel<X, Y, H, VEC, false>;
   }
 };
 struct BwdStage {
@@ -720,7 +726,7 @@ cudaError_t norm_gate_bwd_plan(const NormArgs& a, const LayerDevice& dev, NormBw
   int per_sm = by_smem < by_threads ? by_smem : by_threads;
   if (per_sm < 1) per_sm = 1;
   int slots = dev.sms / b.parts * per_sm;
-  const auto kernel = by_types(a, BwdKernel{b});
+  const auto kernel = by_types(a, BwdKernel{a});
   if (smem > 40 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -751,7 +757,7 @@ cudaError_t launch_norm_gate_bwd(const NormArgs& a, const NormBwdPlan& plan, flo
     attr[0] = attr[1];  // no cluster
     cfg.numAttrs = 1;
   }
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, by_types(a, BwdKernel{plan}), a, plan.parts,
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, by_types(a, BwdKernel{a}), a, plan.parts,
                                            plan.part_cols, plan.stages, plan.stage_bytes, partial);
   if (e == cudaSuccess) note_launches(1);
   return e;
