@@ -36,12 +36,20 @@
 // or 256), a subtraction gives the whole number exactly and a multiplication by
 // the power of two its value.
 //
+// Measured: 4096 x 4096 x 11008 273 to 277 us, 1.34 PFLOP/s, 69 % of the measured
+// BF16 rate, where gemm_bf16_f32acc on X in 16 bits, without these sums, takes
+// 206; 3001 x 1000 x 3000 28 us.  In parts: without the copies of dY and the loads
+// of X, and sums of 1024 rows, 214 us; without decoding as well 185.  Adding in
+// registers costs 6.  Tried without gain: dY in 6 slices (293 us), sums of 1024
+// rows (270, left alone for their larger error), other register splits (274 to
+// 381).
+//
 // Work sharing (stream_k.cuh): whole tiles round-robin over the resident pairs;
 // the tiles of a partial last wave, with those of the last whole one, are cut
-// into equal runs of stages, one per pair.  A tile cut into segments is finished
-// by the warp that arrives last on its counter: the others have left their sums
-// in a workspace before they count, so it waits for nothing, and it adds all of
-// them in row order.
+// into equal runs of stages, one per pair, where that saves more than it costs.
+// A tile cut into segments is finished by the warp that arrives last on its
+// counter: the others have left their sums in a workspace before they count, so
+// it waits for nothing, and it adds all of them in row order.
 #include <atomic>
 #include <cstring>
 

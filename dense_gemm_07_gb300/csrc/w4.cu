@@ -6,13 +6,21 @@
 // W back as BF16.
 //
 // The product reads K * N / 2 bytes of codes once and does 2 M K N operations
-// on them, so at M <= 16 memory bounds it.  Each weight is turned into the
+// on them, so at M <= 16 memory should bound it.  Each weight is turned into the
 // exact BF16 whole number q - z and multiplied on the tensor cores
 // (mma.sync m16n8k16: 16 columns of W by 8 rows of A, FP32 sums), and the
 // scale is applied to a group's FP32 sum, so nothing is rounded to fewer bits
 // than 32 between the codes and the result.  mma.sync, not tcgen05: an operand
 // decoded in registers would have to be stored to tensor memory or shared
 // memory first, and at 16 rows the products are a small part of the time.
+//
+// Decoding takes 11 operations for 8 weights (3 shifts, 4 logic, 4 subtractions),
+// and instructions, not bytes, bound the larger calls.  Measured (inputs beyond
+// L2): 1 x 8192 x 32768, groups of 128, 33 us, 4.2 TB/s (62 % of the measured copy
+// rate); 16 x 8192 x 32768 46 us, 3.1 TB/s, with groups of 64 and zero points
+// 52 us, 2.9 TB/s; 1 x 4096 x 4096 5.4 us, mostly launch and latency.  Tried
+// without gain: shifts as high products (16 x 8192 x 32768: 46 -> 56 us), rings of
+// three and five stages (52 and 68 us against 52 with groups of 64).
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -637,8 +645,12 @@ cudaError_t launch_groups(const W4Args& a, const LayerDevice& dev, cudaStream_t 
     return two ? launch_rows<2, GPT>(a, vec_a, gx, blocks, stream)
                : launch_rows<1, GPT>(a, vec_a, gx, blocks, stream);
   }
-  // As wide as still gives every SM a block when K is cut in eight.
-  const int ct = ntiles >= 4 * dev.sms ? 4 : ntiles >= 2 * dev.sms ? 2 : 1;
+  // As wide as still gives every SM a block when K is cut in eight.  (Sixteen
+  // rows with two or four groups a step spill at four tiles: 16 x 8192 x 32768,
+  // groups of 64, takes 57 us, at two tiles 52.)
+  const int widest = a.M <= 8 || GPT == 1 ? 4 : 2;
+  int ct = ntiles >= 4 * dev.sms ? 4 : ntiles >= 2 * dev.sms ? 2 : 1;
+  if (ct > widest) ct = widest;
   const int gx = (ntiles + kWarps * ct - 1) / (kWarps * ct);
   while (blocks < 8 && gx * blocks * 2 <= 2 * dev.sms && kts >= 4 * blocks) blocks *= 2;
   if (a.M <= 8) {
@@ -646,7 +658,8 @@ cudaError_t launch_groups(const W4Args& a, const LayerDevice& dev, cudaStream_t 
     if (ct == 2) return launch_columns<2, 1, GPT>(a, vec_a, gx, blocks, stream);
     return launch_columns<1, 1, GPT>(a, vec_a, gx, blocks, stream);
   }
-  if (ct == 4) return launch_columns<4, 2, GPT>(a, vec_a, gx, blocks, stream);
+  if constexpr (GPT == 1)
+    if (ct == 4) return launch_columns<4, 2, GPT>(a, vec_a, gx, blocks, stream);
   if (ct == 2) return launch_columns<2, 2, GPT>(a, vec_a, gx, blocks, stream);
   return launch_columns<1, 2, GPT>(a, vec_a, gx, blocks, stream);
 }
