@@ -14,13 +14,16 @@
 // decoded in registers would have to be stored to tensor memory or shared
 // memory first, and at 16 rows the products are a small part of the time.
 //
-// Decoding takes 11 operations for 8 weights (3 shifts, 4 logic, 4 subtractions),
-// and instructions, not bytes, bound the larger calls.  Measured (inputs beyond
-// L2): 1 x 8192 x 32768, groups of 128, 33 us, 4.2 TB/s (62 % of the measured copy
-// rate); 16 x 8192 x 32768 46 us, 3.1 TB/s, with groups of 64 and zero points
-// 52 us, 2.9 TB/s; 1 x 4096 x 4096 5.4 us, mostly launch and latency.  Tried
-// without gain: shifts as high products (16 x 8192 x 32768: 46 -> 56 us), rings of
-// three and five stages (52 and 68 us against 52 with groups of 64).
+// Decoding takes 11 operations for 8 weights (3 shifts, 4 logic, 4 subtractions).
+// At sixteen rows no unit is full (16 x 16384 x 8192, groups of 64, counters: 1.9
+// of 4 instructions a cycle, integer pipe 35 %, tensor pipe 27 %): 16 warps an SM,
+// which 128 registers a thread allow, do not cover the latencies of decoding and
+// products.  Measured (M x K x N, inputs beyond L2): 1 x 8192 x 32768, groups of
+// 128, 33 us, 4.2 TB/s (62 % of the measured copy rate); 16 x 8192 x 32768 46 us,
+// 3.1 TB/s, with groups of 64 and zero points 52 us, 2.9 TB/s; 1 x 4096 x 4096
+// 5.4 us, mostly launch and latency.  Tried without gain: shifts as high products
+// (16 x 8192 x 32768: 46 -> 56 us), rings of three and five stages (52 and 68 us
+// against 52 with groups of 64).
 #include <cuda_bf16.h>
 
 #include "kernels.h"
