@@ -99,13 +99,13 @@ struct WarpWeights {
   int64_t tile_stride;    // from a tile to the next 16 columns
   // What a step costs besides its weights is kept small by working out here
   // what does not change from step to step.  Jobs: the granules that this lane
-  // copies (job i * 32 + lane; row 0 of its array, bytes from row to row).
-  uintptr_t row0[kMetaJobs];
-  int64_t row_bytes[kMetaJobs];
-  int job_grp[kMetaJobs];   // group of the step, or past all groups: no job
-  int job_to[kMetaJobs];    // offset in the stage
-  int job_skip[kMetaJobs];  // granules between the row's first and the job's
-  int job_len[kMetaJobs];   // bytes wanted from the row
+  // copies (job i * 32 + lane).
+  uintptr_t row0[kMetaJobs];      // the row of the job's group in step 0
+  int64_t step_bytes[kMetaJobs];  // from there to its row in the next step
+  int job_steps[kMetaJobs];       // steps in which that group lies in the matrix
+  int job_to[kMetaJobs];          // offset in the stage
+  int job_skip[kMetaJobs];        // bytes of granules between the row's first and the job's
+  int job_len[kMetaJobs];         // bytes wanted from the row (-16: no job)
   // Low address bits of the arrays' first rows: where in its granules a row
   // starts (tiles are 32 and 16 bytes apart, so all of them start alike).
   uint32_t scale_low, zero_low, scale_row, zero_row;
@@ -125,12 +125,13 @@ struct WarpWeights {
       const bool scale = piece < 3;
       const int cols = min(kW4TileN, p.N - (nt0 + c) * kW4TileN);
       const bool live = cg < CT * GPT && c < tiles && (scale || zeros);
-      row0[i] = scale ? scale0 + c * 32 : zero0 + c * 16;
-      row_bytes[i] = scale ? p.ld_scales * 2 : p.ld_zeros;
-      job_grp[i] = live ? cg % GPT : 0x40000000;
+      const int64_t row_bytes = scale ? p.ld_scales * 2 : p.ld_zeros;
+      row0[i] = (scale ? scale0 + c * 32 : zero0 + c * 16) + cg % GPT * row_bytes;
+      step_bytes[i] = GPT * row_bytes;
+      job_steps[i] = (G - cg % GPT + GPT - 1) / GPT;
       job_to[i] = CT * kW4TileBytes + cg * kMetaBytes + piece * 16;
       job_skip[i] = (scale ? piece : piece - 3) * 16;
-      job_len[i] = scale ? cols * 2 : cols;
+      job_len[i] = !live ? -16 : scale ? cols * 2 : cols;
     }
     scale_row = static_cast<uint32_t>(p.ld_scales * 2);
     zero_row = static_cast<uint32_t>(p.ld_zeros);
@@ -138,9 +139,8 @@ struct WarpWeights {
     zero_low = static_cast<uint32_t>(zero0);
   }
 
-  // Zeroes the group words of this warp's stages: a group past the matrix is
-  // then multiplied by 0 or by an earlier group's scale of the column, never by
-  // what shared memory held before (its products are 0: A is 0 past K).
+  // Zeroes the group words of this warp's stages: nothing is copied to those of
+  // columns past the matrix, and they are read (for sums that are never written).
   __device__ __forceinline__ void clear(uint8_t* ring, int stages, int stage_bytes) const {
     for (int s = 0; s < stages; ++s)
       for (int i = lane; i < CT * GPT * kMetaBytes / 16; i += 32)
@@ -149,7 +149,11 @@ struct WarpWeights {
     __syncwarp();
   }
 
-  // Starts the copies of step kt into a stage; the caller commits.
+  // Starts the copies of step kt into a stage; the caller commits.  A group past
+  // the matrix gets the scale 0: A and its products are 0 past K, but 0 times what
+  // the stage held before need not be.  (The row of an earlier step that started
+  // elsewhere in its granules has the scales of other columns, or the gap between
+  // two rows, in the same place, and its own column's may be infinite.)
   __device__ __forceinline__ void copy(uint8_t* stage, int kt) const {
     const uint8_t* from = src + static_cast<int64_t>(kt) * kW4TileBytes;
     uint8_t* to = stage + lane * 16;
@@ -161,11 +165,13 @@ struct WarpWeights {
       }
 #pragma unroll
     for (int i = 0; i < kMetaJobs; ++i) {
-      const int grp = kt * GPT + job_grp[i];
-      const uintptr_t at = row0[i] + grp * row_bytes[i];
+      const uintptr_t at = row0[i] + kt * step_bytes[i];
       const int skip = job_skip[i] - static_cast<int>(at & 15u);
-      if (grp < G && skip < job_len[i])
-        cp_async_16(stage + job_to[i], reinterpret_cast<const void*>(at + skip));
+      if (skip < job_len[i]) {
+        const bool there = GPT == 1 || kt < job_steps[i];  // (one group a step: all are)
+        cp_async_16(stage + job_to[i], there ? reinterpret_cast<const void*>(at + skip) : from,
+                    there ? 16u : 0u);
+      }
     }
   }
 

@@ -1,0 +1,44 @@
+"""Corners of the layer operators that their plain sizes do not reach: the tile
+variants of large matrices, poisoned neighbours, reused stages of a ring, calls
+after a bounded wait ran out, outputs in place of inputs.
+
+Sizes are chosen for a device of 152 SMs (the variants go by the SM count)."""
+import pytest
+import torch
+
+import dense_gemm_07_gb300 as g7
+from test_gpu_layer import _strided, _w4_case
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+# ---------------------------------------------------------------- 4-bit weights
+
+# K ends in the first group of its last 128 rows, and a warp's ring comes round
+# to a stage that held groups of the matrix.
+@pytest.mark.parametrize("M,K,N,group", [
+    (1, 8256, 9729, 64), (2, 8256, 5001, 64), (4, 8225, 5001, 32), (3, 8225, 9729, 32),
+    (8, 8256, 9729, 64), (5, 320, 9729, 64), (7, 8225, 9729, 32), (6, 8256, 5001, 64),
+    (16, 8256, 5001, 64), (16, 8225, 5001, 32), (12, 2112, 401, 64)])
+def test_w4_groups_past_the_matrix_add_nothing(M, K, N, group):
+    """The groups that fill up the last 128 rows weigh nothing, whatever scales a
+    column's neighbours, its other groups or the gaps between rows hold: a column
+    of NaN scales is NaN and changes no other, one of infinite scales (positive
+    products) is infinite."""
+    a, codes, scales, _ = _w4_case(M + K, M, K, N, group, False)
+    a = a.abs() + 1.0
+    nan, inf = N // 3, N - 2
+    codes[:, inf] = 15
+    packed = g7.w4_pack(codes)
+    clean = g7.gemm_w4(a, packed, scales, group=group)
+    poisoned = scales.clone()
+    poisoned[:, nan] = float("nan")
+    poisoned[:, inf] = float("inf")
+    # rows an odd number of elements apart, NaN between them
+    out = g7.gemm_w4(a, packed, _strided(poisoned, 2), group=group)
+    assert bool(out[:, nan].isnan().all())
+    assert bool((out[:, inf] == float("inf")).all())
+    rest = [c for c in range(N) if c not in (nan, inf)]
+    assert torch.equal(out[:, rest], clean[:, rest])
