@@ -548,9 +548,10 @@ norm_gate_bwd_kernel(NormArgs p, int parts, int part_cols, int stages, int stage
     cluster_sums(t, boxes[odd][1], parts, rank);
     if (has_y) {
       if (row_gate && threadIdx.x == 0 && rank == 0) p.dgate[row * p.gate_row] = t[1];
-      const Pair c2p = both(post ? -(t[0] * inv_d) * r2 : 0.0f);
+      const Pair c2p = both(-(t[0] * inv_d) * r2);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = fma2(y[i], c2p, mul2(u[i], r2p));
+      for (int i = 0; i < 4; ++i)  // without w_post dy = gate du: 0 times y need not be 0
+        o[i] = post ? fma2(y[i], c2p, mul2(u[i], r2p)) : u[i];
       floats_of(o, v);
       own_store<VEC>(p.dy + row * p.ld_dy + col0, D, v);
     }

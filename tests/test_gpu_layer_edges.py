@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import dense_gemm_07_gb300 as g7
-from test_gpu_layer import _strided, _w4_case
+from test_gpu_layer import _gen, _norm_case, _randn, _strided, _w4_case
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,21 @@ def test_w4_groups_past_the_matrix_add_nothing(M, K, N, group):
     assert bool((out[:, inf] == float("inf")).all())
     rest = [c for c in range(N) if c not in (nan, inf)]
     assert torch.equal(out[:, rest], clean[:, rest])
+
+
+# ------------------------------------------------------------------- norms
+
+@pytest.mark.parametrize("D", [77, 520, 5000])
+@pytest.mark.parametrize("gate", ["none", "channel", "row", "full"])
+def test_norm_gate_bwd_without_norms_does_not_look_at_y(D, gate):
+    """Without post norm and pre norm dy = gate * d_x_out: a value of y that is not
+    finite stays out of it."""
+    T = 6
+    c = _norm_case(D, T, D, F32, F32, gate, post=False, pre=False)
+    w = _randn(_gen(D), T, D)
+    want = g7.gemm_norm_gate_bwd(**c, d_x_out=w)
+    c["y"][1, 3], c["y"][4, D - 1] = float("inf"), float("nan")
+    got = g7.gemm_norm_gate_bwd(**c, d_x_out=w)
+    assert torch.equal(got.dy, want.dy) and torch.equal(got.dx, want.dx)
+    gates = torch.ones((), device="cuda") if c["gate"] is None else c["gate"]
+    assert torch.equal(got.dy, (gates * w).to(BF16))
