@@ -4,6 +4,7 @@
 // translation units.  Not installed; not part of the ABI.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -41,6 +42,23 @@ gemm_status_t layer_from_cuda(cudaError_t e);
 gemm_status_t layer_ckpt8_wgrad(int64_t T, int64_t K, int64_t N, const uint8_t* q,
                                 const uint8_t* scales, const uint16_t* dY, int64_t ld_dy,
                                 float* dW, int64_t ldw, float beta, cudaStream_t stream);
+
+// Lets `kernel` ask for up to `most` bytes of dynamic shared memory on the current
+// device.  The limit belongs to the kernel, not to a launch: it is set once, to the
+// largest size of any call, and never lowered under another thread's launch.
+// `done`: a bit per device (api.cu admits 64), one word per kernel.
+template <typename... P>
+cudaError_t allow_shared(void (*kernel)(P...), size_t most, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(most));
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // ---- element access shared by the kernels
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }

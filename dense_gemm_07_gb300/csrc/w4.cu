@@ -595,11 +595,6 @@ int blocks_for(int64_t total, int threads) {
 
 cudaError_t launch_cluster(void (*kernel)(W4Args, int), const W4Args& a, bool vec_a, int gx,
                            int gy, int blocks, size_t smem, cudaStream_t stream) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0] = pdl_attribute();
@@ -622,23 +617,31 @@ size_t larger(size_t a, size_t b) { return a > b ? a : b; }
 template <int CT, int GPT>
 cudaError_t launch_rows(const W4Args& a, bool vec_a, int gx, int blocks, cudaStream_t stream) {
   constexpr int STAGES = 4;
-  const int rows = a.M < 8 ? a.M : 8;
-  const size_t smem =
-      larger(static_cast<size_t>(kWarps) * STAGES * (WarpWeights<CT, GPT>::kStageBytes + rows * 256),
-             sizeof(float) * kWarps * CT * 16 * 9);
-  return launch_cluster(w4_rows_kernel<CT, GPT, STAGES>, a, vec_a, gx, (a.M + 7) / 8, blocks,
-                        smem, stream);
+  static std::atomic<uint64_t> allowed{0};
+  auto smem = [](int rows) {
+    return larger(
+        static_cast<size_t>(kWarps) * STAGES * (WarpWeights<CT, GPT>::kStageBytes + rows * 256),
+        sizeof(float) * kWarps * CT * 16 * 9);
+  };
+  const auto kernel = w4_rows_kernel<CT, GPT, STAGES>;
+  const cudaError_t e = allow_shared(kernel, smem(8), &allowed);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(kernel, a, vec_a, gx, (a.M + 7) / 8, blocks, smem(a.M < 8 ? a.M : 8),
+                        stream);
 }
 
 template <int CT, int NT, int GPT>
 cudaError_t launch_columns(const W4Args& a, bool vec_a, int gx, int blocks, cudaStream_t stream) {
   constexpr int STAGES = CT == 4 ? 2 : 4;
+  static std::atomic<uint64_t> allowed{0};
   const size_t smem =
       larger(static_cast<size_t>(2) * 8 * NT * kPhaseRow +
                  static_cast<size_t>(kWarps) * STAGES * WarpWeights<CT, GPT>::kStageBytes,
              sizeof(float) * 8 * NT * (kWarps * CT * 16 + 4));
-  return launch_cluster(w4_columns_kernel<CT, NT, GPT, STAGES>, a, vec_a, gx,
-                        (a.M + 8 * NT - 1) / (8 * NT), blocks, smem, stream);
+  const auto kernel = w4_columns_kernel<CT, NT, GPT, STAGES>;
+  const cudaError_t e = allow_shared(kernel, smem, &allowed);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(kernel, a, vec_a, gx, (a.M + 8 * NT - 1) / (8 * NT), blocks, smem, stream);
 }
 
 template <int GPT>
