@@ -684,14 +684,19 @@ void bwd_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, const NormBw
   cfg->numAttrs = 2;
 }
 
+using BwdFunction = void (*)(NormArgs, int, int, int, int, float*);
+// The kernel for these operands, with leave to use the whole ring.
 struct BwdKernel {
   const NormArgs& a;
+  BwdFunction* kernel;
   template <typename X, typename Y, typename H, bool VEC>
-  void (*go() const)(NormArgs, int, int, int, int, float*) {
+  cudaError_t go() const {
     const bool all = a.y != nullptr && a.dh != nullptr && a.d_x_out != nullptr &&
                      a.w_post != nullptr && (a.gate == nullptr || a.gate_row == 0);
-    if (VEC && all) return norm_gate_bwd_kernel<X, Y, H, VEC, VEC>;
-    return norm_gate_bwd_kernel<X, Y, H, VEC, false>;
+    static std::atomic<uint64_t> allowed[2] = {};
+    *kernel = VEC && all ? norm_gate_bwd_kernel<X, Y, H, VEC, VEC>
+                         : norm_gate_bwd_kernel<X, Y, H, VEC, false>;
+    return allow_shared(*kernel, kRingBytes, &allowed[VEC && all]);
   }
 };
 struct BwdStage {
@@ -737,12 +742,6 @@ cudaError_t norm_gate_bwd_plan(const NormArgs& a, const LayerDevice& dev, NormBw
   int per_sm = by_smem < by_threads ? by_smem : by_threads;
   if (per_sm < 1) per_sm = 1;
   int slots = dev.sms / b.parts * per_sm;
-  const auto kernel = by_types(a, BwdKernel{a});
-  if (smem > 40 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
   b.slots = slots;
   if (b.parts > 1) {
     cudaLaunchConfig_t cfg;
@@ -750,7 +749,9 @@ cudaError_t norm_gate_bwd_plan(const NormArgs& a, const LayerDevice& dev, NormBw
     bwd_config(&cfg, attr, b, nullptr);
     cfg.numAttrs = 1;
     int clusters = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+    BwdFunction kernel = nullptr;
+    cudaError_t e = by_types(a, BwdKernel{a, &kernel});
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
     if (e != cudaSuccess) return e;
     if (clusters < 1) return cudaErrorInvalidConfiguration;
     if (clusters < slots) slots = clusters;
@@ -768,8 +769,11 @@ cudaError_t launch_norm_gate_bwd(const NormArgs& a, const NormBwdPlan& plan, flo
     attr[0] = attr[1];  // no cluster
     cfg.numAttrs = 1;
   }
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, by_types(a, BwdKernel{a}), a, plan.parts,
-                                           plan.part_cols, plan.stages, plan.stage_bytes, partial);
+  BwdFunction kernel = nullptr;
+  cudaError_t e = by_types(a, BwdKernel{a, &kernel});
+  if (e == cudaSuccess)
+    e = cudaLaunchKernelEx(&cfg, kernel, a, plan.parts, plan.part_cols, plan.stages,
+                           plan.stage_bytes, partial);
   if (e == cudaSuccess) note_launches(1);
   return e;
 }

@@ -10,10 +10,11 @@ import torch
 
 import dense_gemm_07_gb300 as g7
 from dense_gemm_07_gb300 import _abi
-from test_gpu_layer import _w4_case
+from test_gpu_layer import _gen, _norm_case, _randn, _w4_case
 
 pytestmark = pytest.mark.gpu
 
+F32 = torch.float32
 REPS = 1500
 
 
@@ -60,3 +61,28 @@ def test_w4_of_unlike_rows_from_host_threads():
     for out, want in zip(outs, wants):
         assert torch.equal(out, want)
 
+
+def test_norm_gradients_of_unlike_widths_from_host_threads():
+    calls, outs, wants = [], [], []
+    for D in (1024, 2048, 3000, 4096):
+        T = 8
+        c = _norm_case(D, T, D, F32, F32, "full")
+        dxo, dh = _randn(_gen(D), T, D), _randn(_gen(D + 1), T, D)
+        wants.append(g7.gemm_norm_gate_bwd(**c, d_x_out=dxo, d_h=dh))
+        out = g7.NormGateGrads(*[torch.zeros_like(t) for t in wants[-1]])
+        args = _abi.GemmNormGateArgs(
+            T, D, c["x"].data_ptr(), D, _abi.TYPE_F32, c["y"].data_ptr(), D, _abi.TYPE_F32,
+            c["weight_post"].data_ptr(), c["gate"].data_ptr(), D, _abi.GATE_FULL,
+            c["weight_pre"].data_ptr(), 1.0, 1e-6)
+        grads = _abi.GemmNormGateGrads(
+            dxo.data_ptr(), D, dh.data_ptr(), D, _abi.TYPE_F32, out.dx.data_ptr(), D,
+            out.dy.data_ptr(), D, out.dgate.data_ptr(), out.dweight_post.data_ptr(),
+            out.dweight_pre.data_ptr())
+
+        def call(stream, args=args, grads=grads, keep=(c, dxo, dh)):
+            return _abi.gemm_norm_gate_bwd(args, grads, stream)
+        calls.append(call)
+        outs.append(out)
+    _together(calls)
+    for out, want in zip(outs, wants):
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
