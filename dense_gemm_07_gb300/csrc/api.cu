@@ -1322,7 +1322,7 @@ int64_t gemm_pair_units(int64_t M, int64_t N, int64_t K, int32_t max_pairs,
 }
 
 gemm_status_t gemm_debug_inject(int mode, uint64_t wait_ns) {
-  if (mode < 0 || mode > 1) return GEMM_ERR_INVALID_ARG;
+  if (mode < 0 || mode > 2) return GEMM_ERR_INVALID_ARG;
   DeviceState* d = nullptr;
   const gemm_status_t s = device_state(&d);
   if (s != GEMM_OK) return s;

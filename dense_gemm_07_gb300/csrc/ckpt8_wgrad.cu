@@ -49,7 +49,9 @@
 // into equal runs of stages, one per pair, where that saves more than it costs.
 // A tile cut into segments is finished by the warp that arrives last on its
 // counter: the others have left their sums in a workspace before they count, so
-// it waits for nothing, and it adds all of them in row order.
+// it waits for nothing, and it adds all of them in row order.  (A pair whose
+// bounded wait ran out counts its segments without summing them: the counters are
+// at zero after every launch, and a later call finds no trace of it.)
 #include <atomic>
 #include <cstring>
 
@@ -249,7 +251,9 @@ ckpt8_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constan
     regs_dec<kRegsCopy>();
     if (warp == 0 && lane == 0) {
       // ------------------------------------------------------- copies of dY
-      const bool skip = p.status[1] == 1;  // test fault: the first stage is never copied
+      // test faults: the first stage is never copied (2: by the first pair alone)
+      const unsigned int fault = p.status[1];
+      const bool skip = fault == 1 || (fault == 2 && pair == 0);
       Ring ring;
       int last[STAGES];
       for (int s = 0; s < STAGES; ++s) last[s] = -1;
@@ -434,6 +438,9 @@ ckpt8_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constan
     it.init(sched, pair);
     WorkUnit w;
     bool ok = true;
+    auto counter = [&]() {  // of the unit's tile
+      return p.counters + (static_cast<int64_t>(w.tile - sched.dp_tiles) * 2 + rank) * EPI_WARPS + ew;
+    };
     while (ok && it.next(sched, pairs, w)) {
       float sum[128];
 #pragma unroll
@@ -475,12 +482,10 @@ ckpt8_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constan
         for (int i = 0; i < 128; ++i) mine[i * 32] = sum[i];
         __threadfence();
         __syncwarp();
-        unsigned int* counter =
-            p.counters + (static_cast<int64_t>(w.tile - sched.dp_tiles) * 2 + rank) * EPI_WARPS + ew;
         unsigned int before = 0;
         if (lane == 0) {
-          before = atomicAdd(counter, 1u);
-          if (before + 1 == static_cast<unsigned int>(st.nseg)) *counter = 0u;  // for the next launch
+          before = atomicAdd(counter(), 1u);
+          if (before + 1 == static_cast<unsigned int>(st.nseg)) *counter() = 0u;  // for the next launch
         }
         before = __shfl_sync(0xFFFFFFFFu, before, 0);
         __threadfence();
@@ -554,7 +559,16 @@ ckpt8_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constan
         }
       }
     }
-    if (!ok && lane == 0) give_up(abort, peer_abort, p.status);
+    if (!ok && lane == 0) {
+      give_up(abort, peer_abort, p.status);
+      // The segments left are not summed, but they count all the same, so that
+      // the counters are at zero after this launch too.
+      do {
+        if (w.k0 == 0 && w.k1 == sched.num_kb) continue;
+        if (atomicAdd(counter(), 1u) + 1 == static_cast<unsigned int>(sk_tile(sched, w.tile).nseg))
+          *counter() = 0u;
+      } while (it.next(sched, pairs, w));
+    }
     if (lane == 0) bulk_wait_all();  // every store has completed before the CTA exits
   }
 

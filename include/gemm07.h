@@ -258,7 +258,10 @@ GEMM07_API gemm_status_t gemm_get_device_status(void *stream);
  *            cluster paths, M == 1 included) withhold the copy of their first k-slice
  *            (first stage), so a bounded wait runs out: the kernels unwind,
  *            return, and gemm_get_device_status() reports GEMM_ERR_TIMEOUT
- *            (C is then incomplete).  Nothing faults, traps or hangs.
+ *            (C is then incomplete).  Nothing faults, traps or hangs.  The
+ *            weight gradient gemm_ckpt8_wgrad does the same.
+ *   mode 2:  as 1, but only the first pair of SMs of gemm_ckpt8_wgrad
+ *            withholds its copy: the others finish their shares.
  * Returns GEMM_ERR_INVALID_ARG for an unknown mode.  Not for production use.
  */
 GEMM07_API gemm_status_t gemm_debug_inject(int mode, uint64_t wait_ns);

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import dense_gemm_07_gb300 as g7
+from dense_gemm_07_gb300 import _abi
 from test_gpu_layer import _gen, _norm_case, _randn, _strided, _w4_case
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +61,42 @@ def test_norm_gate_bwd_without_norms_does_not_look_at_y(D, gate):
     assert torch.equal(got.dy, want.dy) and torch.equal(got.dx, want.dx)
     gates = torch.ones((), device="cuda") if c["gate"] is None else c["gate"]
     assert torch.equal(got.dy, (gates * w).to(BF16))
+
+
+# ------------------------------------------------- 8-bit weight gradient
+
+def _whole(seed, T, K, N):
+    """A checkpoint of whole numbers (step 1), a dY and their exact gradient (every
+    sum stays below 2^24)."""
+    g = _gen(seed)
+    x = torch.randint(-8, 9, (T, K), generator=g, device="cuda").float()
+    x[::32] = 127.0
+    dy = torch.randint(-3, 4, (T, N), generator=g, device="cuda").to(BF16)
+    return g7.gemm_ckpt8_pack(x), dy, x.double().t() @ dy.double()
+
+
+# one tile in two parts; tiles in two and three parts; more tiles than pairs, whose
+# parts are summed one early and one late in the launch
+@pytest.mark.parametrize("T,K,N", [(4096, 128, 256), (3328, 1000, 3001), (4096, 2816, 2048)])
+def test_calls_after_one_pair_gave_up_are_exact(T, K, N):
+    """One pair's first copy is withheld: it gives up, and the pairs that share
+    its tiles have counted their parts.  The calls after it find no trace of that,
+    nor does the gradient through an activation, which counts in the same words."""
+    first, second = _whole(1, T, K, N), _whole(2, T, K, N)
+    z = [_randn(_gen(s), 512, 8192) for s in (3, 4)]
+    kept = [g7.gemm_ckpt8_pack(v) for v in z]
+    dbias = [g7.gemm_ckpt8_act_grad(v, k, "relu")[1] for v, k in zip(z, kept)]
+    for after in ("wgrad", "act_grad"):
+        assert torch.equal(g7.gemm_ckpt8_wgrad(*first[:2]).double(), first[2])
+        try:
+            assert _abi.gemm_debug_inject(2, 2_000_000) == _abi.GEMM_OK
+            g7.gemm_ckpt8_wgrad(*first[:2])
+            assert g7.gemm_get_device_status() == _abi.GEMM_ERR_TIMEOUT
+        finally:
+            assert _abi.gemm_debug_inject(0, 0) == _abi.GEMM_OK
+        for i in range(2):
+            if after == "act_grad":
+                assert torch.equal(g7.gemm_ckpt8_act_grad(z[i], kept[i], "relu")[1], dbias[i])
+            x, dy, want = (second, first)[i]
+            assert torch.equal(g7.gemm_ckpt8_wgrad(x, dy).double(), want)
+    assert g7.gemm_get_device_status() == _abi.GEMM_OK
