@@ -136,7 +136,7 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
     with _lock:
         if _lib is None:
             if build_if_missing:
-                path = _build.build()
+                path = _build.build_library()
             else:
                 path = _build.LIB_PATH
             try:

@@ -16,15 +16,13 @@ from typing import NamedTuple
 
 import torch
 
-from . import _abi as abi
 from . import _build
 
 
 @functools.lru_cache(maxsize=None)
 def _binding():
     """The compiled binding (built first if needed); there is no other path."""
-    abi.lib()
-    loader = importlib.machinery.ExtensionFileLoader("layer_binding", _build.BINDING_PATH)
+    loader = importlib.machinery.ExtensionFileLoader("layer_binding", _build.build_binding())
     spec = importlib.util.spec_from_loader("layer_binding", loader)
     module = importlib.util.module_from_spec(spec)
     loader.exec_module(module)
