@@ -8,7 +8,9 @@ the host compiler against the installed torch into ``_lib/layer_binding.so``,
 which is linked to the library.  The library needs no torch, and is all that
 the C entry points and the ctypes layer load.
 
-A rebuild of either happens only when one of its sources or headers is newer.
+A rebuild of either happens only when one of its sources or headers is newer,
+and of the binding also when the installed torch or Python is another one than
+it was compiled against (recorded beside it).
 """
 from __future__ import annotations
 
@@ -28,6 +30,7 @@ LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libgemm07.so")
 BINDING_SRC = os.path.join(CSRC, "layer_binding.cpp")
 BINDING_PATH = os.path.join(LIB_DIR, "layer_binding.so")
+BINDING_STAMP = os.path.join(LIB_DIR, "layer_binding.txt")  # what it was compiled against
 HEADER = os.path.join(ROOT, "include", "gemm07.h")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -75,8 +78,25 @@ def _torch_dir() -> str | None:
     return d if os.path.exists(os.path.join(d, "lib", "libc10_cuda.so")) else None
 
 
+def _torch_version(torch_dir: str) -> str:
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        return f.read()
+
+
+def _binding_stamp(torch_dir: str) -> str:
+    return "\n".join([torch_dir, sysconfig.get_config_var("SOABI") or "",
+                      _torch_version(torch_dir)])
+
+
 def binding_up_to_date() -> bool:
-    return _newer(BINDING_PATH, [BINDING_SRC, HEADER, __file__])
+    d = _torch_dir()
+    if d is None or not _newer(BINDING_PATH, [BINDING_SRC, HEADER, __file__]):
+        return False
+    try:
+        with open(BINDING_STAMP) as f:
+            return f.read() == _binding_stamp(d)
+    except FileNotFoundError:
+        return False
 
 
 def _run(cmd, what, verbose=False):
@@ -131,6 +151,8 @@ def _link_binding(torch_dir: str, obj: str) -> None:
           "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN",
           f"-Wl,-rpath,{libs}"], "linking layer_binding.so")
     os.replace(tmp, BINDING_PATH)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_binding_stamp(torch_dir))
 
 
 def build_binding(force: bool = False) -> str:

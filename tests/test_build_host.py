@@ -1,5 +1,5 @@
 """What is built when, with compilers that only record their command: the library
-by itself where there is no torch."""
+by itself where there is no torch, the binding again for another torch."""
 import os
 import sys
 
@@ -22,7 +22,8 @@ def commands(tmp_path, monkeypatch):
     monkeypatch.setattr(_build.subprocess, "run", run)
     monkeypatch.setattr(_build, "_nvcc", lambda: os.path.join("cuda", "bin", "nvcc"))
     for name, value in (("BUILD_DIR", "b"), ("LIB_DIR", "l"), ("LIB_PATH", "l/libgemm07.so"),
-                        ("BINDING_PATH", "l/layer_binding.so")):
+                        ("BINDING_PATH", "l/layer_binding.so"),
+                        ("BINDING_STAMP", "l/layer_binding.txt")):
         monkeypatch.setattr(_build, name, str(tmp_path / value))
     return ran
 
@@ -44,7 +45,7 @@ def test_the_library_builds_without_torch(commands, monkeypatch):
         _build.build_binding()
 
 
-def test_the_binding_is_built_with_the_library(commands):
+def test_the_binding_is_built_with_the_library_and_again_for_another_torch(commands, monkeypatch):
     pytest.importorskip("torch")
     if _build._torch_dir() is None:
         pytest.skip("torch without CUDA")
@@ -55,6 +56,13 @@ def test_the_binding_is_built_with_the_library(commands):
     _build.build()
     _build.build_binding()
     assert not commands
+    for change in (("_torch_version", lambda d: "another"), ("_torch_dir", lambda: str(os.sep))):
+        monkeypatch.setattr(_build, *change)
+        _build.build()
+        assert _compilers(commands) == {"g++"} and len(commands) == 2  # compiled and linked
+        commands.clear()
+        _build.build_binding()
+        assert not commands
 
 
 def test_the_ctypes_layer_asks_for_the_library_alone(commands):
