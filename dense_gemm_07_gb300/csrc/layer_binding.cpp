@@ -272,8 +272,12 @@ gemm_norm_gate_args_t norm_args(const Tensor& x, const Maybe& y, const Maybe& we
       a.gate_mode = GEMM_GATE_CHANNEL;
     else
       bad_value("gate must be D values, T x 1 or T x D");
-    if (gate->scalar_type() != at::kFloat || gate->device() != device || !gate->is_contiguous())
-      bad_value("gate must be contiguous float32 on " + device.str());
+    if (gate->scalar_type() != at::kFloat || gate->device() != device)
+      bad_value("gate must be float32 on " + device.str());
+    if (a.gate_mode == GEMM_GATE_FULL)
+      a.ld_gate = matrix(*gate, "gate", {at::kFloat}, device);
+    else if (!gate->is_contiguous())
+      bad_value("a gate per channel or per row must be contiguous");
     a.gate = ptr<float>(*gate);
   }
   a.alpha = static_cast<float>(scale);
@@ -323,6 +327,8 @@ std::tuple<Tensor, Maybe, Maybe, Maybe, Maybe> norm_gate_bwd(
   if (y) dy = empty({a.T, a.D}, at::kBFloat16, device);
   if (weight_post) dw_post = empty({a.D}, at::kFloat, device);
   if (gate) dgate = empty(gate->sizes(), at::kFloat, device);
+  if (a.gate_mode == GEMM_GATE_FULL && a.ld_gate > a.D)  // dgate has the gate's row stride
+    dgate = empty({a.T, a.ld_gate}, at::kFloat, device).narrow(1, 0, a.D);
   if (weight_pre) dw_pre = empty({a.D}, at::kFloat, device);
   g.dx = ptr(dx);
   g.dy = ptr<uint16_t>(dy);

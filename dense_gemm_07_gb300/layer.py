@@ -76,8 +76,8 @@ def gemm_norm_gate(x, y=None, weight_post=None, gate=None, weight_pre=None,
         h     = x_out / rms(x_out) * weight_pre
 
     x, y: T x D, float32 or bfloat16 each (y: a block's output, None for none).
-    gate: float32, one value per channel (D), per row (T x 1) or per element
-    (T x D).  x_out has x's type and may be x; h is bfloat16, or None without
+    gate: float32, one value per channel (D), per row (T x 1; both contiguous) or
+    per element (T x D).  x_out has x's type and may be x; h is bfloat16, or None without
     weight_pre."""
     return _binding().norm_gate(x, y, weight_post, gate, weight_pre, residual_scale, eps, x_out, h,
                                 _handle(stream))
@@ -98,7 +98,7 @@ def gemm_norm_gate_bwd(x, y=None, d_x_out=None, d_h=None, weight_post=None, gate
 
     d_x_out (x's type) may be None; d_h (float32 or bfloat16) is needed with
     weight_pre.  dx has x's type, dy is bfloat16 (the operand of the gradient
-    GEMMs), the others are float32."""
+    GEMMs), the others are float32; dgate has the shape and the row stride of gate."""
     return NormGateGrads(*_binding().norm_gate_bwd(x, y, d_x_out, d_h, weight_post, gate,
                                                    weight_pre, residual_scale, eps,
                                                    _handle(stream)))

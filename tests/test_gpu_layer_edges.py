@@ -8,7 +8,8 @@ import torch
 
 import dense_gemm_07_gb300 as g7
 from dense_gemm_07_gb300 import _abi
-from test_gpu_layer import _gen, _norm_case, _randn, _strided, _w4_case
+from test_gpu_layer import (_check_grads, _gen, _norm_case, _norm_ref, _randn, _strided,
+                            _w4_case)
 
 pytestmark = pytest.mark.gpu
 
@@ -61,6 +62,35 @@ def test_norm_gate_bwd_without_norms_does_not_look_at_y(D, gate):
     assert torch.equal(got.dy, want.dy) and torch.equal(got.dx, want.dx)
     gates = torch.ones((), device="cuda") if c["gate"] is None else c["gate"]
     assert torch.equal(got.dy, (gates * w).to(BF16))
+
+
+@pytest.mark.parametrize("T,D,extra", [(9, 520, 8), (9, 520, 3), (5, 77, 1), (1, 64, 5), (6, 1, 2),
+                                       (3, 5000, 16)])
+def test_norm_gate_takes_a_gate_of_any_row_stride(T, D, extra):
+    """A gate per element is a matrix like the others; its gradient has its shape."""
+    c = _norm_case(D, T, D, BF16, F32, "full")
+    dxo, dh = _randn(_gen(1), T, D, dtype=BF16), _randn(_gen(2), T, D)
+    s = dict(c, gate=_strided(c["gate"], extra))
+    # (rows off the 16-byte grid are summed in another order: half a unit of BF16)
+    for got, want in zip(g7.gemm_norm_gate(**s), g7.gemm_norm_gate(**c)):
+        assert torch.allclose(got.float(), want.float(), rtol=2.0 ** -7, atol=1e-6)
+    got = g7.gemm_norm_gate_bwd(**s, d_x_out=dxo, d_h=dh)
+    want = g7.gemm_norm_gate_bwd(**c, d_x_out=dxo, d_h=dh)
+    assert got.dgate.shape == (T, D)
+    ref = _norm_ref(c, 1.0, 1e-6)
+    _check_grads(got, ref, dxo, dh, BF16, D)
+    _check_grads(want, ref, dxo, dh, BF16, D)
+
+
+def test_norm_gate_refuses_gates_with_gaps_or_overlaps():
+    c = _norm_case(1, 5, 16, F32, F32, "none")
+    for gate in (torch.ones((16, 2), device="cuda")[:, 0],       # per channel, every other value
+                 torch.ones((5, 2), device="cuda")[:, :1],       # per row
+                 torch.ones((1, 16), device="cuda").expand(5, 16),  # rows that overlap
+                 torch.ones((5, 32), device="cuda")[:, ::2],
+                 torch.ones((5, 16), device="cuda").to(BF16)):
+        with pytest.raises((ValueError, TypeError)):
+            g7.gemm_norm_gate(c["x"], c["y"], gate=gate)
 
 
 # ------------------------------------------------- 8-bit weight gradient
