@@ -132,10 +132,6 @@ __device__ __forceinline__ void cp_async_16(void* dst, const void* src, uint32_t
                "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(shared_u32(dst)), "l"(src)
-               : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }

@@ -291,9 +291,11 @@ __device__ __forceinline__ void finish(int outs, int rank, int blocks, At at, Pu
 
 // ------------------------------------------- few rows: K goes over the warps
 //
-// Up to 8 rows of A; a cluster takes CT tiles of columns, the 128-row blocks of
-// K go round over the warps of its blocks.  A's pieces come through the ring
+// Up to kFewRows rows of A; a cluster takes CT tiles of columns, the 128-row blocks
+// of K go round over the warps of its blocks.  A's pieces come through the ring
 // like the weights.  The warps' sums are added in warp order.
+constexpr int kFewRows = 4;
+
 template <int CT, int GPT, int STAGES>
 __global__ void __launch_bounds__(kThreads, 2) w4_rows_kernel(W4Args p, int vec_a) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -302,15 +304,14 @@ __global__ void __launch_bounds__(kThreads, 2) w4_rows_kernel(W4Args p, int vec_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int blocks = static_cast<int>(gridDim.z), rank = static_cast<int>(blockIdx.z);
-  const int nt0 = blockIdx.x * CT, m0 = blockIdx.y * 8;
-  const int rows = min(8, p.M - m0);
+  const int nt0 = blockIdx.x * CT, rows = p.M;
   const int first = rank * kWarps + warp, step = blocks * kWarps;
   const int stage_bytes = Weights::kStageBytes + rows * 256;
   uint8_t* ring = smem + warp * STAGES * stage_bytes;
   const bool mine = g < rows;
   const Weights w(p, nt0);
   w.clear(ring, STAGES, stage_bytes);
-  const __nv_bfloat16* a_row = p.A + (m0 + (mine ? g : 0)) * p.lda;
+  const __nv_bfloat16* a_row = p.A + (mine ? g : 0) * p.lda;
   const int whole = p.K / kW4TileK;  // blocks of K that end inside the row
   grid_dependency_wait();
   grid_dependents_go();
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_rows_kernel(W4Args p, int vec_
          [&](int i) { return &red[0][i % (CT * 16)][i / (CT * 16)]; },
          [&](int i, float v) {
            const int n = nt0 * 16 + i % (CT * 16);
-           if (n < p.N) write_c(p, m0 + i / (CT * 16), n, v);
+           if (n < p.N) write_c(p, i / (CT * 16), n, v);
          });
 }
 
@@ -624,10 +625,9 @@ cudaError_t launch_rows(const W4Args& a, bool vec_a, int gx, int blocks, cudaStr
         sizeof(float) * kWarps * CT * 16 * 9);
   };
   const auto kernel = w4_rows_kernel<CT, GPT, STAGES>;
-  const cudaError_t e = allow_shared(kernel, smem(8), &allowed);
+  const cudaError_t e = allow_shared(kernel, smem(kFewRows), &allowed);
   if (e != cudaSuccess) return e;
-  return launch_cluster(kernel, a, vec_a, gx, (a.M + 7) / 8, blocks, smem(a.M < 8 ? a.M : 8),
-                        stream);
+  return launch_cluster(kernel, a, vec_a, gx, 1, blocks, smem(a.M), stream);
 }
 
 template <int CT, int NT, int GPT>
@@ -649,7 +649,7 @@ cudaError_t launch_groups(const W4Args& a, const LayerDevice& dev, cudaStream_t 
   const bool vec_a = (reinterpret_cast<uintptr_t>(a.A) & 15u) == 0 && (a.lda % 8 == 0 || a.M == 1);
   const int ntiles = (a.N + kW4TileN - 1) / kW4TileN, kts = (a.K + kW4TileK - 1) / kW4TileK;
   int blocks = 1;
-  if (a.M <= 4) {
+  if (a.M <= kFewRows) {
     const bool two = ntiles >= 4 * dev.sms;
     const int gx = two ? (ntiles + 1) / 2 : ntiles;
     // few columns: at least two steps to a warp of each block
