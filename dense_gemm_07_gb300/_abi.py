@@ -127,6 +127,7 @@ SIGNATURES = [
                                    ctypes.c_int32, _vp, _i64, _vp, _vp]),
     ("gemm_ckpt8_wgrad", _i32, [_i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i64,
                                 ctypes.c_float, _vp]),
+    ("gemm_ckpt8_wgrad_units", _i64, [_i64, _i64, _i64, _i32, _i32, _vp, _i64]),
 ]
 
 
@@ -263,11 +264,22 @@ def gemm_pair_units(M, N, K, max_pairs, pair, schedule=SCHEDULE_AUTO):
     """The BF16 paired-SM kernel's work units for one pair, in order, as a
     list of (tile, k0, k1, slot, first_pair, segments, stream_k, n_off,
     width) tuples; raises on bad arguments."""
-    n = lib().gemm_pair_units(M, N, K, max_pairs, schedule, pair, None, 0)
+    return _units("gemm_pair_units", M, N, K, max_pairs, schedule, pair)
+
+
+def gemm_ckpt8_wgrad_units(T, K, N, max_pairs, pair):
+    """The weight gradient's work units for one pair, as gemm_pair_units lists
+    them (slices of 128 rows of T)."""
+    return _units("gemm_ckpt8_wgrad_units", T, K, N, max_pairs, pair)
+
+
+def _units(name, *args):
+    fn = getattr(lib(), name)
+    n = fn(*args, None, 0)
     if n < 0:
-        raise ValueError("gemm_pair_units: argument out of range")
+        raise ValueError(f"{name}: argument out of range")
     buf = (ctypes.c_int64 * (9 * max(n, 1)))()
-    n2 = lib().gemm_pair_units(M, N, K, max_pairs, schedule, pair, buf, n)
+    n2 = fn(*args, buf, n)
     assert n2 == n
     return [tuple(buf[9 * i:9 * i + 9]) for i in range(n)]
 

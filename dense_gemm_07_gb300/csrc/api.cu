@@ -1020,6 +1020,42 @@ gemm_status_t run_bf16_noalloc(int64_t M, int64_t N, int64_t K,
       ldc, m, n, ps, sk_sync, tag, d->status, epi_identity(), stream));
 }
 
+// The units of one pair, nine numbers each (gemm_pair_units in the header).
+int64_t list_units(const PairSchedule& ps, int pair, int64_t* out, int64_t cap) {
+  if (pair >= ps.pairs) return 0;
+  WorkIter wi;
+  wi.init(ps, pair);
+  WorkUnit w;
+  int64_t n = 0;
+  while (wi.next(ps, ps.pairs, w)) {
+    if (n < cap) {
+      int64_t* o = out + 9 * n;
+      o[6] = w.tile >= ps.dp_tiles ? 1 : 0;
+      o[7] = w.n_off;
+      o[8] = w.width;
+      o[0] = w.tile;
+      o[1] = w.k0;
+      o[2] = w.k1;
+      const bool whole = w.k0 == 0 && w.k1 == ps.num_kb;
+      if (whole) {
+        o[3] = -1;
+        o[4] = pair;
+        o[5] = 1;
+      } else {
+        const SkTile st = sk_tile(ps, w.tile);
+        o[3] = sk_slot(ps, pair, w.tile);
+        o[4] = st.q_first;
+        o[5] = st.nseg;
+      }
+    }
+    ++n;
+  }
+  return n;
+}
+
+// The 256 x 256 tiles of a K x N weight gradient fit 32 bits.
+bool wgrad_tiles_ok(int64_t K, int64_t N) { return (K + 255) / 256 * ((N + 255) / 256) <= kMaxDim; }
+
 }  // namespace
 
 // ---- services for the layer operators' entry points (layer.h)
@@ -1069,7 +1105,7 @@ gemm_status_t layer_ckpt8_wgrad(int64_t T, int64_t K, int64_t N, const uint8_t* 
   if (s != GEMM_OK) return s;
   const int max_pairs = ckpt8_wgrad_pairs();
   if (max_pairs <= 0) return GEMM_ERR_LAUNCH;
-  if ((K + 255) / 256 * ((N + 255) / 256) > kMaxDim) return GEMM_ERR_INVALID_ARG;
+  if (!wgrad_tiles_ok(K, N)) return GEMM_ERR_INVALID_ARG;
   const PairSchedule ps = ckpt8_wgrad_schedule(T, K, N, max_pairs);
   // dY is copied to aligned rows when the copy engine cannot read it in place
   // (as gemm_bf16_f32acc's B).
@@ -1289,36 +1325,17 @@ int64_t gemm_pair_units(int64_t M, int64_t N, int64_t K, int32_t max_pairs,
   if (schedule < GEMM_SCHEDULE_AUTO || schedule > GEMM_SCHEDULE_COLUMN_SPLIT)
     return -1;
   if (cap > 0 && out == nullptr) return -1;
-  const PairSchedule ps = pair_schedule(M, N, K, max_pairs, schedule);
-  if (pair >= ps.pairs) return 0;
-  WorkIter wi;
-  wi.init(ps, pair);
-  WorkUnit w;
-  int64_t n = 0;
-  while (wi.next(ps, ps.pairs, w)) {
-    if (n < cap) {
-      int64_t* o = out + 9 * n;
-      o[6] = w.tile >= ps.dp_tiles ? 1 : 0;
-      o[7] = w.n_off;
-      o[8] = w.width;
-      o[0] = w.tile;
-      o[1] = w.k0;
-      o[2] = w.k1;
-      const bool whole = w.k0 == 0 && w.k1 == ps.num_kb;
-      if (whole) {
-        o[3] = -1;
-        o[4] = pair;
-        o[5] = 1;
-      } else {
-        const SkTile st = sk_tile(ps, w.tile);
-        o[3] = sk_slot(ps, pair, w.tile);
-        o[4] = st.q_first;
-        o[5] = st.nseg;
-      }
-    }
-    ++n;
-  }
-  return n;
+  return list_units(pair_schedule(M, N, K, max_pairs, schedule), pair, out, cap);
+}
+
+int64_t gemm_ckpt8_wgrad_units(int64_t T, int64_t K, int64_t N, int32_t max_pairs,
+                               int32_t pair, int64_t* out, int64_t cap) {
+  if (T < 1 || K < 1 || N < 1 || T > kMaxDim || K > kMaxDim || N > kMaxDim ||
+      !wgrad_tiles_ok(K, N))
+    return -1;
+  if (max_pairs < 1 || pair < 0 || pair >= max_pairs) return -1;
+  if (cap > 0 && out == nullptr) return -1;
+  return list_units(ckpt8_wgrad_schedule(T, K, N, max_pairs), pair, out, cap);
 }
 
 gemm_status_t gemm_debug_inject(int mode, uint64_t wait_ns) {

@@ -632,6 +632,16 @@ GEMM07_API gemm_status_t gemm_ckpt8_wgrad(int64_t T, int64_t K, int64_t N, const
                                           int64_t ld_dy, float *dW, int64_t ldw, float beta,
                                           void *stream);
 
+/*
+ * gemm_ckpt8_wgrad_units: the work units of pair `pair` in gemm_ckpt8_wgrad for
+ * a T x K checkpoint and a T x N dY when `max_pairs` pairs are resident, as
+ * gemm_pair_units lists them: tiles of 256 x 256 of dW, 128 rows of T to a slice.
+ * No GPU needed.  -1 for an argument out of range.
+ */
+GEMM07_API int64_t gemm_ckpt8_wgrad_units(int64_t T, int64_t K, int64_t N,
+                                          int32_t max_pairs, int32_t pair,
+                                          int64_t *out, int64_t cap);
+
 #ifdef __cplusplus
 }
 #endif

@@ -107,7 +107,7 @@ def _whole(seed, T, K, N):
 
 # one tile in two parts; tiles in two and three parts; more tiles than pairs, whose
 # parts are summed one early and one late in the launch
-@pytest.mark.parametrize("T,K,N", [(4096, 128, 256), (3328, 1000, 3001), (4096, 2816, 2048)])
+@pytest.mark.parametrize("T,K,N", [(4096, 128, 256), (8448, 1000, 3001), (4096, 2816, 2048)])
 def test_calls_after_one_pair_gave_up_are_exact(T, K, N):
     """One pair's first copy is withheld: it gives up, and the pairs that share
     its tiles have counted their parts.  The calls after it find no trace of that,
