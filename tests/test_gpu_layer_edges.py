@@ -8,8 +8,9 @@ import torch
 
 import dense_gemm_07_gb300 as g7
 from dense_gemm_07_gb300 import _abi
-from test_gpu_layer import (_check_grads, _gen, _norm_case, _norm_ref, _randn, _strided,
-                            _w4_case)
+from layer_reference import EPS32, w4_weights
+from test_gpu_layer import (_check_grads, _close, _gen, _norm_case, _norm_ref, _randn, _strided,
+                            _w4_case, _w4_tol)
 
 pytestmark = pytest.mark.gpu
 
@@ -44,6 +45,19 @@ def test_w4_groups_past_the_matrix_add_nothing(M, K, N, group):
     assert bool((out[:, inf] == float("inf")).all())
     rest = [c for c in range(N) if c not in (nan, inf)]
     assert torch.equal(out[:, rest], clean[:, rest])
+
+
+# One tile of columns a warp, two, and four: N at the limits between them (4848 and
+# 9712 columns on 152 SMs) and odd remainders of a warp's tiles; K in one step, in
+# three, and cut over the blocks of a cluster.
+@pytest.mark.parametrize("M", [1, 4, 5, 8, 9, 16])
+@pytest.mark.parametrize("K,N", [(129, 4853), (320, 9729), (33, 9713), (1100, 4848), (257, 16401)])
+@pytest.mark.parametrize("group,zeros", [(32, False), (64, True), (128, False), (32, True)])
+def test_w4_of_wide_matrices(M, K, N, group, zeros):
+    a, codes, scales, z = _w4_case(M * 31 + N, M, K, N, group, zeros)
+    out = g7.gemm_w4(a, g7.w4_pack(codes), scales, zeros=z, group=group)
+    w = w4_weights(codes, scales, z, group)
+    _close(out, a.double() @ w, _w4_tol(a, w, K, group, out), "product")
 
 
 # ------------------------------------------------------------------- norms
@@ -82,6 +96,30 @@ def test_norm_gate_takes_a_gate_of_any_row_stride(T, D, extra):
     _check_grads(want, ref, dxo, dh, BF16, D)
 
 
+@pytest.mark.parametrize("D", [520, 77, 4096, 5000, 8192])
+@pytest.mark.parametrize("place", ["x", "d_x_out"])
+@pytest.mark.parametrize("xt", [F32, BF16])
+def test_norm_gate_bwd_in_place(D, place, xt):
+    """dx may be x or d_x_out: enough rows that a block's copies run ahead."""
+    T = 700
+    c = _norm_case(D, T, D, xt, F32, "channel")
+    dxo, dh = _randn(_gen(1), T, D, dtype=xt), _randn(_gen(2), T, D)
+    want = g7.gemm_norm_gate_bwd(**c, d_x_out=dxo, d_h=dh)
+    dx = c["x"] if place == "x" else dxo
+    out = [torch.empty_like(t) for t in want]
+    kind = _abi.TYPE_BF16 if xt == BF16 else _abi.TYPE_F32
+    args = _abi.GemmNormGateArgs(
+        T, D, c["x"].data_ptr(), D, kind, c["y"].data_ptr(), D, _abi.TYPE_F32,
+        c["weight_post"].data_ptr(), c["gate"].data_ptr(), D, _abi.GATE_CHANNEL,
+        c["weight_pre"].data_ptr(), 1.0, 1e-6)
+    grads = _abi.GemmNormGateGrads(
+        dxo.data_ptr(), D, dh.data_ptr(), D, _abi.TYPE_F32, dx.data_ptr(), D,
+        out[1].data_ptr(), D, out[3].data_ptr(), out[2].data_ptr(), out[4].data_ptr())
+    assert _abi.gemm_norm_gate_bwd(args, grads, torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(dx, want.dx)
+    assert all(torch.equal(a, b) for a, b in zip(out[1:], want[1:]))
+
+
 def test_norm_gate_refuses_gates_with_gaps_or_overlaps():
     c = _norm_case(1, 5, 16, F32, F32, "none")
     for gate in (torch.ones((16, 2), device="cuda")[:, 0],       # per channel, every other value
@@ -103,6 +141,30 @@ def _whole(seed, T, K, N):
     x[::32] = 127.0
     dy = torch.randint(-3, 4, (T, N), generator=g, device="cuda").to(BF16)
     return g7.gemm_ckpt8_pack(x), dy, x.double().t() @ dy.double()
+
+
+# (76 pairs) a second tile for some pairs, two and three whole waves; shared tiles
+# alone, in two and in three parts; a whole wave before shared ones; rows that the
+# copy engine cannot read in place
+@pytest.mark.parametrize("T,K,N", [
+    (130, 2560, 2100), (257, 4000, 2304), (640, 3900, 3841), (4096, 2816, 2048), (4100, 2700, 2041),
+    (8448, 1000, 3001), (8700, 2048, 1536), (3500, 4096, 2560), (3521, 4090, 2501)])
+def test_ckpt8_wgrad_of_many_tiles(T, K, N):
+    kept, dy, want = _whole(T, T, K, N)
+    got = g7.gemm_ckpt8_wgrad(kept, dy)
+    assert torch.equal(got.double(), want)
+    out = got.clone()
+    g7.gemm_ckpt8_wgrad(kept, dy, out=out, beta=-2.0)
+    assert torch.equal(out.double(), -want)
+    # and within the bound of test_ckpt8_wgrad on values that round, bit for bit again
+    x = _randn(_gen(T), T, K)
+    dy = _randn(_gen(N), T, N, dtype=BF16)
+    k = g7.gemm_ckpt8_pack(x)
+    v = g7.gemm_ckpt8_unpack(k, F32).double()
+    got = g7.gemm_ckpt8_wgrad(k, dy)
+    units = 64 + 2 * (T // 512 + 2)
+    _close(got, v.t() @ dy.double(), units * EPS32 * (v.abs().t() @ dy.double().abs()) + 1e-37)
+    assert torch.equal(got, g7.gemm_ckpt8_wgrad(k, dy))
 
 
 # one tile in two parts; tiles in two and three parts; more tiles than pairs, whose
