@@ -38,9 +38,10 @@
 //
 // Measured: 4096 x 4096 x 11008 273 to 277 us, 1.34 PFLOP/s, 69 % of the measured
 // BF16 rate, where gemm_bf16_f32acc on X in 16 bits, without these sums, takes
-// 206; 3001 x 1000 x 3000 28 us.  In parts: without the copies of dY and the loads
-// of X, and sums of 1024 rows, 214 us; without decoding as well 185.  Adding in
-// registers costs 6.  Tried without gain: dY in 6 slices (293 us), sums of 1024
+// 206 (with beta, which reads dW, 345 us); 3001 x 1000 x 3000 28 to 31 us.  The 96
+// registers a thread that the block is launched with spill 148 bytes.  In parts:
+// without the copies of dY and the loads of X, and sums of 1024 rows, 214 us;
+// without decoding as well 185.  Adding in registers costs 6.  Tried without gain: dY in 6 slices (293 us), sums of 1024
 // rows (270, left alone for their larger error), other register splits (274 to
 // 381).
 //

@@ -18,12 +18,15 @@
 // At sixteen rows no unit is full (16 x 16384 x 8192, groups of 64, counters: 1.9
 // of 4 instructions a cycle, integer pipe 35 %, tensor pipe 27 %): 16 warps an SM,
 // which 128 registers a thread allow, do not cover the latencies of decoding and
-// products.  Measured (M x K x N, inputs beyond L2): 1 x 8192 x 32768, groups of
-// 128, 33 us, 4.2 TB/s (62 % of the measured copy rate); 16 x 8192 x 32768 46 us,
-// 3.1 TB/s, with groups of 64 and zero points 52 us, 2.9 TB/s; 1 x 4096 x 4096
-// 5.4 us, mostly launch and latency.  Tried without gain: shifts as high products
-// (16 x 8192 x 32768: 46 -> 56 us), rings of three and five stages (52 and 68 us
-// against 52 with groups of 64).
+// products.  With groups of 32 and two tiles a warp the ring and its scales take
+// 118 KB a block at more than eight rows (116 KB at four rows, K over the warps),
+// so one block and 8 warps an SM.  Measured (M x K x N, inputs beyond L2): 1 x 8192
+// x 32768, groups of 128, 33 us, 4.2 TB/s (62 % of the measured copy rate); 16 x
+// 8192 x 32768 46 us, 3.0 TB/s, with zero points and groups of 64 52 us, 2.8 TB/s,
+// of 32 71 us, 2.2 TB/s; 4 x 8192 x 32768 with groups of 32 50 us, 3.2 TB/s; 1 x
+// 4096 x 4096 6.1 us, mostly launch and latency.  Tried without gain: shifts as
+// high products (16 x 8192 x 32768: 46 -> 56 us), rings of three and five stages
+// (52 and 68 us against 52 with groups of 64).
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -45,7 +48,9 @@ constexpr int kThreads = kWarps * 32;
 __host__ __device__ __forceinline__ int nibble_shift(int e) { return 4 * (e / 2 + 4 * (e % 2)); }
 
 // The codes at pair i of a word, as two BF16 whole numbers 128 + q: the bits
-// 0x4300 | q are exactly 128 + q.
+// 0x4300 | q are exactly 128 + q.  (Whole numbers made into floating point under a
+// fixed exponent are a published way of decoding few-bit weights: Kim et al., "Who
+// Says Elephants Can't Run", 2022.)
 // One three-input logic operation for both (written as & and | it became two).
 __device__ __forceinline__ uint32_t decode_pair(uint32_t w, int i) {
   uint32_t d;
@@ -658,8 +663,9 @@ cudaError_t launch_groups(const W4Args& a, const LayerDevice& dev, cudaStream_t 
                : launch_rows<1, GPT>(a, vec_a, gx, blocks, stream);
   }
   // As wide as still gives every SM a block when K is cut in eight.  (Sixteen
-  // rows with two or four groups a step spill at four tiles: 16 x 8192 x 32768,
-  // groups of 64, takes 57 us, at two tiles 52.)
+  // rows at four tiles do not fit 128 registers: with one group a step 8 bytes
+  // spill, with two 128, which took 57 us at 16 x 8192 x 32768 against 52 at two
+  // tiles; with four 76.)
   const int widest = a.M <= 8 || GPT == 1 ? 4 : 2;
   int ct = ntiles >= 4 * dev.sms ? 4 : ntiles >= 2 * dev.sms ? 2 : 1;
   if (ct > widest) ct = widest;

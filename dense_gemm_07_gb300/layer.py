@@ -3,9 +3,11 @@ with gate and residual, 8-bit activation checkpoints.
 
 Every function passes CUDA tensors to the C entry point of its name (declared in
 ``include/gemm07.h``) through the compiled binding ``csrc/layer_binding.cpp``, on
-``stream`` (default: the current stream).  Matrices have contiguous rows and any
-row stride; a refused argument raises ValueError or TypeError, a status of the
-library GemmError.
+``stream`` (default: the current stream).  Tensors that a call makes come from the
+current stream's memory, as in the rest of the package: another ``stream`` has to
+wait for the current one first, as it has to for the operands.  Matrices have
+contiguous rows and any row stride; a refused argument raises ValueError or
+TypeError, a status of the library GemmError.
 """
 from __future__ import annotations
 
