@@ -10,7 +10,7 @@ the C entry points and the ctypes layer load.
 
 A rebuild of either happens only when one of its sources or headers is newer,
 and of the binding also when the installed torch or Python is another one than
-it was compiled against (recorded beside it).
+it was compiled against (recorded under ``_build/``).
 """
 from __future__ import annotations
 
@@ -30,7 +30,7 @@ LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libgemm07.so")
 BINDING_SRC = os.path.join(CSRC, "layer_binding.cpp")
 BINDING_PATH = os.path.join(LIB_DIR, "layer_binding.so")
-BINDING_STAMP = os.path.join(LIB_DIR, "layer_binding.txt")  # what it was compiled against
+BINDING_STAMP = os.path.join(BUILD_DIR, "layer_binding.txt")  # what it was compiled against
 HEADER = os.path.join(ROOT, "include", "gemm07.h")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

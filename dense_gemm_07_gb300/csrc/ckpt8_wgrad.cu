@@ -41,9 +41,9 @@
 // 206 (with beta, which reads dW, 345 us); 3001 x 1000 x 3000 28 to 31 us.  The 96
 // registers a thread that the block is launched with spill 148 bytes.  In parts:
 // without the copies of dY and the loads of X, and sums of 1024 rows, 214 us;
-// without decoding as well 185.  Adding in registers costs 6.  Tried without gain: dY in 6 slices (293 us), sums of 1024
-// rows (270, left alone for their larger error), other register splits (274 to
-// 381).
+// without decoding as well 185.  Adding in registers costs 6.  Tried without
+// gain: dY in 6 slices (293 us), sums of 1024 rows (270, left alone for their
+// larger error), other register splits (274 to 381).
 //
 // Work sharing (stream_k.cuh): whole tiles round-robin over the resident pairs;
 // the tiles of a partial last wave, with those of the last whole one, are cut

@@ -23,7 +23,7 @@ def commands(tmp_path, monkeypatch):
     monkeypatch.setattr(_build, "_nvcc", lambda: os.path.join("cuda", "bin", "nvcc"))
     for name, value in (("BUILD_DIR", "b"), ("LIB_DIR", "l"), ("LIB_PATH", "l/libgemm07.so"),
                         ("BINDING_PATH", "l/layer_binding.so"),
-                        ("BINDING_STAMP", "l/layer_binding.txt")):
+                        ("BINDING_STAMP", "b/layer_binding.txt")):
         monkeypatch.setattr(_build, name, str(tmp_path / value))
     return ran
 
