@@ -14,7 +14,10 @@ missing or unloadable library is an error, never a fallback.
 Beside the GEMM stand the operators of a transformer layer around it: products
 with 4-bit weights (``gemm_w4``), norms with gate and residual
 (``gemm_norm_gate``) and 8-bit activation checkpoints (``gemm_ckpt8_*``);
-``layer_example`` runs them together.
+``layer_example`` runs them together.  A layer of experts is made of 8-bit
+floating-point products (``gemm_fp8_quantize``, ``gemm_fp8``, ``gemm_fp8_experts``),
+its router (``gemm_route``) and ``gemm_combine``; ``experts_example`` runs them
+together.
 
 The raw ctypes entry points (integer addresses) are in ``dense_gemm_07_gb300.abi``.
 """
@@ -29,17 +32,23 @@ _LAYER = ("gemm_w4", "w4_pack", "w4_quantize", "w4_unpack",
           "gemm_norm_gate", "gemm_norm_gate_bwd", "NormGateGrads",
           "gemm_ckpt8_pack", "gemm_ckpt8_unpack", "gemm_ckpt8_act_grad",
           "gemm_ckpt8_wgrad", "Ckpt8")
+_EXPERTS = ("Fp8", "gemm_fp8_quantize", "gemm_fp8", "gemm_fp8_experts",
+            "Routing", "gemm_route", "gemm_route_bwd", "gemm_combine", "gemm_combine_bwd")
 
 __all__ = ["abi", "build", "GemmError", "gemm_f32", "gemm_bf16_f32acc", "gemm_f32_ladder",
            "gemm_f32_ex", "gemm_bf16_f32acc_ex",
            "gemm_f32_host", "gemm_bf16_f32acc_host", "gemm_get_device_status",
-           "gemm_status_string", "plan", *_LAYER]
+           "gemm_status_string", "plan", *_LAYER, *_EXPERTS]
 
 
 def __getattr__(name):
     if name in _LAYER:
         from . import layer
         globals().update({n: getattr(layer, n) for n in _LAYER})
+        return globals()[name]
+    if name in _EXPERTS:
+        from . import experts
+        globals().update({n: getattr(experts, n) for n in _EXPERTS})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 

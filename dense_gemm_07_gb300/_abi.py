@@ -52,6 +52,40 @@ class GemmW4(ctypes.Structure):
                 ("ld_zeros", ctypes.c_int64), ("group", ctypes.c_int32)]
 
 
+class GemmFp8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("ld_scales", ctypes.c_int64),
+                ("square", ctypes.c_int32)]
+
+
+class GemmFp8QuantizeArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("C", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_type", ctypes.c_int32),
+                ("square", ctypes.c_int32), ("transpose", ctypes.c_int32),
+                ("index", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("batch", ctypes.c_int64), ("x_step", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("codes_step", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("ld_scales", ctypes.c_int64), ("scales_step", ctypes.c_int64)]
+
+
+class GemmRouteArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("logits", ctypes.c_void_p), ("ld", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("bias", ctypes.c_void_p),
+                ("groups", ctypes.c_int32), ("groups_kept", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class GemmCombineArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("D", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("R", ctypes.c_int64), ("rows", ctypes.c_void_p), ("ld_rows", ctypes.c_int64),
+                ("rows_type", ctypes.c_int32), ("slot", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("x_type", ctypes.c_int32)]
+
+
 class GemmNormGateArgs(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("D", ctypes.c_int64),
                 ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_type", ctypes.c_int32),
@@ -128,6 +162,18 @@ SIGNATURES = [
     ("gemm_ckpt8_wgrad", _i32, [_i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i64,
                                 ctypes.c_float, _vp]),
     ("gemm_ckpt8_wgrad_units", _i64, [_i64, _i64, _i64, _i32, _i32, _vp, _i64]),
+    ("gemm_fp8_quantize", _i32, [ctypes.POINTER(GemmFp8QuantizeArgs), _vp]),
+    ("gemm_fp8", _i32, [_i64, _i64, _i64, ctypes.POINTER(GemmFp8), ctypes.POINTER(GemmFp8), _vp,
+                        _i64, _i32, ctypes.POINTER(GemmEpilogue), _vp]),
+    ("gemm_fp8_experts", _i32, [_i64, _i64, _i64, _i64, ctypes.POINTER(GemmFp8),
+                                ctypes.POINTER(GemmFp8), _vp, _vp, _i64, _i32,
+                                ctypes.POINTER(GemmEpilogue), _vp]),
+    ("gemm_route_workspace_bytes", _i64, [_i64, _i64]),
+    ("gemm_route", _i32, [ctypes.POINTER(GemmRouteArgs), _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    ("gemm_route_bwd", _i32, [ctypes.POINTER(GemmRouteArgs), _vp, _vp, _vp, _i64, _vp]),
+    ("gemm_combine", _i32, [ctypes.POINTER(GemmCombineArgs), _vp, _i64, _i32, _vp]),
+    ("gemm_combine_bwd", _i32, [ctypes.POINTER(GemmCombineArgs), _vp, _i64, _i32, _vp, _i64, _vp,
+                                _vp]),
 ]
 
 
@@ -337,3 +383,43 @@ def gemm_ckpt8_act_grad(T, N, G, ldg, g_type, q, scales, activation, dZ, ld_dz, 
 
 def gemm_ckpt8_wgrad(T, K, N, q, scales, dY, ld_dy, dW, ldw, beta, stream):
     return lib().gemm_ckpt8_wgrad(T, K, N, q, scales, dY, ld_dy, dW, ldw, beta, stream)
+
+
+def gemm_fp8_quantize(args, stream):
+    """args: a GemmFp8QuantizeArgs."""
+    return lib().gemm_fp8_quantize(_epi(args), stream)
+
+
+def gemm_fp8(M, N, K, A, B, C, ldc, c_type, epilogue, stream):
+    """A, B: GemmFp8; epilogue: a GemmEpilogue or None."""
+    return lib().gemm_fp8(M, N, K, _epi(A), _epi(B), C, ldc, c_type, _epi(epilogue), stream)
+
+
+def gemm_fp8_experts(E, M, N, K, A, B, offsets, C, ldc, c_type, epilogue, stream):
+    return lib().gemm_fp8_experts(E, M, N, K, _epi(A), _epi(B), offsets, C, ldc, c_type,
+                                  _epi(epilogue), stream)
+
+
+def gemm_route_workspace_bytes(T, E):
+    return lib().gemm_route_workspace_bytes(T, E)
+
+
+def gemm_route(args, index, weight, slot, source, offsets, workspace, stream):
+    """args: a GemmRouteArgs."""
+    return lib().gemm_route(_epi(args), index, weight, slot, source, offsets, workspace, stream)
+
+
+def gemm_route_bwd(args, index, d_weight, d_logits, ld_d, stream):
+    """args: a GemmRouteArgs."""
+    return lib().gemm_route_bwd(_epi(args), index, d_weight, d_logits, ld_d, stream)
+
+
+def gemm_combine(args, out, ld_out, out_type, stream):
+    """args: a GemmCombineArgs."""
+    return lib().gemm_combine(_epi(args), out, ld_out, out_type, stream)
+
+
+def gemm_combine_bwd(args, d_out, ld_d_out, d_out_type, d_rows, ld_d_rows, d_weight, stream):
+    """args: a GemmCombineArgs."""
+    return lib().gemm_combine_bwd(_epi(args), d_out, ld_d_out, d_out_type, d_rows, ld_d_rows,
+                                  d_weight, stream)

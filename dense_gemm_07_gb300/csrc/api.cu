@@ -11,6 +11,7 @@
 
 #include "../../include/gemm07.h"
 #include "kernels.h"
+#include "experts.h"
 #include "layer.h"
 #include "tile_order.cuh"
 
@@ -1096,6 +1097,11 @@ void layer_scratch_done(const LayerScratch& s, cudaStream_t stream) {
 gemm_status_t layer_epilogue(const gemm_epilogue_t* e, EpiParams* out) { return to_epi(e, out); }
 
 gemm_status_t layer_from_cuda(cudaError_t e) { return from_cuda(e); }
+
+gemm_status_t layer_map_bytes(CUtensorMap* map, const void* base, int64_t inner, int64_t outer,
+                              int64_t ld, uint32_t box_rows) {
+  return make_map_typed(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, inner, outer, ld, 128, box_rows);
+}
 
 gemm_status_t layer_ckpt8_wgrad(int64_t T, int64_t K, int64_t N, const uint8_t* q,
                                 const uint8_t* scales, const uint16_t* dY, int64_t ld_dy,

@@ -1,0 +1,438 @@
+// fp8_few.cu -- products of 8-bit floating-point matrices with a scale for each
+// block of 128 values, on 128-column tiles of C:
+//   C[m][n] = act(alpha * sum_kb sa[kb][m] * sb * P[m][n][kb] + beta * C + bias[n]),
+//   P = sum over the 128 k of block kb of a[m][k] * b[n][k].
+// The tensor core forms P (products of 8-bit codes are exact, at most 128 of them
+// are added in tensor memory), and every P is scaled and added in registers in
+// FP32: one multiply-add for each element of C and block of 128 k.
+//
+// The rows of B (columns of C) are the MMA's 128 lanes and the rows of A its 16 to
+// 128 columns, as many as the tile has in steps of 16: a few rows cost a narrow MMA,
+// and the scales of A's rows, which change along a thread's sums, are read from
+// shared memory as broadcasts, sa * sb already multiplied where a block of B is
+// 128 x 128.  The tile's K is shared by the 1 to 8 CTAs of a cluster; their partial
+// sums meet in distributed shared memory and are added in rank order.
+//
+// Roles, 384 threads: warp 0 copies both operands by TMA (a ring of 128-byte
+// rows), warp 1 issues the MMAs, warp 2 stages the scales, warps 4-11 add (two
+// groups of four take turns at 16 columns) and write C.  Two CTAs share an SM, so
+// that one's start and end overlap the other's copies.  Every wait is bounded.
+#include <atomic>
+
+#include "experts.h"
+#include "fp8.cuh"
+#include "kernels.h"
+#include "sm103_ptx.cuh"
+
+namespace g07 {
+namespace {
+
+constexpr int TILE_N = 128;
+constexpr int BK = kFp8Block;
+constexpr int B_BYTES = TILE_N * BK;
+constexpr int THREADS = 384;
+constexpr int SUM_WARPS = 8;
+constexpr int MAX_STAGES = 8;
+constexpr int SLOTS = 4;  // staged scales
+// Shared memory of a CTA when two share an SM (228 KB, 1 KB of it reserved for each).
+constexpr int kSmemBytes = 228 * 1024 / 2 - 1024;
+
+// Registers a thread of the wide kernel's roles (setmaxnreg): together what the
+// block is launched with, 384 x 80.
+constexpr int kRegsOther = 32, kRegsSum = 104;
+constexpr int kRegsBlock = 128 * kRegsOther + 256 * kRegsSum;
+static_assert(kRegsBlock <= THREADS * 80, "register split");
+
+template <int COLS>
+struct alignas(16) Control {
+  static constexpr int ACCS = COLS <= 32 ? 4 : 2;
+  float scale[SLOTS][COLS];
+  uint64_t full[MAX_STAGES];
+  uint64_t empty[MAX_STAGES];
+  uint64_t acc_full[ACCS];
+  uint64_t acc_empty[ACCS];
+  uint64_t scale_full[SLOTS];
+  uint64_t scale_empty[SLOTS];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  Fp8Rows rows;  // the tile's expert and rows
+};
+
+struct FewArgs {
+  Fp8GemmArgs g;
+  int cols, stages, split, n_tiles;
+  unsigned int* status;
+};
+
+__device__ __forceinline__ void give_up(volatile int* abort, unsigned int* status) {
+  *abort = 1;
+  atomicOr(status, 1u);
+}
+
+// SQUARE: a block of B's scales is 128 x 128, so that sa * sb is staged; else every
+// row of B has its own and a thread multiplies by its row's.
+template <int COLS, bool SQUARE>
+__global__ void __launch_bounds__(THREADS, 2)
+fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const FewArgs p) {
+  using Ctl = Control<COLS>;
+  constexpr int ACCS = Ctl::ACCS;
+  constexpr int CHUNKS = COLS / 32;  // 16-column chunks of a group of four sum warps
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int stage_bytes = B_BYTES + p.cols * BK;
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + p.stages * stage_bytes);
+  volatile int* abort = &ctl->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int tile = static_cast<int>(blockIdx.x) / p.split;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    for (int a = 0; a < ACCS; ++a) {
+      mbar_init(&ctl->acc_full[a], 1);
+      mbar_init(&ctl->acc_empty[a], SUM_WARPS);
+    }
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(&ctl->scale_full[s], 1);
+      mbar_init(&ctl->scale_empty[s], SUM_WARPS);
+    }
+    mbar_init(&ctl->drain, 1);
+    ctl->abort = 0;
+    fence_barrier_init();
+    if (p.g.K > 0) {
+      tma_prefetch_desc(&tmA);
+      tma_prefetch_desc(&tmB);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, ACCS * COLS);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  grid_dependents_go();
+  if (warp == 2) {
+    const int unit = tile / p.n_tiles;
+    Fp8Rows r;
+    if (p.g.E > 0) {
+      r = fp8_expert_rows(p.g.offsets, p.g.E, p.g.M, p.cols, unit);
+    } else {
+      r.expert = 0;
+      r.first = unit * p.cols;
+      r.count = p.g.M - r.first < p.cols ? p.g.M - r.first : p.cols;
+    }
+    if (lane == 0) ctl->rows = r;
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = ctl->tmem_base;
+  const uint64_t limit = wait_limit_ns(p.status);
+  const Fp8Rows rows = ctl->rows;
+  const int n0 = tile % p.n_tiles * TILE_N;
+  const int kbs = (p.g.K + BK - 1) / BK;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(kbs) * rank / p.split);
+  const int kb1 = rows.count > 0 ? static_cast<int>(static_cast<int64_t>(kbs) * (rank + 1) / p.split)
+                                 : kb0;
+  const int ncols = (rows.count + 15) & ~15;
+
+  const int group = (warp >> 2) & 1;         // of the sum warps: takes chunks group, group + 2, ...
+  const int tlane = (warp & 3) * 32 + lane;  // lane of the MMA, column of the tile
+  // The sums leave through the ring, once every MMA that read it has completed:
+  // 128 columns of C a row of A.
+  float* part = reinterpret_cast<float*>(smem);
+
+  if (warp < 4) {
+    if constexpr (COLS > 32) regs_dec<kRegsOther>();
+    if (warp == 0 && lane == 0) {
+      // ----------------------------------------------------------- copies
+      // test fault: the first stage is never copied
+      const bool skip = p.status[1] == 1u;
+      const int brow = rows.expert * p.g.N + n0;
+      int stage = 0;
+      uint32_t phase = 0;
+      int last[MAX_STAGES];
+      for (int s = 0; s < MAX_STAGES; ++s) last[s] = -1;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort, limit)) {
+          give_up(abort, p.status);
+          break;
+        }
+        if (!(skip && kb == kb0)) {
+          uint8_t* b = smem + stage * stage_bytes;
+          mbar_arrive_expect_tx(&ctl->full[stage], stage_bytes);
+          tma_load_2d(b, &tmB, &ctl->full[stage], kb * BK, brow);
+          tma_load_2d(b + B_BYTES, &tmA, &ctl->full[stage], kb * BK, rows.first);
+#pragma unroll
+          for (int s = 0; s < MAX_STAGES; ++s)
+            if (s == stage) last[s] = static_cast<int>(phase);
+        }
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      // copies in flight land before the CTA may exit
+      volatile int never = 0;
+#pragma unroll
+      for (int s = 0; s < MAX_STAGES; ++s)
+        if (last[s] >= 0 &&
+            !mbar_wait(&ctl->full[s], static_cast<uint32_t>(last[s]), &never, limit))
+          give_up(abort, p.status);
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------------------- MMAs
+      const uint32_t idesc = idesc_e4m3_f32(TILE_N, ncols);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool issued = false;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&ctl->acc_empty[acc], acc_phase ^ 1u, abort, limit) ||
+            !mbar_wait(&ctl->full[stage], phase, abort, limit)) {
+          give_up(abort, p.status);
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t b = smem_u32(smem + stage * stage_bytes);
+#pragma unroll
+        for (int kk = 0; kk < BK / 32; ++kk)
+          mma_e4m3_ss(tmem + acc * COLS, sdesc_sw128(b + kk * 32, 16, 1024),
+                      sdesc_sw128(b + B_BYTES + kk * 32, 16, 1024), idesc, kk != 0 ? 1u : 0u);
+        issued = true;
+        mma_commit(&ctl->empty[stage]);
+        mma_commit(&ctl->acc_full[acc]);
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (++acc == ACCS) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      if (issued) {
+        mma_commit(&ctl->drain);
+        volatile int never = 0;
+        if (!mbar_wait(&ctl->drain, 0u, &never, limit)) give_up(abort, p.status);
+      }
+    } else if (warp == 2) {
+      // ----------------------------------------------------------- scales
+      const float* sa = p.g.sa + rows.first;
+      const float* sb = p.g.sb;
+      if (SQUARE)
+        sb += (static_cast<int64_t>(rows.expert) * p.n_tiles + n0 / TILE_N) * p.g.ld_sb;
+      int slot = 0;
+      uint32_t phase = 0;
+      float v[COLS / 32];
+      auto load = [&](int kb) {
+        const float f = SQUARE ? __ldg(sb + kb) : 1.0f;
+#pragma unroll
+        for (int i = 0; i < COLS / 32; ++i)
+          v[i] = i * 32 + lane < rows.count ? f * __ldg(sa + kb * p.g.ld_sa + i * 32 + lane) : 0.0f;
+      };
+      if (kb0 < kb1) load(kb0);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!__all_sync(0xFFFFFFFFu,
+                        mbar_wait(&ctl->scale_empty[slot], phase ^ 1u, abort, limit))) {
+          if (lane == 0) give_up(abort, p.status);
+          break;
+        }
+#pragma unroll
+        for (int i = 0; i < COLS / 32; ++i) ctl->scale[slot][i * 32 + lane] = v[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->scale_full[slot]);
+        if (kb + 1 < kb1) load(kb + 1);
+        if (++slot == SLOTS) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else {
+    // --------------------------------------------------------------- sums
+    if constexpr (COLS > 32) regs_inc<kRegsSum>();
+    uint64_t sum[CHUNKS][8];  // column n0 + tlane, 16 rows of A a chunk
+#pragma unroll
+    for (int j = 0; j < CHUNKS; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[j][i] = 0;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const float* sb = p.g.sb + n0 + tlane;
+    const bool in = n0 + tlane < p.g.N;
+    float next = 0.0f;
+    if (!SQUARE && in && kb0 < kb1) next = __ldg(sb + kb0 * p.g.ld_sb);
+    int acc = 0, slot = 0;
+    uint32_t acc_phase = 0, phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const float mine = next;
+      if (!SQUARE && in && kb + 1 < kb1) next = __ldg(sb + (kb + 1) * p.g.ld_sb);
+      const bool ok = mbar_wait(&ctl->scale_full[slot], phase, abort, limit) &&
+                      mbar_wait(&ctl->acc_full[acc], acc_phase, abort, limit);
+      if (!__all_sync(0xFFFFFFFFu, ok)) {
+        if (lane == 0) give_up(abort, p.status);
+        break;
+      }
+      tc_fence_after_sync();
+#pragma unroll
+      for (int j = 0; j < CHUNKS; ++j) {
+        const int col = (2 * j + group) * 16;
+        if (col < ncols) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(taddr + acc * COLS + col, r);
+          tmem_ld_wait();
+          const float4* s = reinterpret_cast<const float4*>(&ctl->scale[slot][col]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 f = s[i];
+            uint64_t lo = pack2(f.x, f.y), hi = pack2(f.z, f.w);
+            if (!SQUARE) {
+              const uint64_t m2 = pack2(mine, mine);
+              lo = mul2(lo, m2);
+              hi = mul2(hi, m2);
+            }
+            sum[j][2 * i] = fma2(pack2u(r[4 * i], r[4 * i + 1]), lo, sum[j][2 * i]);
+            sum[j][2 * i + 1] = fma2(pack2u(r[4 * i + 2], r[4 * i + 3]), hi, sum[j][2 * i + 1]);
+          }
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ctl->acc_empty[acc]);
+        mbar_arrive(&ctl->scale_empty[slot]);
+      }
+      if (++acc == ACCS) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+      if (++slot == SLOTS) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < CHUNKS; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int c = (2 * j + group) * 16 + i;
+        if (c < rows.count) part[c * TILE_N + tlane] = half_of(sum[j][i / 2], i & 1);
+      }
+  }
+
+  // ------------------------------------------------------------------ output
+  if (p.split > 1) cluster_sync();
+  const int n = n0 + tlane;
+  if (warp >= 4 && n < p.g.N) {
+    const float b =
+        p.g.epi.bias ? __ldg(p.g.epi.bias + static_cast<int64_t>(rows.expert) * p.g.N + n) : 0.0f;
+    auto store = [&](int c, float v) {
+      const int64_t at = static_cast<int64_t>(rows.first + c) * p.g.ldc + n;
+      if (p.g.c_bf16) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.g.C) + at;
+        const float old = p.g.epi.beta != 0.0f ? __bfloat162float(*o) : 0.0f;
+        *o = __float2bfloat16_rn(epi_apply(p.g.epi, v, old, b));
+      } else {
+        float* o = static_cast<float*>(p.g.C) + at;
+        const float old = p.g.epi.beta != 0.0f ? *o : 0.0f;
+        *o = epi_apply(p.g.epi, v, old, b);
+      }
+    };
+    if (p.split == 1) {  // the thread's own sums
+      for (int c = group * 16; c < rows.count; c = (c & 15) == 15 ? c + 17 : c + 1)
+        store(c, part[c * TILE_N + tlane]);
+    } else {
+      for (int c = rank * 2 + group; c < rows.count; c += 2 * p.split) {
+        const uint32_t at = smem_u32(part + c * TILE_N + tlane);
+        float v = 0.0f;
+        for (int r = 0; r < p.split; ++r) v += ld_cluster_f32(map_to_rank(at, r));
+        store(c, v);
+      }
+    }
+  }
+  if (p.split > 1) cluster_sync();  // the others have read this CTA's sums
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, ACCS * COLS);
+  }
+}
+
+using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const FewArgs);
+Kernel kernel_of(int cols, bool square) {
+  if (cols <= 32) return square ? fp8_few_kernel<32, true> : fp8_few_kernel<32, false>;
+  return square ? fp8_few_kernel<128, true> : fp8_few_kernel<128, false>;
+}
+std::atomic<uint64_t> g_allowed[4], g_registers[2];
+
+// The shared-memory limit, and that the roles' register shares are there to be drawn
+// on (a larger share than the block was launched with would be waited for for ever).
+cudaError_t prepare(Kernel kernel, bool wide, bool square) {
+  cudaError_t e = allow_shared(kernel, kSmemBytes, &g_allowed[(wide ? 2 : 0) + (square ? 1 : 0)]);
+  if (e != cudaSuccess || !wide) return e;
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (g_registers[square ? 1 : 0].load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kernel);
+  if (e == cudaSuccess && fa.numRegs * THREADS < kRegsBlock) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess) g_registers[square ? 1 : 0].fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t fp8_few_plan(const Fp8GemmArgs& a, const LayerDevice& dev, Fp8FewPlan* plan) {
+  const int64_t n_tiles = (a.N + TILE_N - 1) / TILE_N;
+  const int64_t kbs = (static_cast<int64_t>(a.K) + BK - 1) / BK;
+  int64_t rows = a.M, units;
+  if (a.E > 0) rows = 2 * ((a.M + static_cast<int64_t>(a.E) - 1) / a.E);
+  const int64_t cols = rows > 112 ? 128 : (rows + 15) / 16 * 16;
+  if (a.E > 0) {  // at most floor(M / cols) full units and one ragged one an expert
+    units = a.M / cols + (a.E < a.M ? a.E : a.M);
+  } else {
+    units = (a.M + cols - 1) / cols;
+  }
+  plan->cols = static_cast<int>(cols);
+  plan->tiles = units * n_tiles;
+  const int64_t busy = plan->tiles;
+  int split = 1;
+  while (split < 8 && busy * split * 2 <= 2 * dev.sms && kbs >= 4 * split) split *= 2;
+  plan->split = split;
+  const int control = static_cast<int>(cols <= 32 ? sizeof(Control<32>) : sizeof(Control<128>));
+  int stages = (kSmemBytes - 1024 - control) / (B_BYTES + plan->cols * BK);
+  plan->stages = stages < MAX_STAGES ? stages : MAX_STAGES;
+  return plan->tiles * split <= 0x7FFFFFFF ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_fp8_few(const CUtensorMap& tmA, const CUtensorMap& tmB, const Fp8GemmArgs& a,
+                           const Fp8FewPlan& plan, unsigned int* status, cudaStream_t stream) {
+  const Kernel kernel = kernel_of(plan.cols, a.b_square);
+  cudaError_t e = prepare(kernel, plan.cols > 32, a.b_square);
+  if (e != cudaSuccess) return e;
+  const FewArgs p = {a, plan.cols, plan.stages, plan.split, (a.N + TILE_N - 1) / TILE_N, status};
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = plan.split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1] = pdl_attribute();
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.tiles * plan.split));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, p);
+  if (e == cudaSuccess) note_launches(1);
+  return e;
+}
+
+}  // namespace g07

@@ -1,4 +1,5 @@
-// layer_binding.cpp -- the Python binding of the layer operators: checks torch
+// layer_binding.cpp -- the Python binding of the layer operators (and of the 8-bit
+// products, routing and combining of a layer of experts): checks torch
 // tensors and passes their sizes, addresses and strides to the C entry points
 // of include/gemm07.h.  Compiled code, because at the sizes of a decode step a
 // call's own time is the operator's: marshalling a call in Python took 7 to 18
@@ -8,6 +9,7 @@
 // A refused argument raises ValueError or TypeError, a status of the library
 // GemmError, as in the rest of the package.
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -31,6 +33,7 @@ std::string text(at::ScalarType t) {
     case at::kFloat: return "torch.float32";
     case at::kBFloat16: return "torch.bfloat16";
     case at::kByte: return "torch.uint8";
+    case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn";
     default: return c10::toString(t);
   }
 }
@@ -424,6 +427,334 @@ Tensor ckpt8_wgrad(const Tensor& q, const Tensor& scales, int64_t T, int64_t K, 
   return out;
 }
 
+// ------------------------------------------- 8-bit floating-point products
+
+constexpr int64_t kBlock = 128;
+
+int64_t blocks(int64_t n) { return (n + kBlock - 1) / kBlock; }
+
+void code_rows(const Tensor& codes, const char* name, at::Device device) {
+  const std::string n = name;
+  if (codes.scalar_type() != at::kFloat8_e4m3fn) bad_type(n + " must be torch.float8_e4m3fn");
+  if (codes.device() != device) bad_value(n + " must be on " + device.str());
+  if (codes.size(-1) > 1 && codes.stride(-1) != 1)
+    bad_value(n + ": rows must be contiguous (stride(-1) == 1)");
+  if (reinterpret_cast<uintptr_t>(codes.data_ptr()) % 16)
+    bad_value(n + " must start on a 16-byte boundary");
+}
+
+// The row stride of codes (rows x K); a single row has one of its own.
+int64_t code_stride(int64_t rows, int64_t K, int64_t stride, const char* name) {
+  if (rows <= 1 || K == 0) return (K > 1 ? K + 15 : 16) / 16 * 16;
+  if (stride < K || stride % 16)
+    bad_value(std::string(name) + ": rows must be a multiple of 16 bytes apart (gemm_fp8_quantize "
+                                  "makes them so)");
+  return stride > 16 ? stride : 16;
+}
+
+// A rows x K matrix in 8 bits, after its checks.
+gemm_fp8_t fp8_matrix(const Tensor& codes, const Tensor& scales, bool square, const char* name,
+                      at::Device device) {
+  const std::string n = name;
+  if (codes.dim() != 2) bad_value(n + ".codes must be 2-D");
+  code_rows(codes, (n + ".codes").c_str(), device);
+  const int64_t R = codes.size(0), K = codes.size(1);
+  const int64_t ld_s = square ? matrix(scales, (n + ".scales").c_str(), {at::kFloat}, device,
+                                       blocks(R), blocks(K))
+                              : matrix(scales, (n + ".scales").c_str(), {at::kFloat}, device,
+                                       blocks(K), R);
+  return gemm_fp8_t{ptr(codes), code_stride(R, K, codes.stride(0), name), ptr<float>(scales), ld_s,
+                    square ? 1 : 0};
+}
+
+at::ScalarType product_type(const std::optional<at::ScalarType>& wanted, const Maybe& out) {
+  const at::ScalarType type = wanted ? *wanted : out ? out->scalar_type() : at::kFloat;
+  if (type != at::kFloat && type != at::kBFloat16)
+    bad_type("out_dtype must be torch.float32 or torch.bfloat16");
+  return type;
+}
+
+int32_t abi_type(at::ScalarType t) { return t == at::kBFloat16 ? GEMM_TYPE_BF16 : GEMM_TYPE_F32; }
+
+std::tuple<Tensor, Tensor> fp8_quantize(const Tensor& X, bool square, bool transpose,
+                                        const Maybe& index, const std::optional<int64_t>& stream) {
+  const at::Device device = cuda_device(X, "X");
+  gemm_fp8_quantize_args_t q = {};
+  q.batch = 1;
+  if (X.dim() == 3) {
+    if (!square) bad_value("X must be 2-D (3-D only with square)");
+    if (X.scalar_type() != at::kFloat && X.scalar_type() != at::kBFloat16)
+      bad_type("X must be torch.float32 or torch.bfloat16");
+    q.batch = X.size(0);
+    const int64_t T = X.size(1), C = X.size(2);
+    if (X.numel() > 0) {
+      if (C > 1 && X.stride(2) != 1) bad_value("X: rows must be contiguous (stride(-1) == 1)");
+      if (T > 1 && X.stride(1) < C) bad_value("X: rows must not overlap");
+      if (q.batch > 1 && X.stride(0) < 0) bad_value("X: matrices must not go backwards");
+    }
+    q.T = T;
+    q.C = C;
+    q.ldx = T > 1 && X.numel() > 0 ? X.stride(1) : C > 1 ? C : 1;
+    q.x_step = q.batch > 1 ? X.stride(0) : 0;
+  } else {
+    q.ldx = matrix(X, "X", {at::kFloat, at::kBFloat16}, device);
+    q.T = X.size(0);
+    q.C = X.size(1);
+  }
+  q.x = ptr(X);
+  q.x_type = type_of(X);
+  q.square = square;
+  q.transpose = transpose;
+  int64_t R = transpose ? q.C : q.T;
+  const int64_t K = transpose ? q.T : q.C;
+  if (index) {
+    if (square || transpose) bad_value("index goes without square and transpose");
+    if (index->dim() != 1 || index->scalar_type() != at::kInt || index->device() != device ||
+        !index->is_contiguous())
+      bad_value("index must be a contiguous int32 vector on " + device.str());
+    R = q.rows = index->size(0);
+    // (an empty index is no index, and has no rows)
+    q.index = ptr<int32_t>(*index);
+  }
+  // rows start on 128 bytes: a block is one line
+  const int64_t ld = K > 0 ? blocks(K) * kBlock : kBlock;
+  Tensor codes, scales;
+  if (X.dim() == 3) {
+    codes = empty({q.batch, R, ld}, at::kFloat8_e4m3fn, device).narrow(2, 0, K);
+    scales = empty({q.batch, blocks(R), blocks(K)}, at::kFloat, device);
+    q.codes_step = R * ld;
+    q.scales_step = blocks(R) * blocks(K);
+  } else {
+    codes = empty({R, ld}, at::kFloat8_e4m3fn, device).narrow(1, 0, K);
+    scales = square ? empty({blocks(R), blocks(K)}, at::kFloat, device)
+                    : empty({blocks(K), R}, at::kFloat, device);
+  }
+  if (codes.numel() == 0) return {codes, scales};
+  q.codes = ptr(codes);
+  q.ld = ld;
+  q.scales = ptr<float>(scales);
+  q.ld_scales = scales.size(-1) > 1 ? scales.size(-1) : 1;
+  run("gemm_fp8_quantize", device, stream, [&](void* s) { return gemm_fp8_quantize(&q, s); });
+  return {codes, scales};
+}
+
+Tensor fp8(const Tensor& a_codes, const Tensor& a_scales, bool a_square, const Tensor& b_codes,
+           const Tensor& b_scales, bool b_square, const Maybe& out_, double alpha, double beta,
+           const Maybe& bias, const std::string& act,
+           const std::optional<at::ScalarType>& out_dtype, const std::optional<int64_t>& stream) {
+  const at::Device device = cuda_device(a_codes, "a.codes");
+  if (a_square) bad_value("a must have a scale for each 128 values of a row (square=False)");
+  const gemm_fp8_t a = fp8_matrix(a_codes, a_scales, false, "a", device);
+  const gemm_fp8_t b = fp8_matrix(b_codes, b_scales, b_square, "b", device);
+  const int64_t M = a_codes.size(0), K = a_codes.size(1), N = b_codes.size(0);
+  if (b_codes.size(1) != K)
+    bad_value("inner sizes differ: a is " + text(M) + " x " + text(K) + ", b is " + text(N) +
+              " x " + text(b_codes.size(1)));
+  if (beta != 0.0 && !out_) bad_value("beta != 0 reads C: pass its prior contents as `out`");
+  const at::ScalarType type = product_type(out_dtype, out_);
+  int64_t ldc = 0;
+  Tensor out = output(out_, "out", M, N, type, device, &ldc);
+  if (bias) vector(*bias, "bias", device, N);
+  const gemm_epilogue_t epi = {static_cast<float>(alpha), static_cast<float>(beta),
+                               ptr<float>(bias), activation(act)};
+  run("gemm_fp8", device, stream, [&](void* s) {
+    return gemm_fp8(M, N, K, &a, &b, ptr(out), ldc, abi_type(type), &epi, s);
+  });
+  return out;
+}
+
+Tensor fp8_experts(const Tensor& a_codes, const Tensor& a_scales, bool a_square,
+                   const Tensor& b_codes, const Tensor& b_scales, bool b_square,
+                   const Tensor& offsets, const Maybe& out_, double alpha, double beta,
+                   const Maybe& bias, const std::string& act,
+                   const std::optional<at::ScalarType>& out_dtype,
+                   const std::optional<int64_t>& stream) {
+  const at::Device device = cuda_device(a_codes, "a.codes");
+  if (a_square) bad_value("a must have a scale for each 128 values of a row (square=False)");
+  const gemm_fp8_t a = fp8_matrix(a_codes, a_scales, false, "a", device);
+  const int64_t M = a_codes.size(0), K = a_codes.size(1);
+  if (!b_square || b_codes.dim() != 3)
+    bad_value("b must be E matrices with square scales: codes E x N x K");
+  code_rows(b_codes, "b.codes", device);
+  const int64_t E = b_codes.size(0), N = b_codes.size(1);
+  if (b_codes.size(2) != K)
+    bad_value("inner sizes differ: a is " + text(M) + " x " + text(K) + ", b holds " + text(N) +
+              " x " + text(b_codes.size(2)));
+  const int64_t ld = code_stride(E * N, K, N > 1 ? b_codes.stride(1) : b_codes.stride(0), "b");
+  if (E > 1 && N > 0 && K > 0 && b_codes.stride(0) != N * ld)
+    bad_value("b.codes: the matrices must follow each other (stride(0) == N * stride(1))");
+  if (b_scales.scalar_type() != at::kFloat || b_scales.device() != device ||
+      b_scales.dim() != 3 || b_scales.size(0) != E || b_scales.size(1) != blocks(N) ||
+      b_scales.size(2) != blocks(K) || !b_scales.is_contiguous())
+    bad_value("b.scales must be contiguous float32, E x ceil(N / 128) x ceil(K / 128), on " +
+              device.str());
+  if (offsets.dim() != 1 || offsets.size(0) != E + 1 || offsets.scalar_type() != at::kInt ||
+      offsets.device() != device || !offsets.is_contiguous())
+    bad_value("offsets must be a contiguous int32 vector of " + text(E + 1) + " elements on " +
+              device.str());
+  if (beta != 0.0 && !out_) bad_value("beta != 0 reads C: pass its prior contents as `out`");
+  const at::ScalarType type = product_type(out_dtype, out_);
+  int64_t ldc = 0;
+  Tensor out = output(out_, "out", M, N, type, device, &ldc);
+  if (bias && (bias->scalar_type() != at::kFloat || bias->device() != device || bias->dim() != 2 ||
+               bias->size(0) != E || bias->size(1) != N || !bias->is_contiguous()))
+    bad_value("bias must be contiguous float32, " + text(E) + " x " + text(N) + ", on " +
+              device.str());
+  const gemm_fp8_t b = {ptr(b_codes), ld, ptr<float>(b_scales), blocks(K) > 1 ? blocks(K) : 1, 1};
+  const gemm_epilogue_t epi = {static_cast<float>(alpha), static_cast<float>(beta),
+                               ptr<float>(bias), activation(act)};
+  run("gemm_fp8_experts", device, stream, [&](void* s) {
+    return gemm_fp8_experts(E, M, N, K, &a, &b, ptr<int32_t>(offsets), ptr(out), ldc,
+                            abi_type(type), &epi, s);
+  });
+  return out;
+}
+
+// ------------------------------------------------------------ experts
+
+int32_t score_of(const std::string& name) {
+  if (name == "softmax") return GEMM_ROUTE_SOFTMAX;
+  if (name == "sigmoid") return GEMM_ROUTE_SIGMOID;
+  bad_value("score must be 'softmax' or 'sigmoid'");
+}
+
+void pairs(const Tensor& t, const char* name, at::ScalarType type, at::Device device, int64_t T,
+           int64_t k) {
+  if (t.scalar_type() != type || t.device() != device || t.dim() != 2 || t.size(0) != T ||
+      t.size(1) != k || !t.is_contiguous())
+    bad_value(std::string(name) + " must be contiguous " + (type == at::kInt ? "int32" : "float32") +
+              ", " + text(T) + " x " + text(k) + ", on " + device.str());
+}
+
+gemm_route_args_t route_args(const Tensor& logits, int64_t k, const std::string& score,
+                             bool renormalize, double scale, at::Device device) {
+  gemm_route_args_t a = {};
+  a.ld = matrix(logits, "logits", {at::kFloat, at::kBFloat16}, device);
+  a.T = logits.size(0);
+  a.E = logits.size(1);
+  a.k = k;
+  a.logits = ptr(logits);
+  a.type = type_of(logits);
+  a.score = score_of(score);
+  a.groups = a.groups_kept = a.group_top = 1;
+  a.renormalize = renormalize;
+  a.scale = static_cast<float>(scale);
+  if (a.E < 1 || a.E > 1024) bad_value("there must be 1 to 1024 experts");
+  if (k < 1 || k > 32 || k > a.E) bad_value("k must be 1 to 32 of the experts");
+  return a;
+}
+
+std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor> route(
+    const Tensor& logits, int64_t k, const std::string& score, const Maybe& bias, int64_t groups,
+    int64_t groups_kept, int64_t group_top, bool renormalize, double scale,
+    const std::optional<int64_t>& stream) {
+  const at::Device device = cuda_device(logits, "logits");
+  gemm_route_args_t a = route_args(logits, k, score, renormalize, scale, device);
+  if (groups < 1 || groups > 32 || a.E % groups)
+    bad_value("groups must be 1 to 32 and divide the experts");
+  if (groups_kept < 1 || groups_kept > groups) bad_value("groups_kept must be 1 to groups");
+  if (group_top != 1 && group_top != 2) bad_value("group_top must be 1 or 2");
+  if (k > groups_kept * (a.E / groups)) bad_value("k is more than the experts of the groups kept");
+  if (bias) vector(*bias, "bias", device, a.E);
+  a.bias = ptr<float>(bias);
+  a.groups = static_cast<int32_t>(groups);
+  a.groups_kept = static_cast<int32_t>(groups_kept);
+  a.group_top = static_cast<int32_t>(group_top);
+  Tensor index = empty({a.T, k}, at::kInt, device), weight = empty({a.T, k}, at::kFloat, device);
+  Tensor slot = empty({a.T, k}, at::kInt, device), source = empty({a.T * k}, at::kInt, device);
+  Tensor offsets = empty({a.E + 1}, at::kInt, device);
+  const int64_t bytes = gemm_route_workspace_bytes(a.T, a.E);
+  Tensor workspace = empty({bytes > 0 ? bytes : 0}, at::kByte, device);
+  run("gemm_route", device, stream, [&](void* s) {
+    return gemm_route(&a, ptr<int32_t>(index), ptr<float>(weight), ptr<int32_t>(slot),
+                      ptr<int32_t>(source), ptr<int32_t>(offsets), ptr(workspace), s);
+  });
+  // On another stream than the current one the workspace is kept until that
+  // stream's work has finished; the caller keeps the outputs.
+  if (stream && bytes > 0)
+    c10::cuda::CUDACachingAllocator::recordStream(
+        workspace.storage().data_ptr(),
+        c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(*stream), device.index()));
+  return {index, weight, slot, source, offsets};
+}
+
+Tensor route_bwd(const Tensor& logits, const Tensor& index, const Tensor& d_weight,
+                 const std::string& score, bool renormalize, double scale, const Maybe& out_,
+                 const std::optional<int64_t>& stream) {
+  const at::Device device = cuda_device(logits, "logits");
+  if (index.dim() != 2) bad_value("index must be 2-D");
+  const int64_t k = index.size(1);
+  const gemm_route_args_t a = route_args(logits, k, score, renormalize, scale, device);
+  pairs(index, "index", at::kInt, device, a.T, k);
+  pairs(d_weight, "d_weight", at::kFloat, device, a.T, k);
+  int64_t ld = 0;
+  Tensor out = output(out_, "out", a.T, a.E, logits.scalar_type(), device, &ld);
+  run("gemm_route_bwd", device, stream, [&](void* s) {
+    return gemm_route_bwd(&a, ptr<int32_t>(index), ptr<float>(d_weight), ptr(out), ld, s);
+  });
+  return out;
+}
+
+gemm_combine_args_t combine_args(const Tensor& rows, const Tensor& slot, const Tensor& weight,
+                                 at::Device device) {
+  gemm_combine_args_t a = {};
+  a.ld_rows = matrix(rows, "rows", {at::kFloat, at::kBFloat16}, device);
+  if (slot.dim() != 2) bad_value("slot must be 2-D");
+  a.T = slot.size(0);
+  a.k = slot.size(1);
+  if (a.k > 32) bad_value("a token has at most 32 rows");
+  a.D = rows.size(1);
+  a.R = rows.size(0);
+  pairs(slot, "slot", at::kInt, device, a.T, a.k);
+  pairs(weight, "weight", at::kFloat, device, a.T, a.k);
+  a.rows = ptr(rows);
+  a.rows_type = type_of(rows);
+  a.slot = ptr<int32_t>(slot);
+  a.weight = ptr<float>(weight);
+  a.ldx = a.D > 1 ? a.D : 1;
+  return a;
+}
+
+Tensor combine(const Tensor& rows, const Tensor& slot, const Tensor& weight, const Maybe& x,
+               const Maybe& out_, const std::optional<at::ScalarType>& out_dtype,
+               const std::optional<int64_t>& stream) {
+  const at::Device device = cuda_device(rows, "rows");
+  gemm_combine_args_t a = combine_args(rows, slot, weight, device);
+  if (x) {
+    a.ldx = matrix(*x, "x", {at::kFloat, at::kBFloat16}, device, a.T, a.D);
+    a.x = ptr(*x);
+    a.x_type = type_of(*x);
+  }
+  const at::ScalarType type =
+      product_type(out_dtype ? out_dtype
+                             : out_ ? std::optional<at::ScalarType>(out_->scalar_type())
+                                    : std::optional<at::ScalarType>(
+                                          x ? x->scalar_type() : rows.scalar_type()),
+                   out_);
+  int64_t ld = 0;
+  Tensor out = output(out_, "out", a.T, a.D, type, device, &ld);
+  run("gemm_combine", device, stream,
+      [&](void* s) { return gemm_combine(&a, ptr(out), ld, abi_type(type), s); });
+  return out;
+}
+
+std::tuple<Tensor, Tensor> combine_bwd(const Tensor& d_out, const Tensor& rows, const Tensor& slot,
+                                       const Tensor& weight, const Maybe& d_rows_,
+                                       const std::optional<int64_t>& stream) {
+  const at::Device device = cuda_device(rows, "rows");
+  const gemm_combine_args_t a = combine_args(rows, slot, weight, device);
+  const int64_t ld_d =
+      matrix(d_out, "d_out", {at::kFloat, at::kBFloat16}, device, a.T, a.D);
+  int64_t ld = 0;
+  Tensor d_rows = output(d_rows_, "d_rows", a.R, a.D, rows.scalar_type(), device, &ld);
+  Tensor d_weight = empty({a.T, a.k}, at::kFloat, device);
+  run("gemm_combine_bwd", device, stream, [&](void* s) {
+    return gemm_combine_bwd(&a, ptr(d_out), ld_d, type_of(d_out), ptr(d_rows), ld,
+                            ptr<float>(d_weight), s);
+  });
+  return {d_rows, d_weight};
+}
+
 }  // namespace
 
 PYBIND11_MODULE(layer_binding, m) {
@@ -437,4 +768,11 @@ PYBIND11_MODULE(layer_binding, m) {
   m.def("ckpt8_unpack", &ckpt8_unpack);
   m.def("ckpt8_act_grad", &ckpt8_act_grad);
   m.def("ckpt8_wgrad", &ckpt8_wgrad);
+  m.def("fp8_quantize", &fp8_quantize);
+  m.def("fp8", &fp8);
+  m.def("fp8_experts", &fp8_experts);
+  m.def("route", &route);
+  m.def("route_bwd", &route_bwd);
+  m.def("combine", &combine);
+  m.def("combine_bwd", &combine_bwd);
 }

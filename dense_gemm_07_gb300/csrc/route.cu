@@ -1,0 +1,645 @@
+// route.cu -- tokens to experts: scores, the choice of k of them, their weights, and
+// the order that sorts the chosen (token, expert) pairs by expert.
+//
+// A warp takes a token, lane l its experts l, l + 32, ....  The choice compares
+// score + bias, numbers that may be closer than FP32 tells apart, so it is made in
+// FP32 first, with a bound on the error of each difference; where one of the
+// comparisons that decide the outcome falls below it, the token is chosen again in
+// 64 bits (about one token in a thousand).  Without a bias the scores are in the
+// order of the logits, which need no rounding.  Ties go to the lowest index.
+//
+// Sorting: a block takes 128 tokens and holds a bit for each (expert, token), so
+// that a pair's place among its expert's is a count of bits: no atomics on places,
+// and tokens stay in order.  With more than one block the counts go through memory
+// and a second kernel adds up those of the blocks before.
+//
+// Memory bounds the large sizes (the logits are read once), latency the small ones.
+#include <cfloat>
+
+#include "experts.h"
+#include "kernels.h"
+
+namespace g07 {
+namespace {
+
+constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr int kChunk = kRouteChunk;
+constexpr int kWords = kChunk / 32;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+
+// FP32 and 64-bit values as unsigned numbers in the same order; 0 is below all of
+// them and stands for "not to be chosen": NaN and -infinity.
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return v > -INFINITY ? b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u)
+                       : 0u;
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+__device__ __forceinline__ unsigned long long key_of(double v) {
+  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(v));
+  return v > -INFINITY
+             ? b ^ (static_cast<unsigned long long>(static_cast<long long>(b) >> 63) | (1ull << 63))
+             : 0ull;
+}
+__device__ __forceinline__ double value_of(unsigned long long key) {
+  return __longlong_as_double(
+      static_cast<long long>(key >> 63 ? key ^ (1ull << 63) : ~key));
+}
+// -0 and +0 are equal numbers; keys have to be too.
+template <typename V>
+__device__ __forceinline__ V plain_zero(V v) {
+  return v == V(0) ? V(0) : v;
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kAll, v); }
+__device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
+  const uint32_t hi = static_cast<uint32_t>(v >> 32), top = __reduce_max_sync(kAll, hi);
+  const uint32_t lo = __reduce_max_sync(kAll, hi == top ? static_cast<uint32_t>(v) : 0u);
+  return static_cast<unsigned long long>(top) << 32 | lo;
+}
+
+struct Choice {
+  int index;   // lane j < k: the j-th expert or -1
+  bool close;  // a comparison was too close to tell
+};
+
+// The k largest keys, lowest index first among equals.  key[i] belongs to expert
+// i * 32 + lane.  `told(a, b)`: whether two values, a >= b, that follow each other
+// are surely in that order; same(i, j): whether experts i and j are equal in
+// everything.
+template <int V, typename Key, typename Told, typename Same>
+__device__ __forceinline__ Choice pick(Key (&key)[V], int k, Told told, Same same) {
+  const int lane = threadIdx.x & 31;
+  Choice c{-1, false};
+  Key mine = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) mine = key[i] > mine ? key[i] : mine;
+  Key last = 0;
+  int last_at = -1;
+  for (int j = 0; j <= k; ++j) {  // one more than are chosen: the first that is not
+    const Key top = warp_max(mine);
+    if (top == 0) break;
+    int at = 0x7FFFFFFF;
+    if (mine == top) {
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i)
+        if (key[i] == top) at = i * 32 + lane;
+    }
+    at = static_cast<int>(__reduce_min_sync(kAll, static_cast<unsigned>(at)));
+    if (j > 0 && !told(value_of(last), value_of(top)) && !same(last_at, at)) c.close = true;
+    if (j == k) break;
+    if (lane == j) c.index = at;
+    last = top;
+    last_at = at;
+    if ((at & 31) == lane) {
+      mine = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (i == at >> 5) key[i] = 0;
+        mine = key[i] > mine ? key[i] : mine;
+      }
+    }
+  }
+  return c;
+}
+
+// Leaves only the keys of the `kept` groups with the largest sums of their
+// group_top (1 or 2) largest values; a group without a key that can be chosen is
+// last.  True when it was too close to tell.
+template <int V, typename Key, typename Told>
+__device__ __forceinline__ bool keep_groups(Key (&key)[V], int groups, int size, int kept,
+                                            int group_top, Told told) {
+  const int lane = threadIdx.x & 31;
+  Key sum = 0;  // lane g: group g
+  for (int g = 0; g < groups; ++g) {
+    const int lo = g * size, hi = lo + size;
+    Key mine = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = i * 32 + lane;
+      if (e >= lo && e < hi && key[i] > mine) mine = key[i];
+    }
+    const Key first = warp_max(mine);
+    Key score = first;
+    if (group_top > 1 && first != 0) {
+      const int holder = __ffs(__ballot_sync(kAll, mine == first)) - 1;
+      Key next = mine;
+      if (lane == holder) {  // its second largest; the largest once
+        next = 0;
+        bool seen = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int e = i * 32 + lane;
+          if (e >= lo && e < hi) {
+            if (!seen && key[i] == first)
+              seen = true;
+            else if (key[i] > next)
+              next = key[i];
+          }
+        }
+      }
+      const Key second = warp_max(next);
+      if (second != 0) score = key_of(plain_zero(value_of(first) + value_of(second)));
+    }
+    if (lane == g) sum = score;
+  }
+  unsigned keep = 0;
+  Key last = 0;
+  bool close = false;
+  for (int j = 0; j <= kept; ++j) {
+    const Key top = warp_max(sum);
+    if (j == kept) {
+      close = top != 0 && !told(value_of(last), value_of(top));
+      break;
+    }
+    if (top == 0) break;  // the others have nothing to choose
+    const int at = __ffs(__ballot_sync(kAll, sum == top)) - 1;
+    keep |= 1u << at;
+    if (lane == at) sum = 0;
+    last = top;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int g = (i * 32 + lane) / size;
+    if (g >= groups || !(keep >> g & 1u)) key[i] = 0;
+  }
+  return close;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  return v;
+}
+
+// The choice in 64 bits, from the definition.
+template <int V>
+__device__ __noinline__ int choose_64(const RouteArgs& a, const float (&l)[V], float top) {
+  const int lane = threadIdx.x & 31;
+  double s[V], total = 0.0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    s[i] = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l[i])))
+                     : exp(static_cast<double>(l[i]) - static_cast<double>(top));
+    total += s[i];
+  }
+  if (!a.sigmoid) total = warp_sum(total);
+  unsigned long long key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = i * 32 + lane;
+    double v = a.sigmoid ? s[i] : s[i] / total;
+    if (a.bias && e < a.E) v += static_cast<double>(__ldg(a.bias + e));
+    key[i] = l[i] > -INFINITY ? key_of(plain_zero(v)) : 0ull;
+  }
+  auto told = [](double, double) { return true; };
+  if (a.kept < a.groups) keep_groups<V>(key, a.groups, a.E / a.groups, a.kept, a.group_top, told);
+  if (!a.bias) {  // in the order of the logits
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (key[i] != 0) key[i] = key_of(plain_zero(static_cast<double>(l[i])));
+  }
+  return pick<V>(key, a.k, told, [](int, int) { return true; }).index;
+}
+
+// Experts (lane j: the j-th or -1) and weights of a token from its logits
+// (-infinity past the last expert).
+template <int V>
+__device__ __forceinline__ int route_token(const RouteArgs& a, const float (&l)[V], float* weight) {
+  const int lane = threadIdx.x & 31;
+  bool nan = false;
+  float mine = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    nan |= l[i] != l[i];
+    mine = fmaxf(mine, l[i]);
+  }
+  const float top = value_of(warp_max(key_of(plain_zero(mine))));  // (NaN: no key)
+  const bool any = __any_sync(kAll, mine > -INFINITY);
+  nan = __any_sync(kAll, nan);
+  // Scores that are not numbers choose nothing, and show in the weights.
+  if (nan || (!a.sigmoid && any && top == INFINITY)) {
+    *weight = __int_as_float(0x7FC00000);
+    return -1;
+  }
+  if (!any) {
+    *weight = 0.0f;
+    return -1;
+  }
+
+  // Softmax's sum over all: for the weights themselves unless they are
+  // renormalised, else for the choice alone.
+  const bool scores = a.bias || (a.kept < a.groups && a.group_top > 1);
+  float total = 1.0f;
+  float s[V];
+  if (a.sigmoid) {
+    if (scores) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] = __fdividef(1.0f, 1.0f + __expf(-l[i]));
+    }
+  } else if (scores || !a.renorm) {
+    total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      s[i] = expf(l[i] - top);
+      total += s[i];
+    }
+    total = warp_sum(total);
+    const float inverse = __fdividef(1.0f, total);
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] *= inverse;
+  }
+
+  // How far a difference of two scores in FP32 may be off.  Sigmoid: the
+  // exponential's 2 + 1.2 |l| units in the last place weigh s (1 - s), at most 1/4
+  // and with |l| 0.23, the quotient adds 2 units; softmax: 2 units each for
+  // exponential, sum (of up to 1024 numbers, 32 a lane and 5 steps: 40) and
+  // quotient, of at most the largest score.  Two scores, and half a unit of each
+  // sum with the bias.
+  const float unit = 1.2e-7f;
+  const float slack = a.sigmoid ? 8.0f * unit : 96.0f * unit * __fdividef(1.0f, total);
+  auto told = [&](float hi, float lo) {
+    return hi - lo > slack + 2.0f * unit * fmaxf(fabsf(hi), fabsf(lo));
+  };
+  auto told_sum = [&](float hi, float lo) {
+    return hi - lo > 2.0f * slack + 6.0f * unit * (fabsf(hi) + fabsf(lo) + 1.0f);
+  };
+  auto exact = [](float, float) { return true; };
+
+  uint32_t key[V];
+  bool close = false;
+  if (a.kept < a.groups) {
+    if (scores) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = i * 32 + lane;
+        const float v = s[i] + (a.bias && e < a.E ? __ldg(a.bias + e) : 0.0f);
+        key[i] = l[i] > -INFINITY ? key_of(plain_zero(v)) : 0u;
+      }
+      close = keep_groups<V>(key, a.groups, a.E / a.groups, a.kept, a.group_top, told_sum);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = key_of(plain_zero(l[i]));
+      keep_groups<V>(key, a.groups, a.E / a.groups, a.kept, a.group_top, exact);
+    }
+    if (!a.bias) {  // within the groups by the logits
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (key[i] != 0) key[i] = key_of(plain_zero(l[i]));
+    }
+  } else if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = i * 32 + lane;
+      key[i] = l[i] > -INFINITY && e < a.E ? key_of(plain_zero(s[i] + __ldg(a.bias + e))) : 0u;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = key_of(plain_zero(l[i]));
+  }
+
+  auto logit = [&](int e) {  // of any expert, in every lane
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float x = __shfl_sync(kAll, l[i], e & 31);
+      if (i == e >> 5) v = x;
+    }
+    return v;
+  };
+  int at;
+  if (a.bias) {
+    const Choice c = pick<V>(key, a.k, told, [&](int i, int j) {
+      return logit(i) == logit(j) && __ldg(a.bias + i) == __ldg(a.bias + j);
+    });
+    at = c.index;
+    close |= c.close;
+  } else {
+    at = pick<V>(key, a.k, exact, [](int, int) { return true; }).index;
+  }
+  if (close) at = choose_64<V>(a, l, top);
+
+  // Weights, from the scores without the bias.
+  float chosen = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float x = __shfl_sync(kAll, l[i], at & 31);
+    if (i == at >> 5) chosen = x;
+  }
+  float w = 0.0f;
+  if (a.sigmoid) {
+    if (at >= 0) w = 1.0f / (1.0f + expf(-chosen));
+  } else if (!a.renorm) {
+    if (at >= 0) w = expf(chosen - top) / total;
+  } else {
+    const float most = value_of(warp_max(at >= 0 ? key_of(plain_zero(chosen)) : 0u));
+    if (at >= 0) w = expf(chosen - most);
+  }
+  if (a.renorm) {
+    const float sum = warp_sum(w);
+    w = sum > 0.0f ? w / sum : 0.0f;
+  }
+  *weight = w * a.scale;
+  return at;
+}
+
+// A block of 128 tokens: choices, weights and, for a single block, the sorted order;
+// else the number of its tokens for each expert.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
+  extern __shared__ uint32_t bits[];  // [E][kWords]: the tokens of each expert; then [E] starts
+  __shared__ int warp_total[kWarps];
+  grid_dependency_wait();
+  grid_dependents_go();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t0 = static_cast<int>(blockIdx.x) * kChunk;
+  const int tokens = a.T - t0 < kChunk ? a.T - t0 : kChunk;
+  for (int i = threadIdx.x; i < a.E * kWords; i += kThreads) bits[i] = 0;
+  __syncthreads();
+  auto load = [&](int t, float (&l)[V]) {
+    const T* row = static_cast<const T*>(a.logits) + (t0 + t) * a.ld;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      l[i] = i * 32 + lane < a.E ? to_f32(row[i * 32 + lane]) : -INFINITY;
+  };
+  constexpr bool kAhead = V <= 8;  // a token's logits are on their way while one is chosen
+  float l[V];
+  if (kAhead && warp < tokens) load(warp, l);
+  for (int t = warp; t < tokens; t += kWarps) {
+    float now[V];
+    if (!kAhead) load(t, l);
+#pragma unroll
+    for (int i = 0; i < V; ++i) now[i] = l[i];
+    if (kAhead && t + kWarps < tokens) load(t + kWarps, l);
+    float w;
+    const int at = route_token<V>(a, now, &w);
+    if (lane < a.k) {
+      const int64_t o = static_cast<int64_t>(t0 + t) * a.k + lane;
+      a.index[o] = at;
+      a.weight[o] = w;
+      if (at >= 0) atomicOr(&bits[at * kWords + (t >> 5)], 1u << (t & 31));
+    }
+  }
+  __syncthreads();
+  auto count = [&](int e) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) n += __popc(bits[e * kWords + i]);
+    return n;
+  };
+  if (gridDim.x > 1) {
+    for (int e = threadIdx.x; e < a.E; e += kThreads)
+      a.counts[static_cast<int64_t>(blockIdx.x) * a.E + e] = count(e);
+    return;
+  }
+  // The only block: each thread holds the experts 2 i and 2 i + 1.
+  int* start = reinterpret_cast<int*>(bits + a.E * kWords);
+  const int e0 = 2 * static_cast<int>(threadIdx.x);
+  const int n0 = e0 < a.E ? count(e0) : 0, n1 = e0 + 1 < a.E ? count(e0 + 1) : 0;
+  int upto = n0 + n1;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int v = __shfl_up_sync(kAll, upto, d);
+    if (lane >= d) upto += v;
+  }
+  if (lane == 31) warp_total[warp] = upto;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int i = 0; i < kWarps; ++i) {
+    before += i < warp ? warp_total[i] : 0;
+    all += warp_total[i];
+  }
+  const int at0 = before + upto - n0 - n1;
+  if (e0 < a.E) {
+    start[e0] = at0;
+    a.offsets[e0] = at0;
+  }
+  if (e0 + 1 < a.E) {
+    start[e0 + 1] = at0 + n0;
+    a.offsets[e0 + 1] = at0 + n0;
+  }
+  if (threadIdx.x == 0) a.offsets[a.E] = all;
+  __syncthreads();
+  const int pairs = tokens * a.k;
+  for (int i = threadIdx.x; i < pairs; i += kThreads) {
+    const int t = i / a.k, e = a.index[i];
+    int place = -1;
+    if (e >= 0) {
+      place = start[e];
+      for (int w = 0; w < t >> 5; ++w) place += __popc(bits[e * kWords + w]);
+      place += __popc(bits[e * kWords + (t >> 5)] & ((1u << (t & 31)) - 1u));
+      a.source[place] = t;
+    }
+    a.slot[i] = place;
+    if (i >= all) a.source[i] = -1;
+  }
+}
+
+// The sorted order, a block for each 128 tokens, from the counts of all blocks.
+__global__ void __launch_bounds__(1024) route_sort_kernel(RouteArgs a) {
+  extern __shared__ uint32_t bits[];  // [E][kWords], then [E] starts
+  __shared__ int warp_total[32];
+  grid_dependency_wait();
+  grid_dependents_go();
+  int* start = reinterpret_cast<int*>(bits + a.E * kWords);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int chunks = static_cast<int>(gridDim.x), chunk = static_cast<int>(blockIdx.x);
+  const int t0 = chunk * kChunk;
+  const int tokens = a.T - t0 < kChunk ? a.T - t0 : kChunk;
+  for (int i = threadIdx.x; i < a.E * (kWords + 1); i += 1024) bits[i] = 0;
+  __syncthreads();
+  // an expert's counts: all of them, and those before this block.  Few experts
+  // share their column among several threads.
+  const int parts = 1024 / a.E > 0 ? 1024 / a.E : 1;
+  const int e = static_cast<int>(threadIdx.x) % a.E, part = static_cast<int>(threadIdx.x) / a.E;
+  int total = 0, earlier = 0;
+  if (part < parts) {
+#pragma unroll 8
+    for (int c = part; c < chunks; c += parts) {
+      const int n = __ldg(a.counts + static_cast<int64_t>(c) * a.E + e);
+      total += n;
+      earlier += c < chunk ? n : 0;
+    }
+    // (sums of whole numbers: the order of the atomics does not matter)
+    atomicAdd(&start[e], total);
+    atomicAdd(reinterpret_cast<int*>(&bits[e * kWords]), earlier);
+  }
+  __syncthreads();
+  const bool mine = static_cast<int>(threadIdx.x) < a.E;
+  const int n = mine ? start[threadIdx.x] : 0;
+  earlier = mine ? static_cast<int>(bits[threadIdx.x * kWords]) : 0;
+  int upto = n;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int v = __shfl_up_sync(kAll, upto, d);
+    if (lane >= d) upto += v;
+  }
+  if (lane == 31) warp_total[warp] = upto;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int i = 0; i < 32; ++i) {
+    before += i < warp ? warp_total[i] : 0;
+    all += warp_total[i];
+  }
+  if (mine) {
+    start[threadIdx.x] = before + upto - n + earlier;
+    bits[threadIdx.x * kWords] = 0;
+    if (chunk == 0) a.offsets[threadIdx.x] = before + upto - n;
+  }
+  if (chunk == 0 && threadIdx.x == 0) a.offsets[a.E] = all;
+  __syncthreads();
+  const int pairs = tokens * a.k;
+  const int64_t first = static_cast<int64_t>(t0) * a.k;
+  for (int i = threadIdx.x; i < pairs; i += 1024) {
+    const int x = a.index[first + i], t = i / a.k;
+    if (x >= 0) atomicOr(&bits[x * kWords + (t >> 5)], 1u << (t & 31));
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < pairs; i += 1024) {
+    const int t = i / a.k, x = a.index[first + i];
+    int place = -1;
+    if (x >= 0) {
+      place = start[x];
+      for (int w = 0; w < t >> 5; ++w) place += __popc(bits[x * kWords + w]);
+      place += __popc(bits[x * kWords + (t >> 5)] & ((1u << (t & 31)) - 1u));
+      a.source[place] = t0 + t;
+    }
+    a.slot[first + i] = place;
+    if (first + i >= all) a.source[first + i] = -1;
+  }
+}
+
+// The gradient of the weights with respect to a token's logits: with w_j = scale *
+// s_j (/ S, S = sum of the chosen s when renormalised), d the gradient of w,
+//   ds_j = scale * (d_j - sum_i d_i s_i / S) / S   (scale * d_j),
+// then sigmoid: ds s (1 - s); softmax: s (ds - sum ds s), which for renormalised
+// weights is a softmax over the chosen experts alone, and 0 for all others.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) route_bwd_kernel(RouteArgs a) {
+  grid_dependency_wait();
+  grid_dependents_go();
+  const int lane = threadIdx.x & 31;
+  const int t = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+  int at = -1;
+  float d = 0.0f, l = 0.0f;
+  if (lane < a.k) {
+    const int64_t o = static_cast<int64_t>(t) * a.k + lane;
+    at = __ldg(a.chosen + o);
+    if (at < 0 || at >= a.E) at = -1;
+    if (at >= 0) {
+      d = a.scale * __ldg(a.d_weight + o);
+      l = to_f32(row[at]);
+    }
+  }
+  float g = 0.0f;       // of the chosen logit
+  float rest = 0.0f;    // softmax over all: every expert's share of it
+  float top = 0.0f;
+  const bool over_all = !a.sigmoid && !a.renorm;
+  float all[V];
+  if (a.sigmoid) {
+    const float s = at >= 0 ? 1.0f / (1.0f + expf(-l)) : 0.0f;
+    if (a.renorm) {
+      const float sum = warp_sum(s);
+      const float inverse = sum > 0.0f ? 1.0f / sum : 0.0f;
+      d = (d - warp_sum(d * s) * inverse) * inverse;
+    }
+    g = at >= 0 ? d * s / (1.0f + expf(l)) : 0.0f;
+  } else if (a.renorm) {
+    float most = at >= 0 ? l : -INFINITY;
+#pragma unroll
+    for (int i = 16; i; i >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, i));
+    float s = at >= 0 ? expf(l - most) : 0.0f;
+    const float sum = warp_sum(s);
+    s = sum > 0.0f ? s / sum : s;
+    const float dot = warp_sum(d * s);
+    g = s * (d - dot);
+  } else {
+    top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      all[i] = i * 32 + lane < a.E ? to_f32(row[i * 32 + lane]) : -INFINITY;
+      top = fmaxf(top, all[i]);
+    }
+#pragma unroll
+    for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, i));
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      all[i] = expf(all[i] - top);
+      sum += all[i];
+    }
+    sum = warp_sum(sum);
+    const float s = at >= 0 ? expf(l - top) / sum : 0.0f;
+    g = s * d;
+    const float dot = warp_sum(g);
+    rest = -dot / sum;
+  }
+  T* out = static_cast<T*>(a.d_logits) + t * a.ld_d;
+  float o[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = over_all ? all[i] * rest : 0.0f;
+  for (int j = 0; j < a.k; ++j) {  // in the order of the choice: the same expert twice adds up
+    const int e = __shfl_sync(kAll, at, j);
+    const float v = __shfl_sync(kAll, g, j);
+    if (e >= 0 && (e & 31) == lane) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i == e >> 5) o[i] += v;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i * 32 + lane < a.E) out[i * 32 + lane] = from_f32<T>(o[i]);
+}
+
+template <int V>
+cudaError_t route_of(const RouteArgs& a, bool gradient, cudaStream_t stream) {
+  if (gradient) {
+    const dim3 grid((a.T + 7) / 8);
+    const cudaError_t e =
+        a.bf16 ? launch_pdl(route_bwd_kernel<__nv_bfloat16, V>, grid, dim3(256), 0, stream, a)
+               : launch_pdl(route_bwd_kernel<float, V>, grid, dim3(256), 0, stream, a);
+    if (e == cudaSuccess) note_launches(1);
+    return e;
+  }
+  const int chunks = a.T > kChunk ? (a.T + kChunk - 1) / kChunk : 1;  // (no token: offsets of 0)
+  const size_t smem = static_cast<size_t>(a.E) * (kWords + 1) * 4;  // at most 20 KB
+  cudaError_t e = a.bf16 ? launch_pdl(route_kernel<__nv_bfloat16, V>, dim3(chunks), dim3(kThreads),
+                                      smem, stream, a)
+                         : launch_pdl(route_kernel<float, V>, dim3(chunks), dim3(kThreads), smem,
+                                      stream, a);
+  if (e == cudaSuccess && chunks > 1)
+    e = launch_pdl(route_sort_kernel, dim3(chunks), dim3(1024), smem, stream, a);
+  if (e == cudaSuccess) note_launches(chunks > 1 ? 2 : 1);
+  return e;
+}
+
+cudaError_t by_experts(const RouteArgs& a, bool gradient, cudaStream_t stream) {
+  if (a.E <= 32) return route_of<1>(a, gradient, stream);
+  if (a.E <= 64) return route_of<2>(a, gradient, stream);
+  if (a.E <= 128) return route_of<4>(a, gradient, stream);
+  if (a.E <= 256) return route_of<8>(a, gradient, stream);
+  if (a.E <= 512) return route_of<16>(a, gradient, stream);
+  return route_of<32>(a, gradient, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
+  return by_experts(a, false, stream);
+}
+cudaError_t launch_route_bwd(const RouteArgs& a, cudaStream_t stream) {
+  return by_experts(a, true, stream);
+}
+
+}  // namespace g07

@@ -642,6 +642,181 @@ GEMM07_API int64_t gemm_ckpt8_wgrad_units(int64_t T, int64_t K, int64_t N,
                                           int32_t max_pairs, int32_t pair,
                                           int64_t *out, int64_t cap);
 
+/* ------------------------------------------------------------------------
+ * 8-bit floating-point products, and a layer of experts made of them.  The same
+ * conventions; sizes are at most 2^30.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * A rows x K matrix in 8-bit floating point: element (r, k) is
+ *   E4M3 code at codes + r * ld + k  times  its scale (FP32),
+ * where 128 consecutive k of a row share a scale (square == 0),
+ *   scales[(k / 128) * ld_scales + r],          ld_scales >= rows,
+ * or 128 of them in 128 rows do (square == 1),
+ *   scales[(r / 128) * ld_scales + k / 128],    ld_scales >= ceil(K / 128).
+ * codes start on 16 bytes and ld is a multiple of 16 bytes, at least K (the copy
+ * engine reads them in place; bytes of a row past K may hold anything).
+ */
+typedef struct gemm_fp8 {
+    const void *codes;
+    int64_t ld;
+    const float *scales;
+    int64_t ld_scales;
+    int32_t square;
+} gemm_fp8_t;
+
+/*
+ * gemm_fp8_quantize -- X (T x C, x_type, row stride ldx) in 8-bit floating point.
+ *   The scale of a block of 128 (or 128 x 128) values is the smallest power of two
+ *   2^e (-126 <= e) with max|x| <= 448 * 2^e; a code is x / 2^e rounded to the
+ *   nearest E4M3 number, ties to even.  A block with a value that is not finite has
+ *   the scale 1 and every code NaN.
+ *   transpose: the codes are those of X^T (C x T).
+ *   index: NULL, or `rows` row numbers of X: row i of the codes is row index[i] of X,
+ *     zeros where that is outside 0 .. T - 1 (not with square or transpose).
+ *   batch: matrices, `x_step` elements, `codes_step` bytes and `scales_step` floats
+ *     apart (only with square; 1 otherwise), at most 65535.
+ * The codes have T rows (C when transposed, `rows` with an index), each scale as in
+ * gemm_fp8_t.  Bytes of a row of codes past its length are left as they were.
+ */
+typedef struct gemm_fp8_quantize_args {
+    int64_t T, C;
+    const void *x;
+    int64_t ldx;
+    int32_t x_type;
+    int32_t square, transpose;
+    const int32_t *index;
+    int64_t rows;
+    int64_t batch, x_step;
+    void *codes;
+    int64_t ld, codes_step;
+    float *scales;
+    int64_t ld_scales, scales_step;
+} gemm_fp8_quantize_args_t;
+
+GEMM07_API gemm_status_t gemm_fp8_quantize(const gemm_fp8_quantize_args_t *args, void *stream);
+
+/*
+ * gemm_fp8 -- C := act(alpha * A * B^T + beta * C + bias), A M x K with a scale for
+ * each 128 values of a row, B N x K likewise (a weight gradient's factors) or with
+ * square scales (weights, a row for each column of C), C M x N of type c_type,
+ * epilogue as for gemm_bf16_f32acc_ex (NULL: the product).
+ *   The products of codes of a block of 128 k are added on the tensor cores, their
+ *   sum times both scales in FP32; C is rounded once.
+ *   Gradients are the same operator: dA from dC quantised by rows and B transposed
+ *   (gemm_fp8_quantize with square and transpose); dB from dC and A both transposed.
+ */
+GEMM07_API gemm_status_t gemm_fp8(int64_t M, int64_t N, int64_t K, const gemm_fp8_t *A,
+                                  const gemm_fp8_t *B, void *C, int64_t ldc, int32_t c_type,
+                                  const gemm_epilogue_t *epilogue, void *stream);
+
+/*
+ * gemm_fp8_experts -- gemm_fp8 of rows sorted by expert, each with its expert's B:
+ * rows offsets[e] .. offsets[e + 1] - 1 of A and C are expert e's.
+ *   E: 1 .. 1024 experts; B: E * N rows, expert e's from row e * N on, square scales:
+ *   expert e's from row e * ceil(N / 128) of scales on.
+ *   offsets: E + 1 numbers on the device, held to 0 .. M and to their running
+ *   maximum.  Rows of C before offsets[0] and from offsets[E] on are left as they were.
+ *   epilogue: bias is E x N (row e: expert e's).
+ */
+GEMM07_API gemm_status_t gemm_fp8_experts(int64_t E, int64_t M, int64_t N, int64_t K,
+                                          const gemm_fp8_t *A, const gemm_fp8_t *B,
+                                          const int32_t *offsets, void *C, int64_t ldc,
+                                          int32_t c_type, const gemm_epilogue_t *epilogue,
+                                          void *stream);
+
+/*
+ * gemm_route -- k of E experts for each of T tokens, from logits (T x E, type, row
+ * stride ld).
+ *   Scores s: softmax over the E logits, or the sigmoid of each.
+ *   Choice: the k largest s + bias (bias: E floats for balance, or NULL), ties to the
+ *   lowest expert.  With groups_kept < groups, only from the groups_kept groups (of
+ *   E / groups consecutive experts) whose group_top (1 or 2) largest s + bias have
+ *   the largest sum, ties to the lowest group.  Comparisons are decided as in 64
+ *   bits; without a bias those of experts by the logits.
+ *   An expert with the logit -infinity, or with s + bias of -infinity or NaN, is not
+ *   chosen.  A token with fewer than k others has the index -1 and the weight 0 in
+ *   the places left (a token of padding: all logits -infinity).  A token with a logit
+ *   that is NaN (for softmax also +infinity) has no expert, and NaN weights.
+ *   Weights: scale * s of the chosen, divided by their sum when renormalize is set
+ *   (0 where that sum is 0).
+ * Outputs: index (T x k, in the order of the choice), weight (T x k), and the chosen
+ * pairs sorted by expert, then by token: slot (T x k): a pair's row in that order, -1
+ * without an expert; source (T * k): the token of each row, -1 past the last;
+ * offsets (E + 1): the first row of each expert.
+ *   1 <= k <= 32, E <= 1024, groups <= 32 and a divisor of E, k <= groups_kept * E /
+ *   groups, T * k < 2^31.
+ *   workspace: gemm_route_workspace_bytes(T, E) bytes on 4 bytes, of any content; it
+ *   must not be used by anything else until the call's work has finished.
+ */
+typedef enum gemm_route_score {
+    GEMM_ROUTE_SOFTMAX = 0,
+    GEMM_ROUTE_SIGMOID = 1
+} gemm_route_score_t;
+
+typedef struct gemm_route_args {
+    int64_t T, E, k;
+    const void *logits;
+    int64_t ld;
+    int32_t type;
+    int32_t score;
+    const float *bias;
+    int32_t groups, groups_kept, group_top;
+    int32_t renormalize;
+    float scale;
+} gemm_route_args_t;
+
+/* 0 where none is needed; -1 for a size out of range. */
+GEMM07_API int64_t gemm_route_workspace_bytes(int64_t T, int64_t E);
+GEMM07_API gemm_status_t gemm_route(const gemm_route_args_t *args, int32_t *index,
+                                    float *weight, int32_t *slot, int32_t *source,
+                                    int32_t *offsets, void *workspace, void *stream);
+
+/*
+ * gemm_route_bwd -- d_logits (T x E, the logits' type, row stride ld_d) from d_weight
+ * (T x k), the gradient of the weights, and the index that gemm_route gave.  The
+ * choice itself has no gradient.  Indices outside 0 .. E - 1 contribute nothing, one
+ * that comes twice contributes twice.  Of the arguments T, E, k, the logits, score,
+ * renormalize and scale count.  d_logits may be the logits.
+ */
+GEMM07_API gemm_status_t gemm_route_bwd(const gemm_route_args_t *args, const int32_t *index,
+                                        const float *d_weight, void *d_logits, int64_t ld_d,
+                                        void *stream);
+
+/*
+ * gemm_combine -- the experts' rows back to their tokens:
+ *   out[t] = x[t] + sum over j of weight[t][j] * rows[slot[t][j]]     (T x D)
+ * in FP32, rounded once.  rows: R x D of type rows_type; slot and weight: T x k, k <=
+ * 32, a slot outside 0 .. R - 1 (-1) has no row, and adds 0 * weight; x (x_type) may
+ * be NULL.  out may be x.
+ */
+typedef struct gemm_combine_args {
+    int64_t T, D, k, R;
+    const void *rows;
+    int64_t ld_rows;
+    int32_t rows_type;
+    const int32_t *slot;
+    const float *weight;
+    const void *x;
+    int64_t ldx;
+    int32_t x_type;
+} gemm_combine_args_t;
+
+GEMM07_API gemm_status_t gemm_combine(const gemm_combine_args_t *args, void *out,
+                                      int64_t ld_out, int32_t out_type, void *stream);
+
+/*
+ * gemm_combine_bwd -- from d_out (T x D, d_out_type), the gradient of out:
+ *   d_rows[slot[t][j]] = weight[t][j] * d_out[t]      (R x D, the rows' type)
+ *   d_weight[t][j]     = d_out[t] . rows[slot[t][j]]  (T x k; 0 without a row)
+ * Rows that no slot names are left as they were; slots are distinct (where two are
+ * equal, that row of d_rows is one of the two).  d_rows may be rows.  x's gradient is
+ * d_out.
+ */
+GEMM07_API gemm_status_t gemm_combine_bwd(const gemm_combine_args_t *args, const void *d_out,
+                                          int64_t ld_d_out, int32_t d_out_type, void *d_rows,
+                                          int64_t ld_d_rows, float *d_weight, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
