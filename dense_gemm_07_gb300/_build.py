@@ -148,7 +148,7 @@ def _link_binding(torch_dir: str, obj: str) -> None:
     libs = os.path.join(torch_dir, "lib")
     tmp = BINDING_PATH + f".tmp{os.getpid()}"
     _run(["g++", "-shared", "-o", tmp, obj, f"-L{LIB_DIR}", "-lgemm07", f"-L{libs}", "-lc10",
-          "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN",
+          "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN",
           f"-Wl,-rpath,{libs}"], "linking layer_binding.so")
     os.replace(tmp, BINDING_PATH)
     with open(BINDING_STAMP, "w") as f:

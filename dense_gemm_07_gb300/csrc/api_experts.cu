@@ -76,10 +76,16 @@ gemm_status_t product(int64_t E, int64_t M, int64_t N, int64_t K, const gemm_fp8
   a.C = C;
   a.ldc = ldc;
   a.c_bf16 = c_type == GEMM_TYPE_BF16 ? 1 : 0;
+  CUtensorMap tmA, tmB;
+  if (fp8_takes_wide(a, dev)) {
+    s = layer_map_bytes(&tmA, A->codes, K, M, A->ld, kFp8WideRows);
+    if (s == GEMM_OK) s = layer_map_bytes(&tmB, B->codes, K, b_rows, B->ld, kFp8WideCols);
+    if (s != GEMM_OK) return s;
+    return layer_from_cuda(launch_fp8_wide(tmA, tmB, a, dev, stream));
+  }
   Fp8FewPlan plan;
   s = layer_from_cuda(fp8_few_plan(a, dev, &plan));
   if (s != GEMM_OK) return s;
-  CUtensorMap tmA, tmB;
   std::memset(&tmA, 0, sizeof(tmA));
   std::memset(&tmB, 0, sizeof(tmB));
   if (K > 0) {
@@ -207,7 +213,7 @@ gemm_status_t gemm_fp8_experts(int64_t E, int64_t M, int64_t N, int64_t K, const
 int64_t gemm_route_workspace_bytes(int64_t T, int64_t E) {
   if (!size_ok(T) || E < 1 || E > kRouteMaxExperts) return -1;
   const int64_t chunks = (T + kRouteChunk - 1) / kRouteChunk;
-  return chunks > 1 ? chunks * E * 4 : 0;
+  return chunks > 1 ? chunks * route_count_stride(static_cast<int>(E)) : 0;
 }
 
 gemm_status_t gemm_route(const gemm_route_args_t* args, int32_t* index, float* weight,
@@ -233,7 +239,7 @@ gemm_status_t gemm_route(const gemm_route_args_t* args, int32_t* index, float* w
   a.slot = slot;
   a.source = source;
   a.offsets = offsets;
-  a.counts = static_cast<int*>(workspace);
+  a.counts = static_cast<uint8_t*>(workspace);
   return layer_from_cuda(launch_route(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -60,11 +60,37 @@ cudaError_t fp8_few_plan(const Fp8GemmArgs& a, const LayerDevice& dev, Fp8FewPla
 cudaError_t launch_fp8_few(const CUtensorMap& tmA, const CUtensorMap& tmB, const Fp8GemmArgs& a,
                            const Fp8FewPlan& plan, unsigned int* status, cudaStream_t stream);
 
+// ---- the same on tiles of 128 rows by 256 columns, with square scales (fp8_wide.cu).
+// tmA: boxes of kFp8WideRows rows; tmB: boxes of kFp8WideCols.  K > 0.
+// Whether a product runs there.
+bool fp8_takes_wide(const Fp8GemmArgs& a, const LayerDevice& dev);
+constexpr int kFp8WideRows = 128, kFp8WideCols = 256;
+cudaError_t launch_fp8_wide(const CUtensorMap& tmA, const CUtensorMap& tmB, const Fp8GemmArgs& a,
+                            const LayerDevice& dev, cudaStream_t stream);
+// cudaErrorInvalidConfiguration unless `kernel` is launched with at least `most`
+// registers a block, which its roles' shares (setmaxnreg) are drawn from: a larger
+// share would be waited for for ever.  `done` as in allow_shared.
+template <typename... P>
+cudaError_t check_registers(void (*kernel)(P...), int most, int threads,
+                            std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kernel);
+  if (e == cudaSuccess && fa.numRegs * threads < most) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 // ---- routing (route.cu)
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxChosen = 32;
 constexpr int kRouteMaxGroups = 32;
-constexpr int kRouteChunk = 128;  // tokens of a block
+constexpr int kRouteChunk = 128;  // tokens of a block: their count for an expert is a byte
+__host__ __device__ inline int route_count_stride(int E) { return (E + 3) & ~3; }
 struct RouteArgs {
   int T = 0, E = 0, k = 0;
   const void* logits = nullptr;
@@ -80,7 +106,7 @@ struct RouteArgs {
   int* slot = nullptr;
   int* source = nullptr;
   int* offsets = nullptr;
-  int* counts = nullptr;  // chunks x E, with more than one chunk
+  uint8_t* counts = nullptr;  // chunks x route_count_stride(E), with more than one chunk
   // gradient
   const int* chosen = nullptr;
   const float* d_weight = nullptr;

@@ -25,6 +25,75 @@ __device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// The same by a pair of CTAs, issued by one thread of the even one: A's rows and B's
+// are split between the two CTAs' shared memory at the same offsets.
+__device__ __forceinline__ void mma_e4m3_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// As mbar_wait, for waits that are over soon: the timer, whose reading takes longer than
+// most of them, is left alone for the first 256 polls.
+__device__ __forceinline__ bool wait_soon(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          uint64_t limit_ns) {
+  const uint32_t a = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(a, parity)) return true;
+    if ((i & 255u) == 0) {
+      if (*abort) return false;
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > limit_ns) return false;
+    }
+  }
+}
+
+// The same, acquiring what the other CTA of a pair released.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                             uint64_t limit_ns) {
+  const uint32_t a = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((i & 255u) == 0) {
+      if (*abort) return false;
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > limit_ns) return false;
+    }
+  }
+}
+
+// ---- scales on their way to shared memory: copies of one float each (any alignment of
+// 4), and an arrival on `bar` when all copies of this thread so far have landed.  A
+// block of K takes less time than a load does, so the copies of several are under way.
+__device__ __forceinline__ void copy_scale(float* dst, const float* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(there ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+__device__ __forceinline__ void arrive_when_copied(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -43,10 +112,15 @@ __device__ __forceinline__ uint64_t pack2u(uint32_t lo, uint32_t hi) {
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   return pack2u(__float_as_uint(lo), __float_as_uint(hi));
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
+// c += {lo, hi} * b, for lo and hi that a tensor-memory load is to deliver: volatile, so
+// that it stays behind the wait for it.
+__device__ __forceinline__ void fma2_loaded(uint64_t& c, uint32_t lo, uint32_t hi, uint64_t b) {
+  asm volatile(
+      "{\n\t.reg .b64 t;\n\t"
+      "mov.b64 t, {%1, %2};\n\t"
+      "fma.rn.f32x2 %0, t, %3, %0;\n\t}"
+      : "+l"(c)
+      : "r"(lo), "r"(hi), "l"(b));
 }
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
@@ -57,6 +131,20 @@ __device__ __forceinline__ float half_of(uint64_t v, int high) {
   uint32_t lo, hi;
   asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
   return __uint_as_float(high ? hi : lo);
+}
+
+// 16 lanes (from the address's lane on) by 32 columns of tensor memory: thread t
+// receives, for i = 0 .. 3, columns 8 i + 2 (t % 4) and the next of lane t / 4
+// (r[4 i], r[4 i + 1]) and of lane t / 4 + 8 (r[4 i + 2], r[4 i + 3]).
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 
 // Rows first .. first + count - 1 of one expert.
@@ -106,6 +194,44 @@ __device__ __forceinline__ Fp8Rows fp8_expert_rows(const int* offsets, int E, in
     last = __shfl_sync(0xFFFFFFFFu, end, 31);
   }
   return Fp8Rows{0, 0, 0};
+}
+
+// The first row of each expert and the units of at most `size` rows before it, E + 1
+// of each; the number of all units.  A warp's work; offsets as above.
+__device__ __forceinline__ int fp8_expert_table(const int* offsets, int E, int M, int size,
+                                                int* start, int* before) {
+  const int lane = threadIdx.x & 31;
+  auto held = [&](int v) { return v < 0 ? 0 : v > M ? M : v; };
+  int last = held(__ldg(offsets)), units = 0;
+  if (lane == 0) {
+    start[0] = last;
+    before[0] = 0;
+  }
+  for (int base = 0; base < E; base += 32) {
+    const int e = base + lane;
+    int end = e < E ? held(__ldg(offsets + e + 1)) : 0;
+    end = end > last ? end : last;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, end, d);
+      if (lane >= d && v > end) end = v;
+    }
+    int from = __shfl_up_sync(0xFFFFFFFFu, end, 1);
+    if (lane == 0) from = last;
+    int upto = (end - from + size - 1) / size;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += v;
+    }
+    if (e < E) {
+      start[e + 1] = end;
+      before[e + 1] = units + upto;
+    }
+    units += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    last = __shfl_sync(0xFFFFFFFFu, end, 31);
+  }
+  return units;
 }
 
 }  // namespace g07

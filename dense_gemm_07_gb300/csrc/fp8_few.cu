@@ -33,7 +33,10 @@ constexpr int B_BYTES = TILE_N * BK;
 constexpr int THREADS = 384;
 constexpr int SUM_WARPS = 8;
 constexpr int MAX_STAGES = 8;
-constexpr int SLOTS = 4;  // staged scales
+constexpr int SLOTS = 8;  // blocks of K whose scales are staged
+// Words from one row of A's sums to the next: what a warp stores at once (8 lanes of 4
+// columns) falls into 32 banks.
+constexpr int PART_ROW = TILE_N + 4;
 // Shared memory of a CTA when two share an SM (228 KB, 1 KB of it reserved for each).
 constexpr int kSmemBytes = 228 * 1024 / 2 - 1024;
 
@@ -43,10 +46,11 @@ constexpr int kRegsOther = 32, kRegsSum = 104;
 constexpr int kRegsBlock = 128 * kRegsOther + 256 * kRegsSum;
 static_assert(kRegsBlock <= THREADS * 80, "register split");
 
-template <int COLS>
+template <int COLS, bool SQUARE>
 struct alignas(16) Control {
   static constexpr int ACCS = COLS <= 32 ? 4 : 2;
-  float scale[SLOTS][COLS];
+  float scale[SLOTS][COLS];  // of A's rows
+  float scale_b[SLOTS][SQUARE ? 4 : TILE_N];  // of the block of B, or of its rows
   uint64_t full[MAX_STAGES];
   uint64_t empty[MAX_STAGES];
   uint64_t acc_full[ACCS];
@@ -76,9 +80,11 @@ template <int COLS, bool SQUARE>
 __global__ void __launch_bounds__(THREADS, 2)
 fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const FewArgs p) {
-  using Ctl = Control<COLS>;
+  using Ctl = Control<COLS, SQUARE>;
   constexpr int ACCS = Ctl::ACCS;
-  constexpr int CHUNKS = COLS / 32;  // 16-column chunks of a group of four sum warps
+  // 32-column chunks of a group of four sum warps, and halves of their 32 lanes: a
+  // group takes every other chunk, or where there is one chunk every other half.
+  constexpr int CHUNKS = COLS > 32 ? COLS / 64 : 1, HALVES = COLS > 32 ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int stage_bytes = B_BYTES + p.cols * BK;
@@ -98,7 +104,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       mbar_init(&ctl->acc_empty[a], SUM_WARPS);
     }
     for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(&ctl->scale_full[s], 1);
+      mbar_init(&ctl->scale_full[s], 32);
       mbar_init(&ctl->scale_empty[s], SUM_WARPS);
     }
     mbar_init(&ctl->drain, 1);
@@ -143,7 +149,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int group = (warp >> 2) & 1;         // of the sum warps: takes chunks group, group + 2, ...
   const int tlane = (warp & 3) * 32 + lane;  // lane of the MMA, column of the tile
   // The sums leave through the ring, once every MMA that read it has completed:
-  // 128 columns of C a row of A.
+  // 128 columns of C a row of A, PART_ROW apart.
   float* part = reinterpret_cast<float*>(smem);
 
   if (warp < 4) {
@@ -158,7 +164,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       int last[MAX_STAGES];
       for (int s = 0; s < MAX_STAGES; ++s) last[s] = -1;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort, limit)) {
+        if (!wait_soon(&ctl->empty[stage], phase ^ 1u, abort, limit)) {
           give_up(abort, p.status);
           break;
         }
@@ -181,7 +187,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
       for (int s = 0; s < MAX_STAGES; ++s)
         if (last[s] >= 0 &&
-            !mbar_wait(&ctl->full[s], static_cast<uint32_t>(last[s]), &never, limit))
+            !wait_soon(&ctl->full[s], static_cast<uint32_t>(last[s]), &never, limit))
           give_up(abort, p.status);
     } else if (warp == 1 && lane == 0) {
       // ------------------------------------------------------------- MMAs
@@ -190,8 +196,8 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       uint32_t phase = 0, acc_phase = 0;
       bool issued = false;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&ctl->acc_empty[acc], acc_phase ^ 1u, abort, limit) ||
-            !mbar_wait(&ctl->full[stage], phase, abort, limit)) {
+        if (!wait_soon(&ctl->acc_empty[acc], acc_phase ^ 1u, abort, limit) ||
+            !wait_soon(&ctl->full[stage], phase, abort, limit)) {
           give_up(abort, p.status);
           break;
         }
@@ -216,7 +222,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       if (issued) {
         mma_commit(&ctl->drain);
         volatile int never = 0;
-        if (!mbar_wait(&ctl->drain, 0u, &never, limit)) give_up(abort, p.status);
+        if (!wait_soon(&ctl->drain, 0u, &never, limit)) give_up(abort, p.status);
       }
     } else if (warp == 2) {
       // ----------------------------------------------------------- scales
@@ -226,75 +232,86 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         sb += (static_cast<int64_t>(rows.expert) * p.n_tiles + n0 / TILE_N) * p.g.ld_sb;
       int slot = 0;
       uint32_t phase = 0;
-      float v[COLS / 32];
-      auto load = [&](int kb) {
-        const float f = SQUARE ? __ldg(sb + kb) : 1.0f;
-#pragma unroll
-        for (int i = 0; i < COLS / 32; ++i)
-          v[i] = i * 32 + lane < rows.count ? f * __ldg(sa + kb * p.g.ld_sa + i * 32 + lane) : 0.0f;
-      };
-      if (kb0 < kb1) load(kb0);
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!__all_sync(0xFFFFFFFFu,
-                        mbar_wait(&ctl->scale_empty[slot], phase ^ 1u, abort, limit))) {
+                        wait_soon(&ctl->scale_empty[slot], phase ^ 1u, abort, limit))) {
           if (lane == 0) give_up(abort, p.status);
           break;
         }
 #pragma unroll
-        for (int i = 0; i < COLS / 32; ++i) ctl->scale[slot][i * 32 + lane] = v[i];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->scale_full[slot]);
-        if (kb + 1 < kb1) load(kb + 1);
+        for (int i = 0; i < COLS / 32; ++i) {
+          const bool in = i * 32 + lane < rows.count;
+          copy_scale(&ctl->scale[slot][i * 32 + lane],
+                     in ? sa + kb * p.g.ld_sa + i * 32 + lane : p.g.sa, in);
+        }
+        if (SQUARE) {
+          if (lane == 0) copy_scale(&ctl->scale_b[slot][0], sb + kb, true);
+        } else {
+#pragma unroll
+          for (int i = 0; i < TILE_N / 32; ++i) {
+            const bool in = n0 + i * 32 + lane < p.g.N;
+            copy_scale(&ctl->scale_b[slot][SQUARE ? 0 : i * 32 + lane],
+                       in ? sb + kb * p.g.ld_sb + n0 + i * 32 + lane : p.g.sb, in);
+          }
+        }
+        arrive_when_copied(&ctl->scale_full[slot]);
         if (++slot == SLOTS) {
           slot = 0;
           phase ^= 1u;
         }
       }
+      cp_async_wait_all();  // nothing is on its way when the ring is used again
     }
   } else {
     // --------------------------------------------------------------- sums
     if constexpr (COLS > 32) regs_inc<kRegsSum>();
-    uint64_t sum[CHUNKS][8];  // column n0 + tlane, 16 rows of A a chunk
+    const int quad = warp & 3, pos = lane >> 2, at2 = 2 * (lane & 3);
+    const int h0 = COLS > 32 ? 0 : group, c0 = COLS > 32 ? group * 32 : 0;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32 + 16 * h0) << 16) + c0;
+    const int at = quad * 32 + 16 * h0 + pos;  // lane: at + 16 h + 8 q
+    // [chunk][16 h][8 q][columns 8 i + at2 and the next]
+    uint64_t sum[CHUNKS][HALVES][2][4];
 #pragma unroll
-    for (int j = 0; j < CHUNKS; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[j][i] = 0;
-    const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const float* sb = p.g.sb + n0 + tlane;
-    const bool in = n0 + tlane < p.g.N;
-    float next = 0.0f;
-    if (!SQUARE && in && kb0 < kb1) next = __ldg(sb + kb0 * p.g.ld_sb);
+    for (int j = 0; j < CHUNKS * HALVES * 8; ++j)
+      sum[j / (HALVES * 8)][j / 8 % HALVES][j / 4 % 2][j % 4] = 0;
     int acc = 0, slot = 0;
     uint32_t acc_phase = 0, phase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
-      const float mine = next;
-      if (!SQUARE && in && kb + 1 < kb1) next = __ldg(sb + (kb + 1) * p.g.ld_sb);
-      const bool ok = mbar_wait(&ctl->scale_full[slot], phase, abort, limit) &&
-                      mbar_wait(&ctl->acc_full[acc], acc_phase, abort, limit);
+      const bool ok = wait_soon(&ctl->scale_full[slot], phase, abort, limit) &&
+                      wait_soon(&ctl->acc_full[acc], acc_phase, abort, limit);
       if (!__all_sync(0xFFFFFFFFu, ok)) {
         if (lane == 0) give_up(abort, p.status);
         break;
       }
       tc_fence_after_sync();
+      uint64_t mine[HALVES * 2];  // of B's rows (or of their block)
+#pragma unroll
+      for (int q = 0; q < HALVES * 2; ++q) {
+        const float v = ctl->scale_b[slot][SQUARE ? 0 : at + 8 * q];
+        mine[q] = pack2(v, v);
+      }
 #pragma unroll
       for (int j = 0; j < CHUNKS; ++j) {
-        const int col = (2 * j + group) * 16;
-        if (col < ncols) {
-          uint32_t r[16];
-          tmem_ld_32x32b_x16(taddr + acc * COLS + col, r);
-          tmem_ld_wait();
-          const float4* s = reinterpret_cast<const float4*>(&ctl->scale[slot][col]);
+        if (j * 64 + c0 < ncols) {
+          uint64_t f[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 f = s[i];
-            uint64_t lo = pack2(f.x, f.y), hi = pack2(f.z, f.w);
-            if (!SQUARE) {
-              const uint64_t m2 = pack2(mine, mine);
-              lo = mul2(lo, m2);
-              hi = mul2(hi, m2);
-            }
-            sum[j][2 * i] = fma2(pack2u(r[4 * i], r[4 * i + 1]), lo, sum[j][2 * i]);
-            sum[j][2 * i + 1] = fma2(pack2u(r[4 * i + 2], r[4 * i + 3]), hi, sum[j][2 * i + 1]);
+          for (int i = 0; i < 4; ++i)
+            f[i] = *reinterpret_cast<const uint64_t*>(&ctl->scale[slot][c0 + j * 64 + at2 + 8 * i]);
+          if (SQUARE) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], mine[0]);
+          }
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) {
+            uint32_t r[16];
+            tmem_ld_16x256b_x4(taddr + (static_cast<uint32_t>(16 * h) << 16) + acc * COLS + j * 64, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                fma2_loaded(sum[j][h][q][i], r[4 * i + 2 * q], r[4 * i + 2 * q + 1],
+                            SQUARE ? f[i] : mul2(f[i], mine[2 * h + q]));
           }
         }
       }
@@ -316,14 +333,22 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
     for (int j = 0; j < CHUNKS; ++j)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int c = (2 * j + group) * 16 + i;
-        if (c < rows.count) part[c * TILE_N + tlane] = half_of(sum[j][i / 2], i & 1);
-      }
+      for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int c = c0 + j * 64 + 8 * (i / 2) + at2 + (i & 1);
+            if (c < rows.count)
+              part[c * PART_ROW + at + 16 * h + 8 * q] = half_of(sum[j][h][q][i / 2], i & 1);
+          }
   }
 
   // ------------------------------------------------------------------ output
-  if (p.split > 1) cluster_sync();
+  if (p.split > 1)
+    cluster_sync();
+  else
+    __syncthreads();
   const int n = n0 + tlane;
   if (warp >= 4 && n < p.g.N) {
     const float b =
@@ -340,12 +365,11 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         *o = epi_apply(p.g.epi, v, old, b);
       }
     };
-    if (p.split == 1) {  // the thread's own sums
-      for (int c = group * 16; c < rows.count; c = (c & 15) == 15 ? c + 17 : c + 1)
-        store(c, part[c * TILE_N + tlane]);
+    if (p.split == 1) {
+      for (int c = group; c < rows.count; c += 2) store(c, part[c * PART_ROW + tlane]);
     } else {
       for (int c = rank * 2 + group; c < rows.count; c += 2 * p.split) {
-        const uint32_t at = smem_u32(part + c * TILE_N + tlane);
+        const uint32_t at = smem_u32(part + c * PART_ROW + tlane);
         float v = 0.0f;
         for (int r = 0; r < p.split; ++r) v += ld_cluster_f32(map_to_rank(at, r));
         store(c, v);
@@ -369,21 +393,12 @@ Kernel kernel_of(int cols, bool square) {
 }
 std::atomic<uint64_t> g_allowed[4], g_registers[2];
 
-// The shared-memory limit, and that the roles' register shares are there to be drawn
-// on (a larger share than the block was launched with would be waited for for ever).
+// The shared-memory limit and the wide kernel's registers.
 cudaError_t prepare(Kernel kernel, bool wide, bool square) {
-  cudaError_t e = allow_shared(kernel, kSmemBytes, &g_allowed[(wide ? 2 : 0) + (square ? 1 : 0)]);
+  const cudaError_t e =
+      allow_shared(kernel, kSmemBytes, &g_allowed[(wide ? 2 : 0) + (square ? 1 : 0)]);
   if (e != cudaSuccess || !wide) return e;
-  int dev = 0;
-  e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (g_registers[square ? 1 : 0].load(std::memory_order_acquire) & bit) return cudaSuccess;
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, kernel);
-  if (e == cudaSuccess && fa.numRegs * THREADS < kRegsBlock) e = cudaErrorInvalidConfiguration;
-  if (e == cudaSuccess) g_registers[square ? 1 : 0].fetch_or(bit, std::memory_order_release);
-  return e;
+  return check_registers(kernel, kRegsBlock, THREADS, &g_registers[square ? 1 : 0]);
 }
 
 }  // namespace
@@ -405,7 +420,9 @@ cudaError_t fp8_few_plan(const Fp8GemmArgs& a, const LayerDevice& dev, Fp8FewPla
   int split = 1;
   while (split < 8 && busy * split * 2 <= 2 * dev.sms && kbs >= 4 * split) split *= 2;
   plan->split = split;
-  const int control = static_cast<int>(cols <= 32 ? sizeof(Control<32>) : sizeof(Control<128>));
+  const int control = static_cast<int>(
+      cols <= 32 ? (a.b_square ? sizeof(Control<32, true>) : sizeof(Control<32, false>))
+                 : (a.b_square ? sizeof(Control<128, true>) : sizeof(Control<128, false>)));
   int stages = (kSmemBytes - 1024 - control) / (B_BYTES + plan->cols * BK);
   plan->stages = stages < MAX_STAGES ? stages : MAX_STAGES;
   return plan->tiles * split <= 0x7FFFFFFF ? cudaSuccess : cudaErrorInvalidValue;

@@ -79,7 +79,65 @@ __device__ __forceinline__ void store8(uint8_t* p, int n, uint2 c) {
 constexpr int kRowsPerBlock = kThreads / 16;
 constexpr int kGroup = 4;
 
-template <typename T, bool VEC>
+// Eight elements as loaded, their largest magnitude in a lane's form (the FP32 bits, or
+// two BF16 magnitudes side by side), and that of 16 lanes as FP32 bits.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+  float v[8];
+  template <bool VEC>
+  __device__ __forceinline__ void load(const float* p, int n) { load8<VEC>(p, n, v); }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t = larger(t, magnitude(v[i]));
+    return t;
+  }
+  static __device__ __forceinline__ uint32_t top_of(uint32_t a, uint32_t b) { return larger(a, b); }
+  static __device__ __forceinline__ uint32_t bits(uint32_t t) { return t; }
+  __device__ __forceinline__ uint2 codes(const Scale& s) const {
+    return make_uint2(codes4(v, s), codes4(v + 4, s));
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  uint32_t w[4];
+  template <bool VEC>
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int n) {
+    if (VEC && n >= 8) {
+      const uint4 a = *reinterpret_cast<const uint4*>(p);
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    } else {
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = (2 * i < n ? q[2 * i] : 0u) | (2 * i + 1 < n ? static_cast<uint32_t>(q[2 * i + 1]) : 0u) << 16;
+    }
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t t = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) t = __vmaxu2(t, w[i] & 0x7FFF7FFFu);
+    return t;
+  }
+  static __device__ __forceinline__ uint32_t top_of(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+  static __device__ __forceinline__ uint32_t bits(uint32_t t) {
+    return larger(t << 16, t & 0xFFFF0000u);
+  }
+  __device__ __forceinline__ uint2 codes(const Scale& s) const {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    }
+    return make_uint2(codes4(v, s), codes4(v + 4, s));
+  }
+};
+
+// ALL: every block of 128 is whole and there are groups of kGroup of them.
+template <typename T, bool VEC, bool ALL>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(Fp8QuantArgs a, int kbs,
                                                                  int groups) {
   grid_dependency_wait();
@@ -91,26 +149,24 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(Fp8QuantArgs a,
   int from = r;
   if (live && a.index) from = __ldg(a.index + r);
   const bool zero = !live || from < 0 || from >= a.T;
-  const T* x = static_cast<const T*>(a.x) + (zero ? 0 : from * a.ldx);
-  float v[kGroup][8];
+  const int col0 = kb0 * B + l * 8;
+  const T* x = static_cast<const T*>(a.x) + (zero ? 0 : from * a.ldx + col0);
+  Eight<T> v[kGroup];
+#pragma unroll
+  for (int g = 0; g < kGroup; ++g)
+    v[g].template load<VEC>(x + g * B, zero ? 0 : ALL ? 8 : a.C - col0 - g * B);
+  uint8_t* codes = a.codes + r * a.ld + col0;
+  float* scales = a.scales + kb0 * a.ld_scales + r;
 #pragma unroll
   for (int g = 0; g < kGroup; ++g) {
-    const int col = (kb0 + g) * B + l * 8;
-    load8<VEC>(x + col, zero ? 0 : a.C - col, v[g]);
-  }
-  uint8_t* codes = a.codes + r * a.ld;
+    uint32_t top = v[g].top();
 #pragma unroll
-  for (int g = 0; g < kGroup; ++g) {
-    const int kb = kb0 + g, col = kb * B + l * 8;
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = larger(top, magnitude(v[g][i]));
-#pragma unroll
-    for (int d = 8; d; d >>= 1) top = larger(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    if (!live || kb >= kbs) continue;
-    const Scale s = scale_of(top);
-    if (l == 0) a.scales[kb * a.ld_scales + r] = s.step;
-    store8(codes + col, a.C - col, make_uint2(codes4(v[g], s), codes4(v[g] + 4, s)));
+    for (int d = 8; d; d >>= 1)
+      top = Eight<T>::top_of(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    if (!live || (!ALL && kb0 + g >= kbs)) continue;
+    const Scale s = scale_of(Eight<T>::bits(top));
+    if (l == 0) scales[g * a.ld_scales] = s.step;
+    store8(codes + g * B, ALL ? 8 : a.C - col0 - g * B, v[g].codes(s));
   }
 }
 
@@ -251,8 +307,11 @@ cudaError_t launch_fp8_quantize_rows(const Fp8QuantArgs& a, cudaStream_t stream)
   const int kbs = static_cast<int>(blocks_of(a.C, B)), groups = static_cast<int>(blocks_of(kbs, kGroup));
   const int64_t grid = blocks_of(a.rows, kRowsPerBlock) * groups;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const bool all = a.C % (kGroup * B) == 0;
   return by_type(a, [&](auto t, auto wide) {
-    return launch_pdl(quantize_rows_kernel<decltype(t), decltype(wide)::value>,
+    using T = decltype(t);
+    constexpr bool kWide = decltype(wide)::value;
+    return launch_pdl(all ? quantize_rows_kernel<T, kWide, true> : quantize_rows_kernel<T, kWide, false>,
                       dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, a, kbs, groups);
   });
 }

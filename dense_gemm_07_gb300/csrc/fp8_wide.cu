@@ -1,0 +1,456 @@
+// fp8_wide.cu -- products of 8-bit floating-point matrices (the formula is in
+// fp8_few.cu) of many rows, on tiles of 128 rows by 256 columns of C.
+#include <atomic>
+#include <type_traits>
+
+#include "experts.h"
+#include "fp8.cuh"
+#include "kernels.h"
+#include "normal_tail.cuh"
+#include "sm103_ptx.cuh"
+#include "tile_order.cuh"
+
+namespace g07 {
+namespace {
+
+constexpr int TILE_M = kFp8WideRows;  // rows of C: the MMA's lanes
+constexpr int TILE_N = 256;           // columns of C, in two halves
+constexpr int HALF = 128;
+constexpr int BK = kFp8Block;
+constexpr int STAGES = 4;
+constexpr int A_BYTES = TILE_M * BK;
+constexpr int B_BYTES = TILE_N * BK;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int THREADS = 384;
+constexpr int SUM_WARPS = 8;
+constexpr int GROUP = 12;
+// A sum warp's 32 rows of 16 numbers on their way out, 20 words from one row to the
+// next: rows stay on 16 bytes, and what 8 lanes store at once falls into 32 banks.
+constexpr int STAGED_ROW = 20;
+constexpr int STAGED_FLOATS = 32 * STAGED_ROW;
+constexpr int STAGED_AT = STAGES * STAGE_BYTES;
+constexpr int CONTROL_AT = STAGED_AT + 8 * STAGED_FLOATS * 4;
+// Registers a thread of the roles (setmaxnreg): together at most the 384 x 168 that
+// the block is launched with.
+constexpr int kRegsOther = 88, kRegsSum = 208;
+constexpr int kRegsBlock = 128 * kRegsOther + 256 * kRegsSum;
+static_assert(kRegsBlock <= THREADS * 168, "register split");
+
+struct alignas(16) Control {
+  uint64_t full[STAGES];
+  uint64_t empty[STAGES];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int tiles;
+  int start[kRouteMaxExperts + 1];   // experts: first row of each
+  int before[kRouteMaxExperts + 1];  // experts: units of rows before each
+};
+constexpr size_t kSmemBytes = 1024 + CONTROL_AT + sizeof(Control);  // 1024: to align the ring
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of a block");
+
+struct WideArgs {
+  Fp8GemmArgs g;
+  int n_tiles, units;  // dense: units of rows
+  unsigned int* status;
+};
+
+struct Tile {
+  int expert, first, count, n0;
+};
+
+__device__ __forceinline__ Tile tile_at(const WideArgs& p, const Control* ctl, int t) {
+  Tile r;
+  int left;
+  if (p.g.E == 0) {
+    const TileCoord c = tile_order(t, p.units, p.n_tiles, GROUP);
+    r.expert = 0;
+    r.first = c.m * TILE_M;
+    r.n0 = c.n * TILE_N;
+    left = p.g.M - r.first;
+  } else {
+    // the last expert with before[e] * n_tiles <= t: it has units.  Its units share the
+    // columns of B and follow each other.
+    int lo = 0, hi = p.g.E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (ctl->before[mid] * p.n_tiles <= t)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int units = ctl->before[lo + 1] - ctl->before[lo];
+    const int in = t - ctl->before[lo] * p.n_tiles;
+    r.expert = lo;
+    r.first = ctl->start[lo] + in % units * TILE_M;
+    r.n0 = in / units * TILE_N;
+    left = ctl->start[lo + 1] - r.first;
+  }
+  r.count = left < TILE_M ? left : TILE_M;
+  return r;
+}
+
+__device__ __forceinline__ void give_up(volatile int* abort, unsigned int* status) {
+  *abort = 1;
+  atomicOr(status, 1u);
+}
+
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++at == n) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// act(alpha * v + beta * old + bias) of N consecutive columns.
+template <int N>
+__device__ __forceinline__ void finish(const EpiParams& e, const float (&bias)[N],
+                                       const float (&old)[N], float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] *= e.alpha;
+    if (e.beta != 0.0f) v[i] = fmaf(e.beta, old[i], v[i]);
+    v[i] += bias[i];
+    if (e.act == 1) v[i] = fmaxf(v[i], 0.0f);
+    if (e.act == 2) {
+      float ignored;
+      const float tail = 0.5f * normal_tail2(v[i], &ignored);
+      v[i] *= v[i] > 0.0f ? 1.0f - tail : tail;
+    }
+  }
+}
+
+// 16 columns of C from n on, of the `rows` rows from `first` on, from a warp's staged
+// sums.
+template <typename T>
+__device__ __forceinline__ void store_rows(const Fp8GemmArgs& g, T* C, const float* stage,
+                                           int expert, int first, int rows, int n) {
+  const int lane = threadIdx.x & 31;
+  C += first * g.ldc + n;
+  const float* bias = g.epi.bias ? g.epi.bias + static_cast<int64_t>(expert) * g.N + n : nullptr;
+  if (n + 16 <= g.N && ((reinterpret_cast<uintptr_t>(g.C) | (g.ldc * sizeof(T))) & 15u) == 0) {
+    const int c = (lane & 1) * 8;  // two lanes a row, 8 columns each
+    float b[8], old[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = bias ? __ldg(bias + c + i) : 0.0f;
+#pragma unroll
+    for (int r = lane >> 1; r < 32; r += 16) {
+      if (r < rows) {
+        float v[8];
+        load_vec<8>(stage + r * STAGED_ROW + c, v);
+        T* o = C + r * g.ldc + c;
+        if (g.epi.beta != 0.0f) load_vec<8>(o, old);
+        finish(g.epi, b, old, v);
+        store_vec<8>(o, v);
+      }
+    }
+  } else {  // a lane a column
+    const int c = lane & 15;
+    if (n + c < g.N) {
+      const float b[1] = {bias ? __ldg(bias + c) : 0.0f};
+#pragma unroll 4
+      for (int r = lane >> 4; r < rows; r += 2) {
+        float v[1] = {stage[r * STAGED_ROW + c]}, old[1];
+        T* o = C + r * g.ldc + c;
+        if (g.epi.beta != 0.0f) old[0] = to_f32(*o);
+        finish(g.epi, b, old, v);
+        *o = from_f32<T>(v[0]);
+      }
+    }
+  }
+}
+
+// f with the constant j, 0 .. 7.
+template <typename F>
+__device__ __forceinline__ void of_eight(int j, F f) {
+  switch (j) {
+    case 0: f(std::integral_constant<int, 0>()); break;
+    case 1: f(std::integral_constant<int, 1>()); break;
+    case 2: f(std::integral_constant<int, 2>()); break;
+    case 3: f(std::integral_constant<int, 3>()); break;
+    case 4: f(std::integral_constant<int, 4>()); break;
+    case 5: f(std::integral_constant<int, 5>()); break;
+    case 6: f(std::integral_constant<int, 6>()); break;
+    default: f(std::integral_constant<int, 7>()); break;
+  }
+}
+
+// The 128 columns of a warp's 32 rows, 16 at a time through the staging: put(j) stages
+// columns 16 j and on.  (A loop, with the registers picked by a switch: written out,
+// the code is several times the instruction cache's, and a tile's output took 10000
+// clocks, as long as 10 blocks of K.)
+template <typename F>
+__device__ __forceinline__ void store_tile(const Fp8GemmArgs& g, float* stage, int expert, int first,
+                                           int rows, int n0, F put) {
+#pragma unroll 1
+  for (int j = 0; j < 8 && n0 + 16 * j < g.N; ++j) {
+    __syncwarp();  // the last ones have been read
+    put(j);
+    __syncwarp();
+    if (g.c_bf16)
+      store_rows(g, static_cast<__nv_bfloat16*>(g.C), stage, expert, first, rows, n0 + 16 * j);
+    else
+      store_rows(g, static_cast<float*>(g.C), stage, expert, first, rows, n0 + 16 * j);
+  }
+}
+
+__global__ void __launch_bounds__(THREADS, 1)
+fp8_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ WideArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Control* ctl = reinterpret_cast<Control*>(smem + CONTROL_AT);
+  volatile int* abort = &ctl->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int step = gridDim.x;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&ctl->acc_full[a], 1);
+      mbar_init(&ctl->acc_empty[a], SUM_WARPS);
+    }
+    mbar_init(&ctl->drain, 1);
+    ctl->abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl->tmem_base, 2 * TILE_N);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  grid_dependents_go();
+  if (warp == 2) {
+    int units = p.units;
+    if (p.g.E > 0)
+      units = fp8_expert_table(p.g.offsets, p.g.E, p.g.M, TILE_M, ctl->start, ctl->before);
+    if (lane == 0) ctl->tiles = units * p.n_tiles;
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = ctl->tmem_base;
+  const int tiles = ctl->tiles;
+  const uint64_t limit = wait_limit_ns(p.status);
+  const int kbs = (p.g.K + BK - 1) / BK;
+
+  if (warp < 4) {
+    regs_dec<kRegsOther>();
+    if (warp == 0 && lane == 0) {
+      // ----------------------------------------------------------- copies
+      // test faults: the first stage is never copied (2: by the first block alone)
+      const unsigned int fault = p.status[1];
+      const bool skip = fault == 1 || (fault == 2 && blockIdx.x == 0);
+      Ring ring;
+      int last[STAGES];
+#pragma unroll
+      for (int s = 0; s < STAGES; ++s) last[s] = -1;
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < tiles; t += step) {
+        const Tile w = tile_at(p, ctl, t);
+        const int brow = w.expert * p.g.N + w.n0;
+        for (int kb = 0; kb < kbs; ++kb) {
+          ok = wait_soon(&ctl->empty[ring.at], ring.phase ^ 1u, abort, limit);
+          if (!ok) break;
+          if (!(skip && t == static_cast<int>(blockIdx.x) && kb == 0)) {
+            uint8_t* a = smem + ring.at * STAGE_BYTES;
+            mbar_arrive_expect_tx(&ctl->full[ring.at], STAGE_BYTES);
+            tma_load_2d(a, &tmA, &ctl->full[ring.at], kb * BK, w.first);
+            tma_load_2d(a + A_BYTES, &tmB, &ctl->full[ring.at], kb * BK, brow);
+#pragma unroll
+            for (int s = 0; s < STAGES; ++s)
+              if (s == ring.at) last[s] = static_cast<int>(ring.phase);
+          }
+          ring.next(STAGES);
+        }
+      }
+      if (!ok) give_up(abort, p.status);
+      // copies in flight land before the block may exit
+      volatile int never = 0;
+#pragma unroll
+      for (int s = 0; s < STAGES; ++s)
+        if (last[s] >= 0 &&
+            !wait_soon(&ctl->full[s], static_cast<uint32_t>(last[s]), &never, limit))
+          give_up(abort, p.status);
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------------------- MMAs
+      const uint64_t desc_a = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t desc_b = sdesc_sw128(smem_u32(smem) + A_BYTES, 16, 1024);
+      Ring ring, acc;
+      bool ok = true, issued = false;
+      for (int t = blockIdx.x; ok && t < tiles; t += step) {
+        const Tile w = tile_at(p, ctl, t);
+        const int cols = p.g.N - w.n0 < TILE_N ? (p.g.N - w.n0 + 15) & ~15 : TILE_N;
+        const uint32_t idesc = idesc_e4m3_f32(TILE_M, cols);
+        for (int kb = 0; kb < kbs; ++kb) {
+          ok = wait_soon(&ctl->acc_empty[acc.at], acc.phase ^ 1u, abort, limit) &&
+               wait_soon(&ctl->full[ring.at], ring.phase, abort, limit);
+          if (!ok) break;
+          tc_fence_after_sync();
+          const uint64_t at = static_cast<uint64_t>(ring.at * (STAGE_BYTES >> 4));
+#pragma unroll
+          for (int kk = 0; kk < BK / 32; ++kk)
+            mma_e4m3_ss(tmem + acc.at * TILE_N, desc_a + at + 2 * kk, desc_b + at + 2 * kk, idesc,
+                        kk != 0 ? 1u : 0u);
+          issued = true;
+          mma_commit(&ctl->acc_full[acc.at]);
+          mma_commit(&ctl->empty[ring.at]);
+          ring.next(STAGES);
+          acc.next(2);
+        }
+      }
+      if (!ok) give_up(abort, p.status);
+      if (issued) {
+        mma_commit(&ctl->drain);
+        volatile int never = 0;
+        if (!wait_soon(&ctl->drain, 0u, &never, limit)) give_up(abort, p.status);
+      }
+    }
+  } else {
+    // --------------------------------------------------------------- sums
+    regs_inc<kRegsSum>();
+    const int half = (warp >> 2) - 1;  // its 128 columns of the tile
+    const int quad = warp & 3;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * HALF;
+    float* stage = reinterpret_cast<float*>(smem + STAGED_AT) + (warp - 4) * STAGED_FLOATS;
+    Ring acc;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < tiles; t += step) {
+      const Tile w = tile_at(p, ctl, t);
+      const int n0 = w.n0 + half * HALF;
+      const int rows = w.count - quad * 32 < 32 ? w.count - quad * 32 : 32;  // of this warp's
+      const bool live = n0 < p.g.N;
+      uint64_t sum[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) sum[i] = 0;
+      // A thread has a row of A: its scale times the block's of B.
+      const int blocks = (p.g.N + 127) / 128;
+      const float* sb =
+          p.g.sb + (static_cast<int64_t>(w.expert) * blocks + (live ? n0 / 128 : 0)) * p.g.ld_sb;
+      const float* sa = p.g.sa + w.first + quad * 32 + lane;
+      const bool mine = lane < rows;
+      float fa[3], fb[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        fa[i] = mine && i < kbs ? __ldg(sa + i * p.g.ld_sa) : 0.0f;
+        fb[i] = i < kbs ? __ldg(sb + i) : 0.0f;
+      }
+      for (int kb = 0; kb < kbs; ++kb) {
+        const float scale = fa[0] * fb[0];
+#pragma unroll
+        for (int i = 0; i + 1 < 3; ++i) {
+          fa[i] = fa[i + 1];
+          fb[i] = fb[i + 1];
+        }
+        if (kb + 3 < kbs) {
+          if (mine) fa[2] = __ldg(sa + (kb + 3) * p.g.ld_sa);
+          fb[2] = __ldg(sb + kb + 3);
+        }
+        const bool got = wait_soon(&ctl->acc_full[acc.at], acc.phase, abort, limit);
+        ok = __all_sync(0xFFFFFFFFu, got);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint64_t f = pack2(scale, scale);
+        const uint32_t from = taddr + acc.at * TILE_N;
+        uint32_t r[2][32];  // 32 columns are added while the next are on their way
+        tmem_ld_32x32b_x32(from, r[0]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          tmem_ld_wait();
+          if (j < 3) tmem_ld_32x32b_x32(from + (j + 1) * 32, r[(j + 1) & 1]);
+          if (j == 3) {  // everything has been read
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&ctl->acc_empty[acc.at]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            fma2_loaded(sum[j * 16 + i], r[j & 1][2 * i], r[j & 1][2 * i + 1], f);
+        }
+        acc.next(2);
+      }
+      if (!ok) break;
+      if (live && rows > 0) {
+        store_tile(p.g, stage, w.expert, w.first + quad * 32, rows, n0, [&](int j) {
+          auto put = [&](auto c) {
+            constexpr int J = decltype(c)::value;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<float4*>(stage + lane * STAGED_ROW + 4 * i) = make_float4(
+                  half_of(sum[J * 8 + 2 * i], 0), half_of(sum[J * 8 + 2 * i], 1),
+                  half_of(sum[J * 8 + 2 * i + 1], 0), half_of(sum[J * 8 + 2 * i + 1], 1));
+          };
+          of_eight(j, put);
+        });
+      }
+    }
+    if (!ok && lane == 0) give_up(abort, p.status);
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 2 * TILE_N);
+  }
+}
+
+std::atomic<uint64_t> g_allowed, g_registers;
+
+}  // namespace
+
+// Many rows, for which a thread of fp8_wide has one scale of A for 128 columns, where
+// one of fp8_few reads the scales of its columns: measured, in us with an L2 flush (few,
+// wide): 256 x 4096 x 4096 23, 29 and 1000 x 1000 x 3001 21, 25 (32 tiles); 512 x 4096 x
+// 4096 33, 29 (64 tiles); 2048^3 26, 25; 4096^3 111, 95; 4096 x 4096 x 11008 279, 220.
+// Experts, K 4096: 64 of 2048 columns, 4096 rows (64 each) 124, 128, 16384 rows 246,
+// 218; 8 experts, 512 rows of 4096 columns 44, 46, 16384 of 2048 212, 171.  Where B's
+// rows have scales of their own, both have to be read per column, and fp8_few's narrower
+// tiles are faster (4096 x 4096 x 11008: 306, 318).
+bool fp8_takes_wide(const Fp8GemmArgs& a, const LayerDevice& dev) {
+  if (a.K == 0 || !a.b_square) return false;
+  if (a.E > 0) return a.M / a.E >= TILE_M;
+  const int64_t tiles = (static_cast<int64_t>(a.M) + TILE_M - 1) / TILE_M *
+                        ((static_cast<int64_t>(a.N) + TILE_N - 1) / TILE_N);
+  return 5 * tiles >= 2 * dev.sms;
+}
+
+cudaError_t launch_fp8_wide(const CUtensorMap& tmA, const CUtensorMap& tmB, const Fp8GemmArgs& a,
+                            const LayerDevice& dev, cudaStream_t stream) {
+  cudaError_t e = allow_shared(fp8_wide_kernel, kSmemBytes, &g_allowed);
+  // The roles' register shares are drawn from what the block is launched with.
+  if (e == cudaSuccess) e = check_registers(fp8_wide_kernel, kRegsBlock, THREADS, &g_registers);
+  if (e != cudaSuccess) return e;
+  WideArgs p = {a, (a.N + TILE_N - 1) / TILE_N, 0, dev.status};
+  // (experts: at most this many units, of rows that only the device knows)
+  p.units = a.E == 0 ? (a.M + TILE_M - 1) / TILE_M : a.M / TILE_M + (a.E < a.M ? a.E : a.M);
+  const int64_t tiles = static_cast<int64_t>(p.units) * p.n_tiles;
+  if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles < dev.sms ? tiles : dev.sms));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, fp8_wide_kernel, tmA, tmB, p);
+  if (e == cudaSuccess) note_launches(1);
+  return e;
+}
+
+}  // namespace g07

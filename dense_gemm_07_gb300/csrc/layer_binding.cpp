@@ -9,6 +9,7 @@
 // A refused argument raises ValueError or TypeError, a status of the library
 // GemmError, as in the rest of the package.
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -109,7 +110,8 @@ int32_t type_of(const Tensor& t) {
 }
 
 Tensor empty(at::IntArrayRef size, at::ScalarType type, at::Device device) {
-  return at::empty(size, at::TensorOptions().dtype(type).device(device));
+  // (past torch's dispatcher, which takes most of the time of at::empty)
+  return at::detail::empty_cuda(size, type, device, std::nullopt);
 }
 
 // `out` after its checks, or a new rows x cols tensor; its row stride in *ld.
@@ -520,12 +522,13 @@ std::tuple<Tensor, Tensor> fp8_quantize(const Tensor& X, bool square, bool trans
   const int64_t ld = K > 0 ? blocks(K) * kBlock : kBlock;
   Tensor codes, scales;
   if (X.dim() == 3) {
-    codes = empty({q.batch, R, ld}, at::kFloat8_e4m3fn, device).narrow(2, 0, K);
+    codes = at::detail::empty_strided_cuda({q.batch, R, K}, {R * ld, ld, 1}, at::kFloat8_e4m3fn,
+                                           device);
     scales = empty({q.batch, blocks(R), blocks(K)}, at::kFloat, device);
     q.codes_step = R * ld;
     q.scales_step = blocks(R) * blocks(K);
   } else {
-    codes = empty({R, ld}, at::kFloat8_e4m3fn, device).narrow(1, 0, K);
+    codes = at::detail::empty_strided_cuda({R, K}, {ld, 1}, at::kFloat8_e4m3fn, device);
     scales = square ? empty({blocks(R), blocks(K)}, at::kFloat, device)
                     : empty({blocks(K), R}, at::kFloat, device);
   }
@@ -664,7 +667,8 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor> route(
   Tensor slot = empty({a.T, k}, at::kInt, device), source = empty({a.T * k}, at::kInt, device);
   Tensor offsets = empty({a.E + 1}, at::kInt, device);
   const int64_t bytes = gemm_route_workspace_bytes(a.T, a.E);
-  Tensor workspace = empty({bytes > 0 ? bytes : 0}, at::kByte, device);
+  Maybe workspace;
+  if (bytes > 0) workspace = empty({bytes}, at::kByte, device);
   run("gemm_route", device, stream, [&](void* s) {
     return gemm_route(&a, ptr<int32_t>(index), ptr<float>(weight), ptr<int32_t>(slot),
                       ptr<int32_t>(source), ptr<int32_t>(offsets), ptr(workspace), s);
@@ -673,7 +677,7 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor> route(
   // stream's work has finished; the caller keeps the outputs.
   if (stream && bytes > 0)
     c10::cuda::CUDACachingAllocator::recordStream(
-        workspace.storage().data_ptr(),
+        workspace->storage().data_ptr(),
         c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(*stream), device.index()));
   return {index, weight, slot, source, offsets};
 }

@@ -25,8 +25,10 @@ namespace {
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kChunk = kRouteChunk;
 constexpr int kWords = kChunk / 32;
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+// A token's choice is a chain of reductions: up to 256 experts, whose keys leave room
+// for it, 32 warps of an SM hide one another's.
+template <int V>
+constexpr int kThreads = V <= 8 ? 1024 : 512;
 
 // FP32 and 64-bit values as unsigned numbers in the same order; 0 is below all of
 // them and stands for "not to be chosen": NaN and -infinity.
@@ -61,46 +63,44 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
   return static_cast<unsigned long long>(top) << 32 | lo;
 }
 
+template <typename Key>
 struct Choice {
-  int index;   // lane j < k: the j-th expert or -1
-  bool close;  // a comparison was too close to tell
+  int index;  // lane j < k: the j-th expert or -1; lane k: the first that is not chosen
+  Key key;    // of it; 0: none
 };
 
-// The k largest keys, lowest index first among equals.  key[i] belongs to expert
-// i * 32 + lane.  `told(a, b)`: whether two values, a >= b, that follow each other
-// are surely in that order; same(i, j): whether experts i and j are equal in
-// everything.
-template <int V, typename Key, typename Told, typename Same>
-__device__ __forceinline__ Choice pick(Key (&key)[V], int k, Told told, Same same) {
+// The k largest keys (and the next one), lowest index first among equals.  key[i]
+// belongs to expert i * 32 + lane.  k < 32 unless nothing asks for the next one.
+template <int V, typename Key>
+__device__ __forceinline__ Choice<Key> pick(Key (&key)[V], int k) {
   const int lane = threadIdx.x & 31;
-  Choice c{-1, false};
+  Choice<Key> c{-1, 0};
   Key mine = 0;
+  auto largest = [&]() {
+    mine = key[0];
 #pragma unroll
-  for (int i = 0; i < V; ++i) mine = key[i] > mine ? key[i] : mine;
-  Key last = 0;
-  int last_at = -1;
-  for (int j = 0; j <= k; ++j) {  // one more than are chosen: the first that is not
+    for (int i = 1; i < V; ++i) mine = key[i] > mine ? key[i] : mine;
+  };
+  largest();
+  for (int j = 0; j <= k && j < 32; ++j) {
     const Key top = warp_max(mine);
     if (top == 0) break;
-    int at = 0x7FFFFFFF;
+    unsigned at = 0x7FFFFFFFu;
     if (mine == top) {
 #pragma unroll
       for (int i = V - 1; i >= 0; --i)
-        if (key[i] == top) at = i * 32 + lane;
+        if (key[i] == top) at = static_cast<unsigned>(i * 32 + lane);
     }
-    at = static_cast<int>(__reduce_min_sync(kAll, static_cast<unsigned>(at)));
-    if (j > 0 && !told(value_of(last), value_of(top)) && !same(last_at, at)) c.close = true;
-    if (j == k) break;
-    if (lane == j) c.index = at;
-    last = top;
-    last_at = at;
-    if ((at & 31) == lane) {
-      mine = 0;
+    at = __reduce_min_sync(kAll, at);
+    if (lane == j) {
+      c.index = static_cast<int>(at);
+      c.key = top;
+    }
+    if (static_cast<int>(at & 31u) == lane) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (i == at >> 5) key[i] = 0;
-        mine = key[i] > mine ? key[i] : mine;
-      }
+      for (int i = 0; i < V; ++i)
+        if (i == static_cast<int>(at >> 5)) key[i] = 0;
+      largest();
     }
   }
   return c;
@@ -114,37 +114,41 @@ __device__ __forceinline__ bool keep_groups(Key (&key)[V], int groups, int size,
                                             int group_top, Told told) {
   const int lane = threadIdx.x & 31;
   Key sum = 0;  // lane g: group g
-  for (int g = 0; g < groups; ++g) {
-    const int lo = g * size, hi = lo + size;
-    Key mine = 0;
+  auto score = [&](Key first, Key second) {
+    if (group_top == 1 || second == 0) return first;
+    return key_of(plain_zero(value_of(first) + value_of(second)));
+  };
+  if (size == 32) {  // a group is one key of each lane
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = i * 32 + lane;
-      if (e >= lo && e < hi && key[i] > mine) mine = key[i];
+      const Key first = warp_max(key[i]);
+      const int holder = __ffs(__ballot_sync(kAll, key[i] == first)) - 1;
+      const Key second = warp_max(lane == holder ? Key(0) : key[i]);
+      const Key s = score(first, second);
+      if (lane == i) sum = s;
     }
-    const Key first = warp_max(mine);
-    Key score = first;
-    if (group_top > 1 && first != 0) {
-      const int holder = __ffs(__ballot_sync(kAll, mine == first)) - 1;
-      Key next = mine;
-      if (lane == holder) {  // its second largest; the largest once
-        next = 0;
-        bool seen = false;
+  } else {
+    for (int g = 0; g < groups; ++g) {
+      const int lo = g * size, hi = lo + size;
+      Key mine = 0, next = 0;  // this lane's two largest
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int e = i * 32 + lane;
-          if (e >= lo && e < hi) {
-            if (!seen && key[i] == first)
-              seen = true;
-            else if (key[i] > next)
-              next = key[i];
+      for (int i = 0; i < V; ++i) {
+        const int e = i * 32 + lane;
+        if (e >= lo && e < hi) {
+          if (key[i] > mine) {
+            next = mine;
+            mine = key[i];
+          } else if (key[i] > next) {
+            next = key[i];
           }
         }
       }
-      const Key second = warp_max(next);
-      if (second != 0) score = key_of(plain_zero(value_of(first) + value_of(second)));
+      const Key first = warp_max(mine);
+      const int holder = __ffs(__ballot_sync(kAll, mine == first)) - 1;
+      const Key second = warp_max(lane == holder ? next : mine);
+      const Key s = score(first, second);
+      if (lane == g) sum = s;
     }
-    if (lane == g) sum = score;
   }
   unsigned keep = 0;
   Key last = 0;
@@ -163,7 +167,7 @@ __device__ __forceinline__ bool keep_groups(Key (&key)[V], int groups, int size,
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int g = (i * 32 + lane) / size;
+    const int g = size == 32 ? i : (i * 32 + lane) / size;
     if (g >= groups || !(keep >> g & 1u)) key[i] = 0;
   }
   return close;
@@ -207,7 +211,8 @@ __device__ __noinline__ int choose_64(const RouteArgs& a, const float (&l)[V], f
     for (int i = 0; i < V; ++i)
       if (key[i] != 0) key[i] = key_of(plain_zero(static_cast<double>(l[i])));
   }
-  return pick<V>(key, a.k, told, [](int, int) { return true; }).index;
+  const int at = pick<V>(key, a.k).index;
+  return lane < a.k ? at : -1;
 }
 
 // Experts (lane j: the j-th or -1) and weights of a token from its logits
@@ -306,7 +311,7 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, const float (&l)[
     for (int i = 0; i < V; ++i) key[i] = key_of(plain_zero(l[i]));
   }
 
-  auto logit = [&](int e) {  // of any expert, in every lane
+  auto logit = [&](int e) {  // of this lane's expert e
     float v = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -315,25 +320,25 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, const float (&l)[
     }
     return v;
   };
-  int at;
+  const Choice<uint32_t> c = pick<V>(key, a.k);
+  float chosen = logit(c.index);
+  int at = lane < a.k ? c.index : -1;
   if (a.bias) {
-    const Choice c = pick<V>(key, a.k, told, [&](int i, int j) {
-      return logit(i) == logit(j) && __ldg(a.bias + i) == __ldg(a.bias + j);
-    });
-    at = c.index;
-    close |= c.close;
-  } else {
-    at = pick<V>(key, a.k, exact, [](int, int) { return true; }).index;
+    // every two that follow each other have to be told apart, or equal in everything
+    const uint32_t before = __shfl_up_sync(kAll, c.key, 1);
+    const int other = __shfl_up_sync(kAll, c.index, 1);
+    const float its = __shfl_up_sync(kAll, chosen, 1);
+    bool unsure = lane > 0 && c.key != 0 && !told(value_of(before), value_of(c.key));
+    if (unsure && its == chosen) unsure = __ldg(a.bias + other) != __ldg(a.bias + c.index);
+    // (of 32 chosen ones the next is not known)
+    close |= __any_sync(kAll, unsure) || a.k == 32;
   }
-  if (close) at = choose_64<V>(a, l, top);
+  if (close) {
+    at = choose_64<V>(a, l, top);
+    chosen = logit(at);
+  }
 
   // Weights, from the scores without the bias.
-  float chosen = 0.0f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const float x = __shfl_sync(kAll, l[i], at & 31);
-    if (i == at >> 5) chosen = x;
-  }
   float w = 0.0f;
   if (a.sigmoid) {
     if (at >= 0) w = 1.0f / (1.0f + expf(-chosen));
@@ -354,7 +359,8 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, const float (&l)[
 // A block of 128 tokens: choices, weights and, for a single block, the sorted order;
 // else the number of its tokens for each expert.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(kThreads<V>) route_kernel(RouteArgs a) {
+  constexpr int kWarps = kThreads<V> / 32;
   extern __shared__ uint32_t bits[];  // [E][kWords]: the tokens of each expert; then [E] starts
   __shared__ int warp_total[kWarps];
   grid_dependency_wait();
@@ -362,7 +368,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t0 = static_cast<int>(blockIdx.x) * kChunk;
   const int tokens = a.T - t0 < kChunk ? a.T - t0 : kChunk;
-  for (int i = threadIdx.x; i < a.E * kWords; i += kThreads) bits[i] = 0;
+  for (int i = threadIdx.x; i < a.E * kWords; i += kThreads<V>) bits[i] = 0;
   __syncthreads();
   auto load = [&](int t, float (&l)[V]) {
     const T* row = static_cast<const T*>(a.logits) + (t0 + t) * a.ld;
@@ -370,17 +376,11 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
     for (int i = 0; i < V; ++i)
       l[i] = i * 32 + lane < a.E ? to_f32(row[i * 32 + lane]) : -INFINITY;
   };
-  constexpr bool kAhead = V <= 8;  // a token's logits are on their way while one is chosen
-  float l[V];
-  if (kAhead && warp < tokens) load(warp, l);
   for (int t = warp; t < tokens; t += kWarps) {
-    float now[V];
-    if (!kAhead) load(t, l);
-#pragma unroll
-    for (int i = 0; i < V; ++i) now[i] = l[i];
-    if (kAhead && t + kWarps < tokens) load(t + kWarps, l);
+    float l[V];
+    load(t, l);
     float w;
-    const int at = route_token<V>(a, now, &w);
+    const int at = route_token<V>(a, l, &w);
     if (lane < a.k) {
       const int64_t o = static_cast<int64_t>(t0 + t) * a.k + lane;
       a.index[o] = at;
@@ -396,8 +396,9 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
     return n;
   };
   if (gridDim.x > 1) {
-    for (int e = threadIdx.x; e < a.E; e += kThreads)
-      a.counts[static_cast<int64_t>(blockIdx.x) * a.E + e] = count(e);
+    for (int e = threadIdx.x; e < a.E; e += kThreads<V>)
+      a.counts[static_cast<int64_t>(blockIdx.x) * route_count_stride(a.E) + e] =
+          static_cast<uint8_t>(count(e));
     return;
   }
   // The only block: each thread holds the experts 2 i and 2 i + 1.
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
   if (threadIdx.x == 0) a.offsets[a.E] = all;
   __syncthreads();
   const int pairs = tokens * a.k;
-  for (int i = threadIdx.x; i < pairs; i += kThreads) {
+  for (int i = threadIdx.x; i < pairs; i += kThreads<V>) {
     const int t = i / a.k, e = a.index[i];
     int place = -1;
     if (e >= 0) {
@@ -456,26 +457,37 @@ __global__ void __launch_bounds__(1024) route_sort_kernel(RouteArgs a) {
   const int tokens = a.T - t0 < kChunk ? a.T - t0 : kChunk;
   for (int i = threadIdx.x; i < a.E * (kWords + 1); i += 1024) bits[i] = 0;
   __syncthreads();
-  // an expert's counts: all of them, and those before this block.  Few experts
-  // share their column among several threads.
-  const int parts = 1024 / a.E > 0 ? 1024 / a.E : 1;
-  const int e = static_cast<int>(threadIdx.x) % a.E, part = static_cast<int>(threadIdx.x) / a.E;
-  int total = 0, earlier = 0;
+  // the experts' counts, four to a word: all of them, and those before this block.  The
+  // blocks are shared among as many threads as there are.
+  const int words = route_count_stride(a.E) / 4, parts = 1024 / words;
+  const int e4 = static_cast<int>(threadIdx.x) % words, part = static_cast<int>(threadIdx.x) / words;
   if (part < parts) {
+    const uint32_t* counts = reinterpret_cast<const uint32_t*>(a.counts) + e4;
+    int total[4] = {0, 0, 0, 0}, earlier[4] = {0, 0, 0, 0};
 #pragma unroll 8
     for (int c = part; c < chunks; c += parts) {
-      const int n = __ldg(a.counts + static_cast<int64_t>(c) * a.E + e);
-      total += n;
-      earlier += c < chunk ? n : 0;
+      const uint32_t n = __ldg(counts + static_cast<int64_t>(c) * words);
+      const uint32_t m = c < chunk ? n : 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        total[i] += static_cast<int>(n >> (8 * i) & 255u);
+        earlier[i] += static_cast<int>(m >> (8 * i) & 255u);
+      }
     }
     // (sums of whole numbers: the order of the atomics does not matter)
-    atomicAdd(&start[e], total);
-    atomicAdd(reinterpret_cast<int*>(&bits[e * kWords]), earlier);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = e4 * 4 + i;
+      if (e < a.E) {
+        atomicAdd(&start[e], total[i]);
+        atomicAdd(reinterpret_cast<int*>(&bits[e * kWords]), earlier[i]);
+      }
+    }
   }
   __syncthreads();
   const bool mine = static_cast<int>(threadIdx.x) < a.E;
   const int n = mine ? start[threadIdx.x] : 0;
-  earlier = mine ? static_cast<int>(bits[threadIdx.x * kWords]) : 0;
+  const int earlier = mine ? static_cast<int>(bits[threadIdx.x * kWords]) : 0;
   int upto = n;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
@@ -614,9 +626,9 @@ cudaError_t route_of(const RouteArgs& a, bool gradient, cudaStream_t stream) {
   }
   const int chunks = a.T > kChunk ? (a.T + kChunk - 1) / kChunk : 1;  // (no token: offsets of 0)
   const size_t smem = static_cast<size_t>(a.E) * (kWords + 1) * 4;  // at most 20 KB
-  cudaError_t e = a.bf16 ? launch_pdl(route_kernel<__nv_bfloat16, V>, dim3(chunks), dim3(kThreads),
+  cudaError_t e = a.bf16 ? launch_pdl(route_kernel<__nv_bfloat16, V>, dim3(chunks), dim3(kThreads<V>),
                                       smem, stream, a)
-                         : launch_pdl(route_kernel<float, V>, dim3(chunks), dim3(kThreads), smem,
+                         : launch_pdl(route_kernel<float, V>, dim3(chunks), dim3(kThreads<V>), smem,
                                       stream, a);
   if (e == cudaSuccess && chunks > 1)
     e = launch_pdl(route_sort_kernel, dim3(chunks), dim3(1024), smem, stream, a);
