@@ -584,6 +584,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteArgs a) {
     }
 #pragma unroll
     for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, i));
+    if (top == -INFINITY) top = 0.0f;  // a token of padding: scores of 0
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -591,10 +592,9 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteArgs a) {
       sum += all[i];
     }
     sum = warp_sum(sum);
-    const float s = at >= 0 ? expf(l - top) / sum : 0.0f;
-    g = s * d;
-    const float dot = warp_sum(g);
-    rest = -dot / sum;
+    const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
+    g = at >= 0 ? expf(l - top) * inverse * d : 0.0f;
+    rest = -warp_sum(g) * inverse;
   }
   T* out = static_cast<T*>(a.d_logits) + t * a.ld_d;
   float o[V];
