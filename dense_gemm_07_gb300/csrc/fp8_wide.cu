@@ -1,7 +1,6 @@
 // fp8_wide.cu -- products of 8-bit floating-point matrices (the formula is in
 // fp8_few.cu) of many rows, on tiles of 128 rows by 256 columns of C.
 #include <atomic>
-#include <type_traits>
 
 #include "experts.h"
 #include "fp8.cuh"
@@ -17,19 +16,20 @@ constexpr int TILE_M = kFp8WideRows;  // rows of C: the MMA's lanes
 constexpr int TILE_N = 256;           // columns of C, in two halves
 constexpr int HALF = 128;
 constexpr int BK = kFp8Block;
-constexpr int STAGES = 4;
+constexpr int STAGES = 3;
 constexpr int A_BYTES = TILE_M * BK;
 constexpr int B_BYTES = TILE_N * BK;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int THREADS = 384;
 constexpr int SUM_WARPS = 8;
 constexpr int GROUP = 12;
-// A sum warp's 32 rows of 16 numbers on their way out, 20 words from one row to the
+// A sum warp's 32 rows of 64 numbers on their way out, 68 words from one row to the
 // next: rows stay on 16 bytes, and what 8 lanes store at once falls into 32 banks.
-constexpr int STAGED_ROW = 20;
+constexpr int STAGED_COLS = 64;
+constexpr int STAGED_ROW = STAGED_COLS + 4;
 constexpr int STAGED_FLOATS = 32 * STAGED_ROW;
 constexpr int STAGED_AT = STAGES * STAGE_BYTES;
-constexpr int CONTROL_AT = STAGED_AT + 8 * STAGED_FLOATS * 4;
+constexpr int CONTROL_AT = STAGED_AT + SUM_WARPS * STAGED_FLOATS * 4;
 // Registers a thread of the roles (setmaxnreg): together at most the 384 x 168 that
 // the block is launched with.
 constexpr int kRegsOther = 88, kRegsSum = 208;
@@ -126,36 +126,34 @@ __device__ __forceinline__ void finish(const EpiParams& e, const float (&bias)[N
   }
 }
 
-// 16 columns of C from n on, of the `rows` rows from `first` on, from a warp's staged
-// sums.
+// 64 columns of C from n on, of the `rows` rows from `first` on, from a warp's staged
+// sums: eight lanes a row, so that a row's part leaves as whole 128-byte lines.
 template <typename T>
 __device__ __forceinline__ void store_rows(const Fp8GemmArgs& g, T* C, const float* stage,
                                            int expert, int first, int rows, int n) {
   const int lane = threadIdx.x & 31;
   C += first * g.ldc + n;
   const float* bias = g.epi.bias ? g.epi.bias + static_cast<int64_t>(expert) * g.N + n : nullptr;
-  if (n + 16 <= g.N && ((reinterpret_cast<uintptr_t>(g.C) | (g.ldc * sizeof(T))) & 15u) == 0) {
-    const int c = (lane & 1) * 8;  // two lanes a row, 8 columns each
+  if (n + STAGED_COLS <= g.N &&
+      ((reinterpret_cast<uintptr_t>(g.C) | (g.ldc * sizeof(T))) & 15u) == 0) {
+    const int c = (lane & 7) * 8;
     float b[8], old[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) b[i] = bias ? __ldg(bias + c + i) : 0.0f;
-#pragma unroll
-    for (int r = lane >> 1; r < 32; r += 16) {
-      if (r < rows) {
-        float v[8];
-        load_vec<8>(stage + r * STAGED_ROW + c, v);
-        T* o = C + r * g.ldc + c;
-        if (g.epi.beta != 0.0f) load_vec<8>(o, old);
-        finish(g.epi, b, old, v);
-        store_vec<8>(o, v);
-      }
+#pragma unroll 2
+    for (int r = lane >> 3; r < rows; r += 4) {
+      float v[8];
+      load_vec<8>(stage + r * STAGED_ROW + c, v);
+      T* o = C + r * g.ldc + c;
+      if (g.epi.beta != 0.0f) load_vec<8>(o, old);
+      finish(g.epi, b, old, v);
+      store_vec<8>(o, v);
     }
   } else {  // a lane a column
-    const int c = lane & 15;
-    if (n + c < g.N) {
+    for (int c = lane; c < STAGED_COLS && n + c < g.N; c += 32) {
       const float b[1] = {bias ? __ldg(bias + c) : 0.0f};
 #pragma unroll 4
-      for (int r = lane >> 4; r < rows; r += 2) {
+      for (int r = 0; r < rows; ++r) {
         float v[1] = {stage[r * STAGED_ROW + c]}, old[1];
         T* o = C + r * g.ldc + c;
         if (g.epi.beta != 0.0f) old[0] = to_f32(*o);
@@ -163,40 +161,6 @@ __device__ __forceinline__ void store_rows(const Fp8GemmArgs& g, T* C, const flo
         *o = from_f32<T>(v[0]);
       }
     }
-  }
-}
-
-// f with the constant j, 0 .. 7.
-template <typename F>
-__device__ __forceinline__ void of_eight(int j, F f) {
-  switch (j) {
-    case 0: f(std::integral_constant<int, 0>()); break;
-    case 1: f(std::integral_constant<int, 1>()); break;
-    case 2: f(std::integral_constant<int, 2>()); break;
-    case 3: f(std::integral_constant<int, 3>()); break;
-    case 4: f(std::integral_constant<int, 4>()); break;
-    case 5: f(std::integral_constant<int, 5>()); break;
-    case 6: f(std::integral_constant<int, 6>()); break;
-    default: f(std::integral_constant<int, 7>()); break;
-  }
-}
-
-// The 128 columns of a warp's 32 rows, 16 at a time through the staging: put(j) stages
-// columns 16 j and on.  (A loop, with the registers picked by a switch: written out,
-// the code is several times the instruction cache's, and a tile's output took 10000
-// clocks, as long as 10 blocks of K.)
-template <typename F>
-__device__ __forceinline__ void store_tile(const Fp8GemmArgs& g, float* stage, int expert, int first,
-                                           int rows, int n0, F put) {
-#pragma unroll 1
-  for (int j = 0; j < 8 && n0 + 16 * j < g.N; ++j) {
-    __syncwarp();  // the last ones have been read
-    put(j);
-    __syncwarp();
-    if (g.c_bf16)
-      store_rows(g, static_cast<__nv_bfloat16*>(g.C), stage, expert, first, rows, n0 + 16 * j);
-    else
-      store_rows(g, static_cast<float*>(g.C), stage, expert, first, rows, n0 + 16 * j);
   }
 }
 
@@ -294,8 +258,8 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         const int cols = p.g.N - w.n0 < TILE_N ? (p.g.N - w.n0 + 15) & ~15 : TILE_N;
         const uint32_t idesc = idesc_e4m3_f32(TILE_M, cols);
         for (int kb = 0; kb < kbs; ++kb) {
-          ok = wait_soon(&ctl->acc_empty[acc.at], acc.phase ^ 1u, abort, limit) &&
-               wait_soon(&ctl->full[ring.at], ring.phase, abort, limit);
+          ok = wait_soon(&ctl->full[ring.at], ring.phase, abort, limit) &&
+               wait_soon(&ctl->acc_empty[acc.at], acc.phase ^ 1u, abort, limit);
           if (!ok) break;
           tc_fence_after_sync();
           const uint64_t at = static_cast<uint64_t>(ring.at * (STAGE_BYTES >> 4));
@@ -384,17 +348,24 @@ fp8_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       }
       if (!ok) break;
       if (live && rows > 0) {
-        store_tile(p.g, stage, w.expert, w.first + quad * 32, rows, n0, [&](int j) {
-          auto put = [&](auto c) {
-            constexpr int J = decltype(c)::value;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 2; ++j) {
+          if (n0 + j * STAGED_COLS < p.g.N) {
+            __syncwarp();  // the last ones have been read
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
               *reinterpret_cast<float4*>(stage + lane * STAGED_ROW + 4 * i) = make_float4(
-                  half_of(sum[J * 8 + 2 * i], 0), half_of(sum[J * 8 + 2 * i], 1),
-                  half_of(sum[J * 8 + 2 * i + 1], 0), half_of(sum[J * 8 + 2 * i + 1], 1));
-          };
-          of_eight(j, put);
-        });
+                  half_of(sum[j * 32 + 2 * i], 0), half_of(sum[j * 32 + 2 * i], 1),
+                  half_of(sum[j * 32 + 2 * i + 1], 0), half_of(sum[j * 32 + 2 * i + 1], 1));
+            __syncwarp();
+            if (p.g.c_bf16)
+              store_rows(p.g, static_cast<__nv_bfloat16*>(p.g.C), stage, w.expert,
+                         w.first + quad * 32, rows, n0 + j * STAGED_COLS);
+            else
+              store_rows(p.g, static_cast<float*>(p.g.C), stage, w.expert, w.first + quad * 32,
+                         rows, n0 + j * STAGED_COLS);
+          }
+        }
       }
     }
     if (!ok && lane == 0) give_up(abort, p.status);

@@ -53,7 +53,7 @@ __device__ __forceinline__ double value_of(unsigned long long key) {
 // -0 and +0 are equal numbers; keys have to be too.
 template <typename V>
 __device__ __forceinline__ V plain_zero(V v) {
-  return v == V(0) ? V(0) : v;
+  return v + V(0);
 }
 
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kAll, v); }
@@ -82,6 +82,7 @@ __device__ __forceinline__ Choice<Key> pick(Key (&key)[V], int k) {
     for (int i = 1; i < V; ++i) mine = key[i] > mine ? key[i] : mine;
   };
   largest();
+#pragma unroll 1
   for (int j = 0; j <= k && j < 32; ++j) {
     const Key top = warp_max(mine);
     if (top == 0) break;
@@ -128,6 +129,7 @@ __device__ __forceinline__ bool keep_groups(Key (&key)[V], int groups, int size,
       if (lane == i) sum = s;
     }
   } else {
+#pragma unroll 1
     for (int g = 0; g < groups; ++g) {
       const int lo = g * size, hi = lo + size;
       Key mine = 0, next = 0;  // this lane's two largest
@@ -153,6 +155,7 @@ __device__ __forceinline__ bool keep_groups(Key (&key)[V], int groups, int size,
   unsigned keep = 0;
   Key last = 0;
   bool close = false;
+#pragma unroll 1
   for (int j = 0; j <= kept; ++j) {
     const Key top = warp_max(sum);
     if (j == kept) {
@@ -376,6 +379,7 @@ __global__ void __launch_bounds__(kThreads<V>) route_kernel(RouteArgs a) {
     for (int i = 0; i < V; ++i)
       l[i] = i * 32 + lane < a.E ? to_f32(row[i * 32 + lane]) : -INFINITY;
   };
+#pragma unroll 1
   for (int t = warp; t < tokens; t += kWarps) {
     float l[V];
     load(t, l);
