@@ -25,18 +25,6 @@ __device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
-// The same by a pair of CTAs, issued by one thread of the even one: A's rows and B's
-// are split between the two CTAs' shared memory at the same offsets.
-__device__ __forceinline__ void mma_e4m3_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                                 uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // As mbar_wait, for waits that are over soon: the timer, whose reading takes longer than
 // most of them, is left alone for the first 256 polls.
 __device__ __forceinline__ bool wait_soon(uint64_t* bar, uint32_t parity, volatile int* abort,
@@ -45,30 +33,6 @@ __device__ __forceinline__ bool wait_soon(uint64_t* bar, uint32_t parity, volati
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(a, parity)) return true;
-    if ((i & 255u) == 0) {
-      if (*abort) return false;
-      const uint64_t t = global_timer_ns();
-      if (t0 == 0) t0 = t;
-      if (t - t0 > limit_ns) return false;
-    }
-  }
-}
-
-// The same, acquiring what the other CTA of a pair released.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                             uint64_t limit_ns) {
-  const uint32_t a = smem_u32(bar);
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(a), "r"(parity)
-        : "memory");
-    if (done) return true;
     if ((i & 255u) == 0) {
       if (*abort) return false;
       const uint64_t t = global_timer_ns();

@@ -1,5 +1,30 @@
 // fp8_wide.cu -- products of 8-bit floating-point matrices (the formula is in
-// fp8_few.cu) of many rows, on tiles of 128 rows by 256 columns of C.
+// fp8_few.cu) of many rows, on tiles of 128 rows by 256 columns of C, B with square
+// scales.
+//
+// A persistent block an SM walks over tiles.  The rows of A are the MMA's lanes, so that
+// a thread has one row's scale, times its 128 columns' block's of B, for all the sums it
+// adds: one multiply-add for each of them and block of 128 k, no scales to read.  Two
+// accumulators of 256 columns take turns: while the sum warps read one (tcgen05.ld
+// 32x32b: the forms that spread columns over lanes read tensor memory at half the rate),
+// the MMAs fill the other.
+//
+// Roles, 384 threads: warp 0 copies both operands by TMA (3 stages of 48 KB), warp 1
+// issues the MMAs, warp 2 works out the experts' rows, warps 4-11 add 128 columns of 32
+// rows each, and write them.
+//
+// What bounds it is the turn of an accumulator, MMAs, signal, reading, signal, which the
+// two hide only in part: four MMAs of 128 x 256 x 32 take 641 clocks back to back (of
+// 128 x 128 x 32 404), a block of K about 900.  4096 x 4096 x 11008: 195 us, 1.89
+// PFLOP/s, 49 % of twice the measured BF16 rate; 226 with bias and GELU, whose
+// exponentials and quotients keep the sum warps from the next tile; 16384 rows of 64
+// experts, 4096 x 2048, 197 us.  The last of ten waves has 8 tiles of 152.
+//
+// Tried: MMAs of 128 columns from two threads, each half with its own signals, 230 us;
+// 16 sum warps 418 to 460; the tiles on pairs of SMs (cta_group::2, 256 x 256), whose
+// signals cross SMs at every block of K, 390 to 400; scalar multiply-adds 238; the scales
+// through shared memory 252; output 16 columns at a time 220 (and 10000 clocks a tile
+// with that code written out eight times, which the instruction cache does not hold).
 #include <atomic>
 
 #include "experts.h"

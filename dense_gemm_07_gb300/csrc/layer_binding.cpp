@@ -10,7 +10,6 @@
 // GemmError, as in the rest of the package.
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
-#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -112,6 +111,18 @@ int32_t type_of(const Tensor& t) {
 Tensor empty(at::IntArrayRef size, at::ScalarType type, at::Device device) {
   // (past torch's dispatcher, which takes most of the time of at::empty)
   return at::detail::empty_cuda(size, type, device, std::nullopt);
+}
+
+// A contiguous tensor of its own over part of a block of bytes (`at` bytes in, a multiple
+// of the type's size): several outputs of a call come from one allocation, which takes as
+// long as each of them would.
+Tensor part(const Tensor& block, at::ScalarType type, at::IntArrayRef size, int64_t at) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      c10::Storage(block.storage()), block.key_set(), c10::scalarTypeToTypeMeta(type));
+  c10::TensorImpl* impl = t.unsafeGetTensorImpl();
+  impl->set_storage_offset(at / static_cast<int64_t>(c10::elementSize(type)));
+  impl->set_sizes_contiguous(size);
+  return t;
 }
 
 // `out` after its checks, or a new rows x cols tensor; its row stride in *ld.
@@ -663,22 +674,22 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor> route(
   a.groups = static_cast<int32_t>(groups);
   a.groups_kept = static_cast<int32_t>(groups_kept);
   a.group_top = static_cast<int32_t>(group_top);
-  Tensor index = empty({a.T, k}, at::kInt, device), weight = empty({a.T, k}, at::kFloat, device);
-  Tensor slot = empty({a.T, k}, at::kInt, device), source = empty({a.T * k}, at::kInt, device);
-  Tensor offsets = empty({a.E + 1}, at::kInt, device);
-  const int64_t bytes = gemm_route_workspace_bytes(a.T, a.E);
-  Maybe workspace;
-  if (bytes > 0) workspace = empty({bytes}, at::kByte, device);
+  // All outputs and the workspace are one block, which lives as long as any of them: also
+  // until the work of another stream than the current one has finished, as the outputs
+  // have to.
+  const int64_t bytes = gemm_route_workspace_bytes(a.T, a.E), n = a.T * k * 4;
+  Tensor block = empty({4 * n + (a.E + 1) * 4 + (bytes > 0 ? bytes : 0)}, at::kByte, device);
+  Tensor index = part(block, at::kInt, {a.T, k}, 0);
+  Tensor weight = part(block, at::kFloat, {a.T, k}, n);
+  Tensor slot = part(block, at::kInt, {a.T, k}, 2 * n);
+  Tensor source = part(block, at::kInt, {a.T * k}, 3 * n);
+  Tensor offsets = part(block, at::kInt, {a.E + 1}, 4 * n);
+  void* workspace =
+      bytes > 0 ? static_cast<uint8_t*>(block.data_ptr()) + 4 * n + (a.E + 1) * 4 : nullptr;
   run("gemm_route", device, stream, [&](void* s) {
     return gemm_route(&a, ptr<int32_t>(index), ptr<float>(weight), ptr<int32_t>(slot),
-                      ptr<int32_t>(source), ptr<int32_t>(offsets), ptr(workspace), s);
+                      ptr<int32_t>(source), ptr<int32_t>(offsets), workspace, s);
   });
-  // On another stream than the current one the workspace is kept until that
-  // stream's work has finished; the caller keeps the outputs.
-  if (stream && bytes > 0)
-    c10::cuda::CUDACachingAllocator::recordStream(
-        workspace->storage().data_ptr(),
-        c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(*stream), device.index()));
   return {index, weight, slot, source, offsets};
 }
 

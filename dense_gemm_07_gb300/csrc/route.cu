@@ -13,9 +13,12 @@
 // and tokens stay in order.  With more than one block the counts go through memory
 // and a second kernel adds up those of the blocks before.
 //
-// Memory bounds the large sizes (the logits are read once), latency the small ones.
-#include <cfloat>
-
+// The instructions of the choice bound it, about 1500 a token of 256 experts, on 128 of
+// 152 SMs (a block for each 128 tokens): 16384 x 256, sigmoid, bias, 4 of 8 groups, 8
+// chosen, 50 us (the logits are 17 MB, 2.5 us).  Loops that are not written out matter:
+// a choice's code written out does not stay in the instruction cache (74 against 58 us
+// under the profiler).  So do the tokens that need 64 bits: chosen by a warp alone, with
+// the other warps waiting, they took 8 us more than by all warps together.
 #include "experts.h"
 #include "kernels.h"
 
@@ -187,25 +190,28 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// The choice in 64 bits, from the definition.
+// The choice in 64 bits, from the definition: the token's logits, and in `score` the
+// sigmoid of each, or its exponential for softmax.
 template <int V>
-__device__ __noinline__ int choose_64(const RouteArgs& a, const float (&l)[V], float top) {
+__device__ __forceinline__ int choose_64(const RouteArgs& a, const float (&l)[V],
+                                         const double* score, float* weight) {
   const int lane = threadIdx.x & 31;
-  double s[V], total = 0.0;
+  double total = 0.0;
+  if (!a.sigmoid) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    s[i] = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l[i])))
-                     : exp(static_cast<double>(l[i]) - static_cast<double>(top));
-    total += s[i];
+    for (int i = 0; i < V; ++i) total += i * 32 + lane < a.E ? score[i * 32 + lane] : 0.0;
+    total = warp_sum(total);
   }
-  if (!a.sigmoid) total = warp_sum(total);
   unsigned long long key[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = i * 32 + lane;
-    double v = a.sigmoid ? s[i] : s[i] / total;
-    if (a.bias && e < a.E) v += static_cast<double>(__ldg(a.bias + e));
-    key[i] = l[i] > -INFINITY ? key_of(plain_zero(v)) : 0ull;
+    key[i] = 0ull;
+    if (e < a.E && l[i] > -INFINITY) {
+      double v = a.sigmoid ? score[e] : score[e] / total;
+      if (a.bias) v += static_cast<double>(__ldg(a.bias + e));
+      key[i] = key_of(plain_zero(v));
+    }
   }
   auto told = [](double, double) { return true; };
   if (a.kept < a.groups) keep_groups<V>(key, a.groups, a.E / a.groups, a.kept, a.group_top, told);
@@ -214,15 +220,24 @@ __device__ __noinline__ int choose_64(const RouteArgs& a, const float (&l)[V], f
     for (int i = 0; i < V; ++i)
       if (key[i] != 0) key[i] = key_of(plain_zero(static_cast<double>(l[i])));
   }
-  const int at = pick<V>(key, a.k).index;
-  return lane < a.k ? at : -1;
+  const int first = pick<V>(key, a.k).index;
+  const int at = lane < a.k ? first : -1;
+  double w = at < 0 ? 0.0 : a.sigmoid ? score[at] : score[at] / total;
+  if (a.renorm) {
+    const double sum = warp_sum(w);
+    w = sum > 0.0 ? w / sum : 0.0;
+  }
+  *weight = static_cast<float>(w) * a.scale;
+  return at;
 }
 
 // Experts (lane j: the j-th or -1) and weights of a token from its logits
-// (-infinity past the last expert).
+// (-infinity past the last expert); *unsure: a comparison was too close to tell.
 template <int V>
-__device__ __forceinline__ int route_token(const RouteArgs& a, const float (&l)[V], float* weight) {
+__device__ __forceinline__ int route_token(const RouteArgs& a, const float (&l)[V], float* weight,
+                                           bool* unsure) {
   const int lane = threadIdx.x & 31;
+  *unsure = false;
   bool nan = false;
   float mine = -INFINITY;
 #pragma unroll
@@ -325,21 +340,18 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, const float (&l)[
   };
   const Choice<uint32_t> c = pick<V>(key, a.k);
   float chosen = logit(c.index);
-  int at = lane < a.k ? c.index : -1;
+  const int at = lane < a.k ? c.index : -1;
   if (a.bias) {
     // every two that follow each other have to be told apart, or equal in everything
     const uint32_t before = __shfl_up_sync(kAll, c.key, 1);
     const int other = __shfl_up_sync(kAll, c.index, 1);
     const float its = __shfl_up_sync(kAll, chosen, 1);
-    bool unsure = lane > 0 && c.key != 0 && !told(value_of(before), value_of(c.key));
-    if (unsure && its == chosen) unsure = __ldg(a.bias + other) != __ldg(a.bias + c.index);
+    bool near = lane > 0 && c.key != 0 && !told(value_of(before), value_of(c.key));
+    if (near && its == chosen) near = __ldg(a.bias + other) != __ldg(a.bias + c.index);
     // (of 32 chosen ones the next is not known)
-    close |= __any_sync(kAll, unsure) || a.k == 32;
+    close |= __any_sync(kAll, near) || a.k == 32;
   }
-  if (close) {
-    at = choose_64<V>(a, l, top);
-    chosen = logit(at);
-  }
+  *unsure = close;
 
   // Weights, from the scores without the bias.
   float w = 0.0f;
@@ -364,11 +376,13 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, const float (&l)[
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads<V>) route_kernel(RouteArgs a) {
   constexpr int kWarps = kThreads<V> / 32;
-  extern __shared__ uint32_t bits[];  // [E][kWords]: the tokens of each expert; then [E] starts
-  __shared__ int warp_total[kWarps];
+  extern __shared__ double score[];  // [E], of a token that needs 64 bits
+  uint32_t* bits = reinterpret_cast<uint32_t*>(score + a.E);  // [E][kWords]: tokens of each expert
+  __shared__ int warp_total[kWarps], unsure[kChunk], unsure_count;
   grid_dependency_wait();
   grid_dependents_go();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) unsure_count = 0;
   const int t0 = static_cast<int>(blockIdx.x) * kChunk;
   const int tokens = a.T - t0 < kChunk ? a.T - t0 : kChunk;
   for (int i = threadIdx.x; i < a.E * kWords; i += kThreads<V>) bits[i] = 0;
@@ -379,18 +393,54 @@ __global__ void __launch_bounds__(kThreads<V>) route_kernel(RouteArgs a) {
     for (int i = 0; i < V; ++i)
       l[i] = i * 32 + lane < a.E ? to_f32(row[i * 32 + lane]) : -INFINITY;
   };
-#pragma unroll 1
-  for (int t = warp; t < tokens; t += kWarps) {
-    float l[V];
-    load(t, l);
-    float w;
-    const int at = route_token<V>(a, l, &w);
+  auto put = [&](int t, int at, float w) {
     if (lane < a.k) {
       const int64_t o = static_cast<int64_t>(t0 + t) * a.k + lane;
       a.index[o] = at;
       a.weight[o] = w;
       if (at >= 0) atomicOr(&bits[at * kWords + (t >> 5)], 1u << (t & 31));
     }
+  };
+#pragma unroll 1
+  for (int t = warp; t < tokens; t += kWarps) {
+    float l[V];
+    load(t, l);
+    float w;
+    bool close;
+    const int at = route_token<V>(a, l, &w, &close);
+    if (close) {
+      if (lane == 0) unsure[atomicAdd(&unsure_count, 1)] = t;
+    } else {
+      put(t, at, w);
+    }
+  }
+  __syncthreads();
+  // What FP32 could not tell, token by token: every thread an expert's score (a warp by
+  // itself would keep its block, and the kernel, waiting for its 64-bit exponentials),
+  // then a warp the choice.
+  const int again = unsure_count;
+#pragma unroll 1
+  for (int u = 0; u < again; ++u) {
+    const int t = unsure[u];
+    float l[V];
+    load(t, l);
+    float top = l[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+    const T* row = static_cast<const T*>(a.logits) + (t0 + t) * a.ld;
+    for (int e = threadIdx.x; e < a.E; e += kThreads<V>) {
+      const double x = static_cast<double>(to_f32(row[e]));
+      score[e] = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - static_cast<double>(top));
+    }
+    __syncthreads();
+    if (warp == 0) {
+      float w;
+      const int at = choose_64<V>(a, l, score, &w);
+      put(t, at, w);
+    }
+    __syncthreads();
   }
   __syncthreads();
   auto count = [&](int e) {
@@ -629,13 +679,14 @@ cudaError_t route_of(const RouteArgs& a, bool gradient, cudaStream_t stream) {
     return e;
   }
   const int chunks = a.T > kChunk ? (a.T + kChunk - 1) / kChunk : 1;  // (no token: offsets of 0)
-  const size_t smem = static_cast<size_t>(a.E) * (kWords + 1) * 4;  // at most 20 KB
+  const size_t sort = static_cast<size_t>(a.E) * (kWords + 1) * 4;
+  const size_t smem = static_cast<size_t>(a.E) * sizeof(double) + sort;  // at most 28 KB
   cudaError_t e = a.bf16 ? launch_pdl(route_kernel<__nv_bfloat16, V>, dim3(chunks), dim3(kThreads<V>),
                                       smem, stream, a)
                          : launch_pdl(route_kernel<float, V>, dim3(chunks), dim3(kThreads<V>), smem,
                                       stream, a);
   if (e == cudaSuccess && chunks > 1)
-    e = launch_pdl(route_sort_kernel, dim3(chunks), dim3(1024), smem, stream, a);
+    e = launch_pdl(route_sort_kernel, dim3(chunks), dim3(1024), sort, stream, a);
   if (e == cudaSuccess) note_launches(chunks > 1 ? 2 : 1);
   return e;
 }
