@@ -40,6 +40,7 @@ constexpr int B_BYTES = TILE_N * BK;
 constexpr int THREADS = 384;
 constexpr int SUM_WARPS = 8;
 constexpr int MAX_STAGES = 8;
+constexpr int MAX_SPLIT = 8;  // CTAs of a cluster
 constexpr int SLOTS = 8;  // blocks of K whose scales are staged
 // Words from one row of A's sums to the next: what a warp stores at once (8 lanes of 4
 // columns) falls into 32 banks.
@@ -81,12 +82,98 @@ __device__ __forceinline__ void give_up(volatile int* abort, unsigned int* statu
   atomicOr(status, 1u);
 }
 
+// Numbers of the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ float4 part4_of(uint32_t at, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(map_to_rank(at, rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float part_of(uint32_t at, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_to_rank(at, rank)) : "memory");
+  return v;
+}
+
+// The tile's part of C from the partial sums, a warp a row of A.  WIDE: a lane takes four
+// adjacent columns; else every 32nd, so that a warp's stores are adjacent.
+struct OutRows {
+  const Fp8GemmArgs& g;
+  const float* part;
+  const Fp8Rows& rows;
+  int n0, split, warp;
+
+  template <bool WIDE, typename T>
+  __device__ __forceinline__ void store(T* C) const {
+    const int lane = threadIdx.x & 31;
+    const float* bias =
+        g.epi.bias ? g.epi.bias + static_cast<int64_t>(rows.expert) * g.N + n0 : nullptr;
+    int col[4];
+    float b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      col[i] = WIDE ? 4 * lane + i : lane + 32 * i;
+      b[i] = bias && n0 + col[i] < g.N ? __ldg(bias + col[i]) : 0.0f;
+    }
+    C += rows.first * g.ldc + n0;
+    for (int c = warp; c < rows.count; c += SUM_WARPS * split) {
+      const float* mine = part + c * PART_ROW;
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (split == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = mine[col[i]];
+      } else {
+        // four parts of a sum are on their way together, and are added in rank order
+#pragma unroll 1
+        for (int r0 = 0; r0 < split; r0 += 4) {
+          float u[4][4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if (r0 + r >= split) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) u[r][i] = 0.0f;
+            } else if (WIDE) {
+              const float4 q = part4_of(smem_u32(mine + 4 * lane), r0 + r);
+              u[r][0] = q.x; u[r][1] = q.y; u[r][2] = q.z; u[r][3] = q.w;
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) u[r][i] = part_of(smem_u32(mine + col[i]), r0 + r);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += u[r][i];
+        }
+      }
+      T* o = C + c * g.ldc;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool in = WIDE || n0 + col[i] < g.N;
+        v[i] = epi_apply(g.epi, v[i], g.epi.beta != 0.0f && in ? to_f32(o[col[i]]) : 0.0f, b[i]);
+      }
+      if constexpr (!WIDE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n0 + col[i] < g.N) o[col[i]] = from_f32<T>(v[i]);
+      } else if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint2*>(o + 4 * lane) =
+            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+      } else {
+        *reinterpret_cast<float4*>(o + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+      }
+    }
+  }
+};
+
 // SQUARE: a block of B's scales is 128 x 128, so that sa * sb is staged; else every
 // row of B has its own and a thread multiplies by its row's.
 template <int COLS, bool SQUARE>
 __global__ void __launch_bounds__(THREADS, 2)
 fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-               const FewArgs p) {
+               const __grid_constant__ FewArgs p) {
   using Ctl = Control<COLS, SQUARE>;
   constexpr int ACCS = Ctl::ACCS;
   // 32-column chunks of a group of four sum warps, and halves of their 32 lanes: a
@@ -154,7 +241,6 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int ncols = (rows.count + 15) & ~15;
 
   const int group = (warp >> 2) & 1;         // of the sum warps: takes chunks group, group + 2, ...
-  const int tlane = (warp & 3) * 32 + lane;  // lane of the MMA, column of the tile
   // The sums leave through the ring, once every MMA that read it has completed:
   // 128 columns of C a row of A, PART_ROW apart.
   float* part = reinterpret_cast<float*>(smem);
@@ -356,31 +442,21 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     cluster_sync();
   else
     __syncthreads();
-  const int n = n0 + tlane;
-  if (warp >= 4 && n < p.g.N) {
-    const float b =
-        p.g.epi.bias ? __ldg(p.g.epi.bias + static_cast<int64_t>(rows.expert) * p.g.N + n) : 0.0f;
-    auto store = [&](int c, float v) {
-      const int64_t at = static_cast<int64_t>(rows.first + c) * p.g.ldc + n;
-      if (p.g.c_bf16) {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.g.C) + at;
-        const float old = p.g.epi.beta != 0.0f ? __bfloat162float(*o) : 0.0f;
-        *o = __float2bfloat16_rn(epi_apply(p.g.epi, v, old, b));
-      } else {
-        float* o = static_cast<float*>(p.g.C) + at;
-        const float old = p.g.epi.beta != 0.0f ? *o : 0.0f;
-        *o = epi_apply(p.g.epi, v, old, b);
-      }
-    };
-    if (p.split == 1) {
-      for (int c = group; c < rows.count; c += 2) store(c, part[c * PART_ROW + tlane]);
+  if (warp >= 4 && n0 < p.g.N) {
+    const bool bf16 = p.g.c_bf16 != 0;
+    const bool whole = n0 + TILE_N <= p.g.N && ((reinterpret_cast<uintptr_t>(p.g.C) |
+                                                 (p.g.ldc * (bf16 ? 2 : 4))) & (bf16 ? 7u : 15u)) == 0;
+    const OutRows out = {p.g, part, rows, n0, p.split, rank * SUM_WARPS + warp - 4};
+    if (bf16) {
+      if (whole)
+        out.store<true>(static_cast<__nv_bfloat16*>(p.g.C));
+      else
+        out.store<false>(static_cast<__nv_bfloat16*>(p.g.C));
     } else {
-      for (int c = rank * 2 + group; c < rows.count; c += 2 * p.split) {
-        const uint32_t at = smem_u32(part + c * PART_ROW + tlane);
-        float v = 0.0f;
-        for (int r = 0; r < p.split; ++r) v += ld_cluster_f32(map_to_rank(at, r));
-        store(c, v);
-      }
+      if (whole)
+        out.store<true>(static_cast<float*>(p.g.C));
+      else
+        out.store<false>(static_cast<float*>(p.g.C));
     }
   }
   if (p.split > 1) cluster_sync();  // the others have read this CTA's sums
@@ -423,9 +499,18 @@ cudaError_t fp8_few_plan(const Fp8GemmArgs& a, const LayerDevice& dev, Fp8FewPla
   }
   plan->cols = static_cast<int>(cols);
   plan->tiles = units * n_tiles;
-  const int64_t busy = plan->tiles;
+  // K is shared until there is a block for each SM, and on to two where that leaves a
+  // block 6 blocks of K at least (4 with few columns, whose exchange is small).  Measured,
+  // in us one after another (1, 2, 4, 8 ways): 128 x 4096 x 4096 22.5, 16.0, 11.7, 13.7;
+  // 200 x 2000 x 500 (K = 500) 9.6, 9.5, 8.1, -; 1000 x 1000 x 3001 22.0, 16.1, 14.7, 24.3;
+  // 700 x 3000 x 2000 17.0, 16.9, 23.4, 47; 1 x 4096 x 4096 14.6, 9.9, 7.3, 6.8.
+  const int64_t least = cols <= 32 ? 4 : 6;
   int split = 1;
-  while (split < 8 && busy * split * 2 <= 2 * dev.sms && kbs >= 4 * split) split *= 2;
+  for (int twice = 2; twice <= MAX_SPLIT && twice <= kbs; twice *= 2) {
+    const int64_t blocks = plan->tiles * twice;
+    if (blocks > dev.sms && (blocks > 2 * dev.sms || kbs / twice < least)) break;
+    split = twice;
+  }
   plan->split = split;
   const int control = static_cast<int>(
       cols <= 32 ? (a.b_square ? sizeof(Control<32, true>) : sizeof(Control<32, false>))

@@ -65,7 +65,8 @@ def gemm_fp8_experts(a, b, offsets, out=None, alpha=1.0, beta=0.0, bias=None, ac
 # --------------------------------------------------------------- experts
 
 class Routing(NamedTuple):
-    """Experts of T tokens, k each, and the chosen pairs sorted by expert."""
+    """Experts of T tokens, k each, and the chosen pairs sorted by expert (parts of one
+    block of memory)."""
     index: torch.Tensor    # T x k int32: the experts, best first; -1: none
     weight: torch.Tensor   # T x k float32
     slot: torch.Tensor     # T x k int32: the pair's row in the sorted order; -1: none

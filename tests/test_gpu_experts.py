@@ -80,12 +80,12 @@ def _spread(g, R, K, dtype=F32):
 
 
 QUANT = [(1, 1), (1, 128), (3, 127), (2, 129), (17, 300), (127, 1000), (16, 512), (33, 640),
-         (130, 257), (1, 4096), (200, 1), (300, 72)]
+         (130, 257), (1, 4096), (200, 1), (300, 72), (40, 132), (9, 1036)]
 
 
 @pytest.mark.parametrize("R,K", QUANT)
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("extra", [0, 8, 3])
+@pytest.mark.parametrize("extra", [0, 4, 8, 3])
 def test_quantize(R, K, dtype, extra):
     x = _spread(_gen(R * 1000 + K), R, K, dtype)
     arg = _strided(x, extra) if extra else x
@@ -409,7 +409,7 @@ def _check_route(logits, k, **kw):
 
 
 ROUTES = [(1, 1, 1), (1, 64, 4), (2, 8, 8), (5, 33, 3), (127, 60, 6), (128, 256, 8), (129, 100, 5),
-          (300, 512, 12), (1000, 72, 2), (3, 1024, 32), (200, 600, 10), (513, 16, 1)]
+          (300, 512, 12), (260, 257, 5), (300, 33, 3), (1000, 72, 2), (3, 1024, 32), (200, 600, 10), (513, 16, 1)]
 
 
 @pytest.mark.parametrize("T,E,k", ROUTES)
