@@ -410,16 +410,17 @@ std::atomic<uint64_t> g_allowed, g_registers;
 }  // namespace
 
 // Many rows, for which a thread of fp8_wide has one scale of A for 128 columns, where
-// one of fp8_few reads the scales of its columns: measured, in us with an L2 flush (few,
-// wide): 256 x 4096 x 4096 23, 29 and 1000 x 1000 x 3001 21, 25 (32 tiles); 512 x 4096 x
-// 4096 33, 29 (64 tiles); 2048^3 26, 25; 4096^3 111, 95; 4096 x 4096 x 11008 279, 220.
-// Experts, K 4096: 64 of 2048 columns, 4096 rows (64 each) 124, 128, 16384 rows 246,
-// 218; 8 experts, 512 rows of 4096 columns 44, 46, 16384 of 2048 212, 171.  Where B's
-// rows have scales of their own, both have to be read per column, and fp8_few's narrower
-// tiles are faster (4096 x 4096 x 11008: 306, 318).
+// one of fp8_few reads the scales of its columns: measured, in us one after another (few,
+// wide): 256 x 4096 x 4096 15, 21 (M x N x K, 32 tiles); 384 x 4096 x 4096 20.8, 21.2 (48);
+// 512 x 4096 x 4096 21.0, 21.3 (64); 700 x 3000 x 2000 16, 14 (72); 2048^3 19, 14; 4096 x
+// 11008 x 4096 260, 191.  Experts, by their average number of rows: 64: 512 rows of 8,
+// 4096 x 4096, 31.4, 30.5 and 4096 rows of 64, 2048 x 4096, 110, 105; 100: 6000 rows of 60,
+// 2000 x 500, 40, 29; 125: 1500 rows of 12, 700 x 2000, 16.4, 15.2; 256: 226, 187; 2048:
+// 197, 142.  Where B's rows have scales of their own, both have to be read per column, and
+// fp8_few's narrower tiles are faster (4096 x 11008 x 4096: 306, 318 with an L2 flush).
 bool fp8_takes_wide(const Fp8GemmArgs& a, const LayerDevice& dev) {
   if (a.K == 0 || !a.b_square) return false;
-  if (a.E > 0) return a.M / a.E >= TILE_M;
+  if (a.E > 0) return a.M / a.E >= TILE_M / 2;
   const int64_t tiles = (static_cast<int64_t>(a.M) + TILE_M - 1) / TILE_M *
                         ((static_cast<int64_t>(a.N) + TILE_N - 1) / TILE_N);
   return 5 * tiles >= 2 * dev.sms;
