@@ -107,8 +107,8 @@ def test_quantize_every_border():
     v = torch.cat([v, -v])
     v = torch.nn.functional.pad(v, (0, -v.numel() % 127)).view(-1, 127)
     v = torch.cat([torch.full((v.shape[0], 1), 448.0), v], 1)  # the scale is 1
-    for f in (1.0, 2.0 ** 40, 2.0 ** -60):
-        x = (v * f).cuda()
+    for f, dtype in itertools.product((1.0, 2.0 ** 40, 2.0 ** -60, 2.0 ** -126), (F32, BF16)):
+        x = (v * f).to(dtype).cuda()
         q = g7.gemm_fp8_quantize(x)
         codes, scales = ref.quantize(x.cpu())
         assert torch.equal(_bits(q.codes).cpu(), codes)
