@@ -190,6 +190,15 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
+// The sigmoid times e^-shift, shift <= 0 the largest of several logits (0 if that is
+// positive), for quotients of sigmoids: by itself it leaves FP32 below a logit of -88,
+// where the quotients are ordinary numbers.  0 where 64 bits have no sigmoid either.
+__device__ __forceinline__ float sigmoid_over(float l, float shift) {
+  const float e = expf(-fabsf(l));
+  const float top = l >= 0.0f ? 1.0f : l < -709.7f ? 0.0f : expf(l - shift);
+  return top / (1.0f + e);
+}
+
 // The choice in 64 bits, from the definition: the token's logits, and in `score` the
 // sigmoid of each, or its exponential for softmax.
 template <int V>
@@ -355,15 +364,11 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, const float (&l)[
 
   // Weights, from the scores without the bias.
   float w = 0.0f;
-  if (a.sigmoid) {
-    if (at >= 0) w = 1.0f / (1.0f + expf(-chosen));
-  } else if (!a.renorm) {
-    if (at >= 0) w = expf(chosen - top) / total;
+  if (!a.renorm) {
+    if (at >= 0) w = a.sigmoid ? 1.0f / (1.0f + expf(-chosen)) : expf(chosen - top) / total;
   } else {
     const float most = value_of(warp_max(at >= 0 ? key_of(plain_zero(chosen)) : 0u));
-    if (at >= 0) w = expf(chosen - most);
-  }
-  if (a.renorm) {
+    if (at >= 0) w = a.sigmoid ? sigmoid_over(chosen, fminf(most, 0.0f)) : expf(chosen - most);
     const float sum = warp_sum(w);
     w = sum > 0.0f ? w / sum : 0.0f;
   }
@@ -612,23 +617,20 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteArgs a) {
   float top = 0.0f;
   const bool over_all = !a.sigmoid && !a.renorm;
   float all[V];
-  if (a.sigmoid) {
-    const float s = at >= 0 ? 1.0f / (1.0f + expf(-l)) : 0.0f;
-    if (a.renorm) {
-      const float sum = warp_sum(s);
-      const float inverse = sum > 0.0f ? 1.0f / sum : 0.0f;
-      d = (d - warp_sum(d * s) * inverse) * inverse;
-    }
-    g = at >= 0 ? d * s / (1.0f + expf(l)) : 0.0f;
-  } else if (a.renorm) {
+  if (a.renorm) {
     float most = at >= 0 ? l : -INFINITY;
 #pragma unroll
     for (int i = 16; i; i >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, i));
-    float s = at >= 0 ? expf(l - most) : 0.0f;
+    float s = 0.0f;
+    if (at >= 0) s = a.sigmoid ? sigmoid_over(l, fminf(most, 0.0f)) : expf(l - most);
     const float sum = warp_sum(s);
     s = sum > 0.0f ? s / sum : s;
     const float dot = warp_sum(d * s);
     g = s * (d - dot);
+    if (a.sigmoid && at >= 0) g /= 1.0f + expf(l);
+  } else if (a.sigmoid) {
+    const float s = at >= 0 ? 1.0f / (1.0f + expf(-l)) : 0.0f;
+    g = at >= 0 ? d * s / (1.0f + expf(l)) : 0.0f;
   } else {
     top = -INFINITY;
 #pragma unroll

@@ -557,6 +557,36 @@ def test_route_gradient(T, E, k, score, renorm, dtype):
     assert torch.equal(got, g7.gemm_route_bwd(logits, index, d, score=score, renormalize=renorm, scale=1.5))
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("low", [-60.0, -88.0, -95.0, -150.0, -400.0])
+def test_route_logits_far_below_zero(score, low):
+    """Sigmoids that FP32 does not hold have quotients that it does."""
+    g = _gen(3)
+    T, E, k = 150, 48, 4
+    logits = _randn(g, T, E) + low
+    logits[0, 5] = 2.0                      # one score that is not small
+    bias = _randn(g, E)
+    for b in (None, bias):
+        _check_route(logits, k, score=score, bias=b)
+    masked = logits.clone()
+    masked[1, 5:] = torch.finfo(F32).min    # experts masked with the lowest value
+    masked[4] = torch.finfo(F32).min
+    # as _check_route's bound, by the logits that are not masks: a mask's exponent is
+    # taken to 0 or from its like
+    step = (64 + 2 * (abs(low) + 10)) * EPS32
+    got, want = g7.gemm_route(masked, k, score=score), ref.route(masked, k, score=score)
+    assert torch.equal(got.index.cpu(), want[0])
+    _close(got.weight.cpu(), want[1], step * want[1] + 1e-37, "weights")
+    index = torch.argsort(torch.rand((T, E), generator=g, device="cuda"), dim=1)[:, :k].to(torch.int32)
+    index[0, 0], index[1, 0], index[2, 3] = 5, 0, -1
+    d = 3.0 * _randn(g, T, k)
+    got = g7.gemm_route_bwd(masked, index, d, score=score)
+    want, size = ref.route_grad(masked, index, d, score, True, 1.0)
+    assert float(want.abs().max()) > 0.1
+    # as test_route_gradient's
+    _close(got, want, (96 + 4 * (abs(low) + 10)) * EPS32 * size + 1e-37, "gradient")
+
+
 # ---------------------------------------------------------------- combining
 
 def _pairs(g, T, k, R, holes=True):
