@@ -102,5 +102,7 @@ def gemm_combine(rows, slot, weight, x=None, out=None, out_dtype=None, stream=No
 
 
 def gemm_combine_bwd(d_out, rows, slot, weight, d_rows=None, stream=None):
-    """(d_rows, d_weight) of gemm_combine.  Rows that no slot names are not written."""
+    """(d_rows, d_weight) of gemm_combine for distinct slots, as a Routing's are: a row
+    that two slots name would need the sum of two gradients, and gets either of them.
+    Rows that no slot names are not written."""
     return _binding().combine_bwd(d_out, rows, slot, weight, d_rows, _handle(stream))

@@ -809,9 +809,9 @@ GEMM07_API gemm_status_t gemm_combine(const gemm_combine_args_t *args, void *out
  * gemm_combine_bwd -- from d_out (T x D, d_out_type), the gradient of out:
  *   d_rows[slot[t][j]] = weight[t][j] * d_out[t]      (R x D, the rows' type)
  *   d_weight[t][j]     = d_out[t] . rows[slot[t][j]]  (T x k; 0 without a row)
- * Rows that no slot names are left as they were; slots are distinct (where two are
- * equal, that row of d_rows is one of the two).  d_rows may be rows.  x's gradient is
- * d_out.
+ * Rows that no slot names are left as they were.  Slots are distinct, as gemm_route's
+ * are: each element of a row that two of them name is that of one of the two, not their
+ * sum.  d_rows may be rows (only with distinct slots).  x's gradient is d_out.
  */
 GEMM07_API gemm_status_t gemm_combine_bwd(const gemm_combine_args_t *args, const void *d_out,
                                           int64_t ld_d_out, int32_t d_out_type, void *d_rows,
