@@ -26,6 +26,7 @@ namespace g07 {
 namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr float kUnit = 1.2e-7f;  // a unit in the last place of FP32, relative: 2^-23
 constexpr int kChunk = kRouteChunk;
 constexpr int kWords = kChunk / 32;
 // A token's choice is a chain of reductions: up to 256 experts, whose keys leave room
@@ -112,24 +113,28 @@ __device__ __forceinline__ Choice<Key> pick(Key (&key)[V], int k) {
 
 // Leaves only the keys of the `kept` groups with the largest sums of their
 // group_top (1 or 2) largest values; a group without a key that can be chosen is
-// last.  True when it was too close to tell.
-template <int V, typename Key, typename Told>
+// last.  slack: how far the scores in such a sum, together, may be off; negative: the
+// values are exact.  FP32 keys that are not: true where another choice of groups is
+// within reach.
+template <int V, typename Key>
 __device__ __forceinline__ bool keep_groups(Key (&key)[V], int groups, int size, int kept,
-                                            int group_top, Told told) {
+                                            int group_top, float slack) {
   const int lane = threadIdx.x & 31;
-  Key sum = 0;  // lane g: group g
-  auto score = [&](Key first, Key second) {
-    if (group_top == 1 || second == 0) return first;
-    return key_of(plain_zero(value_of(first) + value_of(second)));
+  Key sum = 0;           // lane g: group g
+  float addends = 0.0f;  // of the sum: their magnitudes
+  auto put = [&](int g, Key first, Key second) {
+    const bool two = group_top != 1 && second != 0;
+    if (lane != g) return;
+    sum = two ? key_of(plain_zero(value_of(first) + value_of(second))) : first;
+    if constexpr (sizeof(Key) == 4)
+      addends = fabsf(value_of(first)) + (two ? fabsf(value_of(second)) : 0.0f);
   };
   if (size == 32) {  // a group is one key of each lane
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const Key first = warp_max(key[i]);
       const int holder = __ffs(__ballot_sync(kAll, key[i] == first)) - 1;
-      const Key second = warp_max(lane == holder ? Key(0) : key[i]);
-      const Key s = score(first, second);
-      if (lane == i) sum = s;
+      put(i, first, warp_max(lane == holder ? Key(0) : key[i]));
     }
   } else {
 #pragma unroll 1
@@ -150,26 +155,31 @@ __device__ __forceinline__ bool keep_groups(Key (&key)[V], int groups, int size,
       }
       const Key first = warp_max(mine);
       const int holder = __ffs(__ballot_sync(kAll, mine == first)) - 1;
-      const Key second = warp_max(lane == holder ? next : mine);
-      const Key s = score(first, second);
-      if (lane == g) sum = s;
+      put(g, first, warp_max(lane == holder ? next : mine));
     }
   }
   unsigned keep = 0;
-  Key last = 0;
-  bool close = false;
+  Key left = sum;
 #pragma unroll 1
-  for (int j = 0; j <= kept; ++j) {
-    const Key top = warp_max(sum);
-    if (j == kept) {
-      close = top != 0 && !told(value_of(last), value_of(top));
-      break;
-    }
+  for (int j = 0; j < kept; ++j) {
+    const Key top = warp_max(left);
     if (top == 0) break;  // the others have nothing to choose
-    const int at = __ffs(__ballot_sync(kAll, sum == top)) - 1;
+    const int at = __ffs(__ballot_sync(kAll, left == top)) - 1;
     keep |= 1u << at;
-    if (lane == at) sum = 0;
-    last = top;
+    if (lane == at) left = 0;
+  }
+  bool close = false;
+  if constexpr (sizeof(Key) == 4) {
+    if (slack >= 0.0f) {
+      // Each value was rounded at its own size, half a unit of it, and so was their sum:
+      // where they cancel, the sum's size says nothing of its error.  (A bound that is
+      // infinite, or no number, leaves it open.)
+      const float v = value_of(sum), off = slack + 2.0f * kUnit * addends;
+      const bool in = keep >> lane & 1u;
+      const Key least = __reduce_min_sync(kAll, in ? key_of(v - off) : kAll);
+      const Key most = warp_max(in || sum == 0 ? 0u : key_of(v + off));
+      close = most != 0 && most >= least;
+    }
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -222,8 +232,7 @@ __device__ __forceinline__ int choose_64(const RouteArgs& a, const float (&l)[V]
       key[i] = key_of(plain_zero(v));
     }
   }
-  auto told = [](double, double) { return true; };
-  if (a.kept < a.groups) keep_groups<V>(key, a.groups, a.E / a.groups, a.kept, a.group_top, told);
+  if (a.kept < a.groups) keep_groups<V>(key, a.groups, a.E / a.groups, a.kept, a.group_top, -1.0f);
   if (!a.bias) {  // in the order of the logits
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -294,17 +303,12 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, const float (&l)[
   // exponential's 2 + 1.2 |l| units in the last place weigh s (1 - s), at most 1/4
   // and with |l| 0.23, the quotient adds 2 units; softmax: 2 units each for
   // exponential, sum (of up to 1024 numbers, 32 a lane and 5 steps: 40) and
-  // quotient, of at most the largest score.  Two scores, and half a unit of each
-  // sum with the bias.
-  const float unit = 1.2e-7f;
-  const float slack = a.sigmoid ? 8.0f * unit : 96.0f * unit * __fdividef(1.0f, total);
+  // quotient, of at most the largest score.  Two scores (of two experts, or the two
+  // in a group's sum), and half a unit of each sum with the bias.
+  const float slack = a.sigmoid ? 8.0f * kUnit : 96.0f * kUnit * __fdividef(1.0f, total);
   auto told = [&](float hi, float lo) {
-    return hi - lo > slack + 2.0f * unit * fmaxf(fabsf(hi), fabsf(lo));
+    return hi - lo > slack + 2.0f * kUnit * fmaxf(fabsf(hi), fabsf(lo));
   };
-  auto told_sum = [&](float hi, float lo) {
-    return hi - lo > 2.0f * slack + 6.0f * unit * (fabsf(hi) + fabsf(lo) + 1.0f);
-  };
-  auto exact = [](float, float) { return true; };
 
   uint32_t key[V];
   bool close = false;
@@ -316,11 +320,11 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, const float (&l)[
         const float v = s[i] + (a.bias && e < a.E ? __ldg(a.bias + e) : 0.0f);
         key[i] = l[i] > -INFINITY ? key_of(plain_zero(v)) : 0u;
       }
-      close = keep_groups<V>(key, a.groups, a.E / a.groups, a.kept, a.group_top, told_sum);
+      close = keep_groups<V>(key, a.groups, a.E / a.groups, a.kept, a.group_top, slack);
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) key[i] = key_of(plain_zero(l[i]));
-      keep_groups<V>(key, a.groups, a.E / a.groups, a.kept, a.group_top, exact);
+      keep_groups<V>(key, a.groups, a.E / a.groups, a.kept, a.group_top, -1.0f);
     }
     if (!a.bias) {  // within the groups by the logits
 #pragma unroll
