@@ -19,6 +19,8 @@
 // matter: a choice's code written out does not stay in the instruction cache (74 against
 // 58 us under the profiler).  So do the tokens that need 64 bits: chosen by a warp alone,
 // with the other warps waiting, 70 us with an L2 flush, by all warps together 62.
+#include <cfloat>
+
 #include "experts.h"
 #include "kernels.h"
 
@@ -120,14 +122,22 @@ template <int V, typename Key>
 __device__ __forceinline__ bool keep_groups(Key (&key)[V], int groups, int size, int kept,
                                             int group_top, float slack) {
   const int lane = threadIdx.x & 31;
-  Key sum = 0;           // lane g: group g
-  float addends = 0.0f;  // of the sum: their magnitudes
+  Key sum = 0;            // lane g: group g
+  float rounding = 0.0f;  // of the sum
   auto put = [&](int g, Key first, Key second) {
     const bool two = group_top != 1 && second != 0;
     if (lane != g) return;
-    sum = two ? key_of(plain_zero(value_of(first) + value_of(second))) : first;
-    if constexpr (sizeof(Key) == 4)
-      addends = fabsf(value_of(first)) + (two ? fabsf(value_of(second)) : 0.0f);
+    sum = first;
+    if constexpr (sizeof(Key) == 4) rounding = 2.0f * kUnit * fabsf(value_of(first));
+    if (!two) return;
+    auto v = value_of(first) + value_of(second);
+    if constexpr (sizeof(Key) == 4) {
+      rounding += 2.0f * kUnit * fabsf(value_of(second));
+      // (masks of the type's lowest value add up to less than FP32 holds: held at its
+      // lowest, within the bound of which 64 bits decide)
+      v = fmaxf(v, -FLT_MAX);
+    }
+    sum = key_of(plain_zero(v));
   };
   if (size == 32) {  // a group is one key of each lane
 #pragma unroll
@@ -174,7 +184,7 @@ __device__ __forceinline__ bool keep_groups(Key (&key)[V], int groups, int size,
       // Each value was rounded at its own size, half a unit of it, and so was their sum:
       // where they cancel, the sum's size says nothing of its error.  (A bound that is
       // infinite, or no number, leaves it open.)
-      const float v = value_of(sum), off = slack + 2.0f * kUnit * addends;
+      const float v = value_of(sum), off = slack + rounding;
       const bool in = keep >> lane & 1u;
       const Key least = __reduce_min_sync(kAll, in ? key_of(v - off) : kAll);
       const Key most = warp_max(in || sum == 0 ? 0u : key_of(v + off));

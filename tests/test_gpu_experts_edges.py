@@ -5,7 +5,7 @@ import itertools
 import pytest
 import torch
 
-from test_gpu_experts import _check_route, _gen
+from test_gpu_experts import F32, INF, _check_route, _gen, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,19 @@ def test_route_groups_whose_biases_cancel(score, size, groups, kept):
         logits = _pairs_of_near_sums(g, 1500, groups, score, spread)
         _check_route(logits, min(3, 2 * kept), score=score, bias=bias, groups=groups,
                      groups_kept=kept, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("mask", [torch.finfo(F32).min, -2.5e38])
+def test_route_groups_masked_by_the_bias(score, mask):
+    """Two masks add up to less than FP32 holds: the group comes last, but it is there."""
+    g = _gen(2)
+    logits = _randn(g, 70, 24)
+    logits[5, 8:12] = -INF                  # a closed group besides
+    bias = _randn(g, 24, scale=0.1)
+    for groups in ((0, 1, 2, 3, 4, 5), (1, 2, 4), (0, 1, 3, 4, 5)):
+        masked = bias.clone()
+        for i in groups:
+            masked[4 * i:4 * i + 4] = mask
+        for kept, k in ((1, 4), (3, 8), (5, 20)):
+            _check_route(logits, k, score=score, bias=masked, groups=6, groups_kept=kept, group_top=2)
