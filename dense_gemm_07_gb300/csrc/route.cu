@@ -71,16 +71,17 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
 
 template <typename Key>
 struct Choice {
-  int index;  // lane j < k: the j-th expert or -1; lane k: the first that is not chosen
+  int index;  // lane j < k: the j-th expert or -1
   Key key;    // of it; 0: none
+  Key rest;   // the largest of this lane's that are not chosen
 };
 
-// The k largest keys (and the next one), lowest index first among equals.  key[i]
-// belongs to expert i * 32 + lane.  k < 32 unless nothing asks for the next one.
+// The k largest keys, lowest index first among equals.  key[i] belongs to expert
+// i * 32 + lane; those that are not chosen are left.
 template <int V, typename Key>
 __device__ __forceinline__ Choice<Key> pick(Key (&key)[V], int k) {
   const int lane = threadIdx.x & 31;
-  Choice<Key> c{-1, 0};
+  Choice<Key> c{-1, 0, 0};
   Key mine = 0;
   auto largest = [&]() {
     mine = key[0];
@@ -89,7 +90,7 @@ __device__ __forceinline__ Choice<Key> pick(Key (&key)[V], int k) {
   };
   largest();
 #pragma unroll 1
-  for (int j = 0; j <= k && j < 32; ++j) {
+  for (int j = 0; j < k; ++j) {
     const Key top = warp_max(mine);
     if (top == 0) break;
     unsigned at = 0x7FFFFFFFu;
@@ -110,6 +111,7 @@ __device__ __forceinline__ Choice<Key> pick(Key (&key)[V], int k) {
       largest();
     }
   }
+  c.rest = mine;
   return c;
 }
 
@@ -371,8 +373,19 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, const float (&l)[
     const float its = __shfl_up_sync(kAll, chosen, 1);
     bool near = lane > 0 && c.key != 0 && !told(value_of(before), value_of(c.key));
     if (near && its == chosen) near = __ldg(a.bias + other) != __ldg(a.bias + c.index);
-    // (of 32 chosen ones the next is not known)
-    close |= __any_sync(kAll, near) || a.k == 32;
+    // and so has everything that is left from the last: behind one that is its equal
+    // there may be another that is not
+    const uint32_t last = __shfl_sync(kAll, c.key, a.k - 1);
+    const bool behind = last != 0 && c.rest != 0 && !told(value_of(last), value_of(c.rest));
+    if (__any_sync(kAll, behind)) {
+      const float last_logit = __shfl_sync(kAll, chosen, a.k - 1);
+      const float last_bias = __ldg(a.bias + __shfl_sync(kAll, c.index, a.k - 1));
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (key[i] != 0 && !told(value_of(last), value_of(key[i])))
+          near |= l[i] != last_logit || __ldg(a.bias + i * 32 + lane) != last_bias;
+    }
+    close |= __any_sync(kAll, near);
   }
   *unsure = close;
 

@@ -49,3 +49,32 @@ def test_route_groups_masked_by_the_bias(score, mask):
             masked[4 * i:4 * i + 4] = mask
         for kept, k in ((1, 4), (3, 8), (5, 20)):
             _check_route(logits, k, score=score, bias=masked, groups=6, groups_kept=kept, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("alike,k,groups,kept", [(2, 1, 1, 1), (3, 2, 1, 1), (5, 1, 1, 1), (34, 32, 1, 1), (4, 3, 2, 1)])
+def test_route_equal_experts_before_a_near_one(score, alike, k, groups, kept):
+    """The last one chosen ties with the next, and a third one, behind both in FP32, is
+    ahead of them in 64 bits."""
+    g = _gen(alike)
+    E = 2 * alike + 2
+    one = _randn(g, 1, E)
+    one[:, :alike] = one[:, :1]
+    logits = one + 1e-7 * _randn(g, 1500, E)
+    logits[:, :alike] = logits[:, :1]       # experts that are the same in everything
+    s = torch.softmax(one.double(), 1) if score == "softmax" else torch.sigmoid(one.double())
+    bias = (1.5 - s[0]).float()
+    bias[alike + 1:] -= 3.0                 # one expert is near them, the others are not
+    _check_route(logits, k, score=score, bias=bias, groups=groups, groups_kept=kept)
+
+
+def test_route_all_places_taken():
+    """32 chosen experts with a bias, near ties at the last place among them."""
+    g = _gen(8)
+    for E in (32, 33, 70, 300):
+        logits = _randn(g, 200, E)
+        bias = _randn(g, E, scale=0.3)
+        near = (1.5 - torch.sigmoid(logits[:1].double()))[0].float()
+        for b in (bias, torch.zeros_like(bias), near):
+            _check_route(logits, 32, score="sigmoid", bias=b)
+            _check_route(logits[:1] + 1e-7 * _randn(g, 200, E), 32, score="sigmoid", bias=b)
