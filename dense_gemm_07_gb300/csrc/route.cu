@@ -648,6 +648,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteArgs a) {
     float most = at >= 0 ? l : -INFINITY;
 #pragma unroll
     for (int i = 16; i; i >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, i));
+    if (most == -INFINITY) most = 0.0f;  // closed experts: scores of 0
     float s = 0.0f;
     if (at >= 0) s = a.sigmoid ? sigmoid_over(l, fminf(most, 0.0f)) : expf(l - most);
     const float sum = warp_sum(s);

@@ -775,9 +775,10 @@ GEMM07_API gemm_status_t gemm_route(const gemm_route_args_t *args, int32_t *inde
 /*
  * gemm_route_bwd -- d_logits (T x E, the logits' type, row stride ld_d) from d_weight
  * (T x k), the gradient of the weights, and the index that gemm_route gave.  The
- * choice itself has no gradient.  Indices outside 0 .. E - 1 contribute nothing, one
- * that comes twice contributes twice.  Of the arguments T, E, k, the logits, score,
- * renormalize and scale count.  d_logits may be the logits.
+ * choice itself has no gradient.  Indices outside 0 .. E - 1 and experts with the logit
+ * -infinity contribute nothing, an index that comes twice contributes twice.  Of the
+ * arguments T, E, k, the logits, score, renormalize and scale count.  d_logits may be
+ * the logits.
  */
 GEMM07_API gemm_status_t gemm_route_bwd(const gemm_route_args_t *args, const int32_t *index,
                                         const float *d_weight, void *d_logits, int64_t ld_d,

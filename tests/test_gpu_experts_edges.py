@@ -5,7 +5,8 @@ import itertools
 import pytest
 import torch
 
-from test_gpu_experts import F32, INF, _check_route, _gen, _randn
+import dense_gemm_07_gb300 as g7
+from test_gpu_experts import BF16, F32, INF, _check_route, _gen, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +79,23 @@ def test_route_all_places_taken():
         for b in (bias, torch.zeros_like(bias), near):
             _check_route(logits, 32, score="sigmoid", bias=b)
             _check_route(logits[:1] + 1e-7 * _randn(g, 200, E), 32, score="sigmoid", bias=b)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_route_gradient_of_closed_experts(score, dtype):
+    """Experts whose logits are all -infinity have weights of 0, and gradients of 0."""
+    g = _gen(5)
+    logits = _randn(g, 20, 40, dtype=dtype)
+    logits[3] = -INF
+    logits[4, :8] = -INF
+    index = torch.arange(8, dtype=torch.int32, device="cuda").repeat(20, 1)
+    index[3, 2], index[4, 5] = -1, 3
+    d = _randn(g, 20, 8)
+    for renorm in (True, False):
+        got = g7.gemm_route_bwd(logits, index, d, score=score, renormalize=renorm)
+        zero = torch.zeros_like(got[3:5])
+        assert torch.equal(got[3:5], zero), renorm
+        kept = [i for i in range(20) if i not in (3, 4)]
+        want = g7.gemm_route_bwd(logits[kept], index[kept], d[kept], score=score, renormalize=renorm)
+        assert torch.equal(got[kept], want) and bool((want != 0).any(1).all())
