@@ -11,6 +11,7 @@
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
 
@@ -155,6 +156,16 @@ void run(const char* where, at::Device device, const std::optional<int64_t>& str
   const gemm_status_t status = call(s);
   if (before != index) c10::cuda::set_device(before);
   check_status(status, where);
+}
+
+// Runs work of torch's own on the stream that the call runs on.
+template <typename F>
+void on_stream(at::Device device, const std::optional<int64_t>& stream, F work) {
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  if (stream)
+    guard.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(*stream),
+                                                        device.index()));
+  work();
 }
 
 // ---------------------------------------------------------- 4-bit weights
@@ -762,6 +773,8 @@ std::tuple<Tensor, Tensor> combine_bwd(const Tensor& d_out, const Tensor& rows, 
       matrix(d_out, "d_out", {at::kFloat, at::kBFloat16}, device, a.T, a.D);
   int64_t ld = 0;
   Tensor d_rows = output(d_rows_, "d_rows", a.R, a.D, rows.scalar_type(), device, &ld);
+  // Only the device knows which rows no slot names: theirs is the gradient of nothing.
+  if (!d_rows_ && d_rows.numel() > 0) on_stream(device, stream, [&] { d_rows.zero_(); });
   Tensor d_weight = empty({a.T, a.k}, at::kFloat, device);
   run("gemm_combine_bwd", device, stream, [&](void* s) {
     return gemm_combine_bwd(&a, ptr(d_out), ld_d, type_of(d_out), ptr(d_rows), ld,

@@ -104,5 +104,6 @@ def gemm_combine(rows, slot, weight, x=None, out=None, out_dtype=None, stream=No
 def gemm_combine_bwd(d_out, rows, slot, weight, d_rows=None, stream=None):
     """(d_rows, d_weight) of gemm_combine for distinct slots, as a Routing's are: a row
     that two slots name would need the sum of two gradients, and gets either of them.
-    Rows that no slot names are not written."""
+    Rows that no slot names are zero in a new d_rows, which the call clears first, and
+    stay as they are in one that is passed."""
     return _binding().combine_bwd(d_out, rows, slot, weight, d_rows, _handle(stream))

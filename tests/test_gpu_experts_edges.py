@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import dense_gemm_07_gb300 as g7
-from test_gpu_experts import BF16, F32, INF, _check_route, _gen, _randn
+from test_gpu_experts import BF16, F32, INF, NAN, _check_route, _gen, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +99,56 @@ def test_route_gradient_of_closed_experts(score, dtype):
         kept = [i for i in range(20) if i not in (3, 4)]
         want = g7.gemm_route_bwd(logits[kept], index[kept], d[kept], score=score, renormalize=renorm)
         assert torch.equal(got[kept], want) and bool((want != 0).any(1).all())
+
+
+# -------------------------------------------- tensors that the call makes
+
+def _leave(value, *shapes):
+    """Leaves a value in memory that the next tensors of these shapes are likely to get."""
+    blocks = [torch.full(s, value, dtype=d, device="cuda") for s, d in shapes for _ in range(3)]
+    torch.cuda.synchronize()
+    del blocks
+
+
+@pytest.mark.parametrize("D", [64, 1000, 3001])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_combine_gradient_of_rows_without_a_slot(D, dtype):
+    """A new d_rows has zeros in rows that no slot names; one that is passed keeps them."""
+    g = _gen(D)
+    logits = _randn(g, 40, 12)
+    logits[30:] = -INF
+    r = g7.gemm_route(logits, 3)
+    rows, d = _randn(g, 120, D, dtype=dtype), _randn(g, 40, D)
+    slot = r.slot.clone()
+    slot[2] = -1
+    named = torch.zeros(120, dtype=torch.bool, device="cuda")
+    named[slot[slot >= 0].long()] = True
+    old = _randn(g, 120, D, dtype=dtype)
+    want, dw = g7.gemm_combine_bwd(d, rows, slot, r.weight, d_rows=old.clone())
+    assert torch.equal(want[~named], old[~named])
+    want[~named] = 0
+    other = torch.cuda.Stream()
+    for stream in (None, other):
+        for _ in range(3):
+            _leave(NAN, ((120, D), dtype), ((40, 3), F32))
+            other.wait_stream(torch.cuda.current_stream())
+            got, w = g7.gemm_combine_bwd(d, rows, slot, r.weight, stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(got, want) and torch.equal(w, dw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got, w = g7.gemm_combine_bwd(d, rows, slot, r.weight)
+    for _ in range(2):
+        got.fill_(NAN)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(w, dw)
+    # no slot at all
+    none = torch.full_like(slot, -1)
+    _leave(NAN, ((120, D), dtype))
+    got, w = g7.gemm_combine_bwd(d, rows, none, r.weight)
+    assert torch.equal(got, torch.zeros_like(got)) and torch.equal(w, torch.zeros_like(w))
+    empty = torch.empty((40, 0), dtype=torch.int32, device="cuda")
+    _leave(NAN, ((120, D), dtype))
+    got, _ = g7.gemm_combine_bwd(d, rows, empty, empty.float())
+    assert torch.equal(got, torch.zeros_like(got))
