@@ -10,12 +10,14 @@
 // GemmError, as in the rest of the package.
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <initializer_list>
+#include <limits>
 #include <optional>
 #include <string>
 #include <tuple>
@@ -109,9 +111,56 @@ int32_t type_of(const Tensor& t) {
   return t.scalar_type() == at::kBFloat16 ? GEMM_TYPE_BF16 : GEMM_TYPE_F32;
 }
 
-Tensor empty(at::IntArrayRef size, at::ScalarType type, at::Device device) {
-  // (past torch's dispatcher, which takes most of the time of at::empty)
-  return at::detail::empty_cuda(size, type, device, std::nullopt);
+// Runs work of torch's own on the stream that the call runs on.
+template <typename F>
+void on_stream(at::Device device, const std::optional<int64_t>& stream, F work) {
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  if (stream)
+    guard.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(*stream),
+                                                        device.index()));
+  work();
+}
+
+// New tensors come straight from the allocator, past torch's dispatcher, which takes most
+// of the time of at::empty.  Where torch does more than to allocate, it is still done:
+// dispatch modes see the call, and in deterministic mode memory that nothing may be
+// written to is filled, on the stream of the call (work there could run before a fill on
+// the current stream, which is at::empty's: with both, modes do not see the call).
+bool fills() {
+  const at::Context& torch = at::globalContext();
+  return torch.deterministicAlgorithms() && torch.deterministicFillUninitializedMemory();
+}
+template <typename Seen, typename Plain>
+Tensor fresh(at::Device device, const std::optional<int64_t>& stream, Seen seen, Plain plain) {
+  const bool fill = fills();
+  if (!(fill && stream) && c10::impl::TorchDispatchModeTLS::any_modes_set()) return seen();
+  Tensor t = plain();
+  if (fill && t.numel() > 0)
+    on_stream(device, stream, [&] {  // (as torch does: NaN, or the largest whole number)
+      if (t.is_floating_point())
+        t.fill_(std::numeric_limits<double>::quiet_NaN());
+      else
+        t.fill_(255);  // bytes
+    });
+  return t;
+}
+
+Tensor empty(at::IntArrayRef size, at::ScalarType type, at::Device device,
+             const std::optional<int64_t>& stream) {
+  return fresh(
+      device, stream,
+      [&] { return at::empty(size, at::TensorOptions().dtype(type).device(device)); },
+      [&] { return Tensor(at::detail::empty_cuda(size, type, device, std::nullopt)); });
+}
+
+Tensor empty_strided(at::IntArrayRef size, at::IntArrayRef strides, at::ScalarType type,
+                     at::Device device, const std::optional<int64_t>& stream) {
+  return fresh(
+      device, stream,
+      [&] {
+        return at::empty_strided(size, strides, at::TensorOptions().dtype(type).device(device));
+      },
+      [&] { return Tensor(at::detail::empty_strided_cuda(size, strides, type, device)); });
 }
 
 // A contiguous tensor of its own over part of a block of bytes (`at` bytes in, a multiple
@@ -128,13 +177,13 @@ Tensor part(const Tensor& block, at::ScalarType type, at::IntArrayRef size, int6
 
 // `out` after its checks, or a new rows x cols tensor; its row stride in *ld.
 Tensor output(const Maybe& out, const char* name, int64_t rows, int64_t cols, at::ScalarType type,
-              at::Device device, int64_t* ld) {
+              at::Device device, int64_t* ld, const std::optional<int64_t>& stream) {
   if (out) {
     *ld = matrix(*out, name, {type}, device, rows, cols);
     return *out;
   }
   *ld = cols > 1 ? cols : 1;
-  return empty({rows, cols}, type, device);
+  return empty({rows, cols}, type, device, stream);
 }
 
 int32_t activation(const std::string& name) {
@@ -156,16 +205,6 @@ void run(const char* where, at::Device device, const std::optional<int64_t>& str
   const gemm_status_t status = call(s);
   if (before != index) c10::cuda::set_device(before);
   check_status(status, where);
-}
-
-// Runs work of torch's own on the stream that the call runs on.
-template <typename F>
-void on_stream(at::Device device, const std::optional<int64_t>& stream, F work) {
-  c10::cuda::OptionalCUDAStreamGuard guard;
-  if (stream)
-    guard.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(*stream),
-                                                        device.index()));
-  work();
 }
 
 // ---------------------------------------------------------- 4-bit weights
@@ -206,7 +245,7 @@ Tensor w4(const Tensor& A, const Tensor& packed, const Tensor& scales, const May
   if (type != at::kFloat && type != at::kBFloat16)
     bad_type("out_dtype must be torch.float32 or torch.bfloat16");
   int64_t ldc = 0;
-  Tensor out = output(out_, "out", M, N, type, device, &ldc);
+  Tensor out = output(out_, "out", M, N, type, device, &ldc, stream);
   if (bias) vector(*bias, "bias", device, N);
   const gemm_epilogue_t epi = {static_cast<float>(alpha), static_cast<float>(beta),
                                ptr<float>(bias), activation(act)};
@@ -221,7 +260,7 @@ Tensor w4_pack(const Tensor& codes, const std::optional<int64_t>& stream) {
   const at::Device device = cuda_device(codes, "codes");
   const int64_t ld = matrix(codes, "codes", {at::kByte}, device);
   const int64_t K = codes.size(0), N = codes.size(1);
-  Tensor packed = empty({packed_bytes(K, N)}, at::kByte, device);
+  Tensor packed = empty({packed_bytes(K, N)}, at::kByte, device, stream);
   run("gemm_w4_pack", device, stream, [&](void* s) {
     return gemm_w4_pack(K, N, ptr<uint8_t>(codes), ld, ptr(packed), s);
   });
@@ -233,10 +272,10 @@ std::tuple<Tensor, Tensor, Maybe> w4_quantize(const Tensor& B, int64_t group, bo
   const at::Device device = cuda_device(B, "B");
   const int64_t ldb = matrix(B, "B", {at::kFloat, at::kBFloat16}, device);
   const int64_t K = B.size(0), N = B.size(1), G = groups_of(K, group);
-  Tensor packed = empty({packed_bytes(K, N)}, at::kByte, device);
-  Tensor scales = empty({G, N}, at::kBFloat16, device);
+  Tensor packed = empty({packed_bytes(K, N)}, at::kByte, device, stream);
+  Tensor scales = empty({G, N}, at::kBFloat16, device, stream);
   Maybe zeros;
-  if (!symmetric) zeros = empty({G, N}, at::kByte, device);
+  if (!symmetric) zeros = empty({G, N}, at::kByte, device, stream);
   const int64_t ld = N > 1 ? N : 1;
   run("gemm_w4_quantize", device, stream, [&](void* s) {
     return gemm_w4_quantize(K, N, static_cast<int32_t>(group), ptr(B), ldb, type_of(B), ptr(packed),
@@ -252,7 +291,7 @@ Tensor w4_unpack(const Tensor& packed, const Tensor& scales, const Maybe& zeros,
   const int64_t K = rows ? *rows : scales.size(0) * group;
   int64_t N = 0;
   const gemm_w4_t w = weights(packed, scales, zeros, group, K, device, &N);
-  Tensor out = empty({K, N}, at::kBFloat16, device);
+  Tensor out = empty({K, N}, at::kBFloat16, device, stream);
   run("gemm_w4_unpack", device, stream, [&](void* s) {
     return gemm_w4_unpack(K, N, &w, ptr<uint16_t>(out), N > 1 ? N : 1, s);
   });
@@ -320,10 +359,10 @@ std::tuple<Tensor, Maybe> norm_gate(const Tensor& x, const Maybe& y, const Maybe
   const gemm_norm_gate_args_t a =
       norm_args(x, y, weight_post, gate, weight_pre, scale, eps, device);
   int64_t ld_o = 0, ldh = a.D;
-  Tensor x_out = output(x_out_, "x_out", a.T, a.D, x.scalar_type(), device, &ld_o);
+  Tensor x_out = output(x_out_, "x_out", a.T, a.D, x.scalar_type(), device, &ld_o, stream);
   Maybe h;
   if (weight_pre)
-    h = output(h_, "h", a.T, a.D, at::kBFloat16, device, &ldh);
+    h = output(h_, "h", a.T, a.D, at::kBFloat16, device, &ldh, stream);
   else if (h_)
     bad_value("h needs weight_pre");
   run("gemm_norm_gate", device, stream, [&](void* s) {
@@ -349,14 +388,14 @@ std::tuple<Tensor, Maybe, Maybe, Maybe, Maybe> norm_gate_bwd(
     g.dh_type = type_of(*d_h);
   }
   g.dh = ptr(d_h);
-  Tensor dx = empty({a.T, a.D}, x.scalar_type(), device);
+  Tensor dx = empty({a.T, a.D}, x.scalar_type(), device, stream);
   Maybe dy, dw_post, dgate, dw_pre;
-  if (y) dy = empty({a.T, a.D}, at::kBFloat16, device);
-  if (weight_post) dw_post = empty({a.D}, at::kFloat, device);
-  if (gate) dgate = empty(gate->sizes(), at::kFloat, device);
+  if (y) dy = empty({a.T, a.D}, at::kBFloat16, device, stream);
+  if (weight_post) dw_post = empty({a.D}, at::kFloat, device, stream);
+  if (gate) dgate = empty(gate->sizes(), at::kFloat, device, stream);
   if (a.gate_mode == GEMM_GATE_FULL && a.ld_gate > a.D)  // dgate has the gate's row stride
-    dgate = empty({a.T, a.ld_gate}, at::kFloat, device).narrow(1, 0, a.D);
-  if (weight_pre) dw_pre = empty({a.D}, at::kFloat, device);
+    dgate = empty({a.T, a.ld_gate}, at::kFloat, device, stream).narrow(1, 0, a.D);
+  if (weight_pre) dw_pre = empty({a.D}, at::kFloat, device, stream);
   g.dx = ptr(dx);
   g.dy = ptr<uint16_t>(dy);
   g.dgate = ptr<float>(dgate);
@@ -389,11 +428,11 @@ std::tuple<Tensor, Tensor, Maybe> ckpt8_pack(const Tensor& X, const std::optiona
   int64_t ld = N > 1 ? N : 1;
   Maybe act_out;
   if (act)
-    act_out = output(act_out_, "act_out", T, N, at::kBFloat16, device, &ld);
+    act_out = output(act_out_, "act_out", T, N, at::kBFloat16, device, &ld, stream);
   else if (act_out_)
     bad_value("act_out needs an activation");
-  Tensor q = empty({runs * kRun * N}, at::kByte, device);
-  Tensor scales = empty({runs, N}, at::kByte, device);
+  Tensor q = empty({runs * kRun * N}, at::kByte, device, stream);
+  Tensor scales = empty({runs, N}, at::kByte, device, stream);
   run("gemm_ckpt8_pack", device, stream, [&](void* s) {
     return gemm_ckpt8_pack(T, N, ptr(X), ldx, type_of(X), ptr(q), ptr<uint8_t>(scales), kind,
                            ptr<uint16_t>(act_out), ld, s);
@@ -407,7 +446,7 @@ Tensor ckpt8_unpack(const Tensor& q, const Tensor& scales, int64_t T, int64_t N,
   kept(q, scales, T, N, device);
   if (type != at::kFloat && type != at::kBFloat16)
     bad_type("dtype must be torch.float32 or torch.bfloat16");
-  Tensor out = empty({T, N}, type, device);
+  Tensor out = empty({T, N}, type, device, stream);
   run("gemm_ckpt8_unpack", device, stream, [&](void* s) {
     return gemm_ckpt8_unpack(T, N, ptr(q), ptr<uint8_t>(scales), ptr(out), N > 1 ? N : 1,
                              type_of(out), s);
@@ -424,9 +463,9 @@ std::tuple<Tensor, Maybe> ckpt8_act_grad(const Tensor& grad, const Tensor& q, co
   const int64_t ldg = matrix(grad, "grad", {at::kFloat, at::kBFloat16}, device, T, N);
   const int32_t kind = activation(act);
   int64_t ld = 0;
-  Tensor out = output(out_, "out", T, N, at::kBFloat16, device, &ld);
+  Tensor out = output(out_, "out", T, N, at::kBFloat16, device, &ld, stream);
   Maybe dbias;
-  if (bias_grad) dbias = empty({N}, at::kFloat, device);
+  if (bias_grad) dbias = empty({N}, at::kFloat, device, stream);
   run("gemm_ckpt8_act_grad", device, stream, [&](void* s) {
     return gemm_ckpt8_act_grad(T, N, ptr(grad), ldg, type_of(grad), ptr(q), ptr<uint8_t>(scales),
                                kind, ptr<uint16_t>(out), ld, ptr<float>(dbias), s);
@@ -443,7 +482,7 @@ Tensor ckpt8_wgrad(const Tensor& q, const Tensor& scales, int64_t T, int64_t K, 
   const int64_t N = dY.size(1);
   if (beta != 0.0 && !out_) bad_value("beta != 0 reads dW: pass its prior contents as `out`");
   int64_t ldw = 0;
-  Tensor out = output(out_, "out", K, N, at::kFloat, device, &ldw);
+  Tensor out = output(out_, "out", K, N, at::kFloat, device, &ldw, stream);
   run("gemm_ckpt8_wgrad", device, stream, [&](void* s) {
     return gemm_ckpt8_wgrad(T, K, N, ptr(q), ptr<uint8_t>(scales), ptr<uint16_t>(dY), ld,
                             ptr<float>(out), ldw, static_cast<float>(beta), s);
@@ -544,15 +583,14 @@ std::tuple<Tensor, Tensor> fp8_quantize(const Tensor& X, bool square, bool trans
   const int64_t ld = K > 0 ? blocks(K) * kBlock : kBlock;
   Tensor codes, scales;
   if (X.dim() == 3) {
-    codes = at::detail::empty_strided_cuda({q.batch, R, K}, {R * ld, ld, 1}, at::kFloat8_e4m3fn,
-                                           device);
-    scales = empty({q.batch, blocks(R), blocks(K)}, at::kFloat, device);
+    codes = empty_strided({q.batch, R, K}, {R * ld, ld, 1}, at::kFloat8_e4m3fn, device, stream);
+    scales = empty({q.batch, blocks(R), blocks(K)}, at::kFloat, device, stream);
     q.codes_step = R * ld;
     q.scales_step = blocks(R) * blocks(K);
   } else {
-    codes = at::detail::empty_strided_cuda({R, K}, {ld, 1}, at::kFloat8_e4m3fn, device);
-    scales = square ? empty({blocks(R), blocks(K)}, at::kFloat, device)
-                    : empty({blocks(K), R}, at::kFloat, device);
+    codes = empty_strided({R, K}, {ld, 1}, at::kFloat8_e4m3fn, device, stream);
+    scales = square ? empty({blocks(R), blocks(K)}, at::kFloat, device, stream)
+                    : empty({blocks(K), R}, at::kFloat, device, stream);
   }
   if (codes.numel() == 0) return {codes, scales};
   q.codes = ptr(codes);
@@ -578,7 +616,7 @@ Tensor fp8(const Tensor& a_codes, const Tensor& a_scales, bool a_square, const T
   if (beta != 0.0 && !out_) bad_value("beta != 0 reads C: pass its prior contents as `out`");
   const at::ScalarType type = product_type(out_dtype, out_);
   int64_t ldc = 0;
-  Tensor out = output(out_, "out", M, N, type, device, &ldc);
+  Tensor out = output(out_, "out", M, N, type, device, &ldc, stream);
   if (bias) vector(*bias, "bias", device, N);
   const gemm_epilogue_t epi = {static_cast<float>(alpha), static_cast<float>(beta),
                                ptr<float>(bias), activation(act)};
@@ -620,7 +658,7 @@ Tensor fp8_experts(const Tensor& a_codes, const Tensor& a_scales, bool a_square,
   if (beta != 0.0 && !out_) bad_value("beta != 0 reads C: pass its prior contents as `out`");
   const at::ScalarType type = product_type(out_dtype, out_);
   int64_t ldc = 0;
-  Tensor out = output(out_, "out", M, N, type, device, &ldc);
+  Tensor out = output(out_, "out", M, N, type, device, &ldc, stream);
   if (bias && (bias->scalar_type() != at::kFloat || bias->device() != device || bias->dim() != 2 ||
                bias->size(0) != E || bias->size(1) != N || !bias->is_contiguous()))
     bad_value("bias must be contiguous float32, " + text(E) + " x " + text(N) + ", on " +
@@ -689,7 +727,7 @@ std::tuple<Tensor, Tensor, Tensor, Tensor, Tensor> route(
   // until the work of another stream than the current one has finished, as the outputs
   // have to.
   const int64_t bytes = gemm_route_workspace_bytes(a.T, a.E), n = a.T * k * 4;
-  Tensor block = empty({4 * n + (a.E + 1) * 4 + (bytes > 0 ? bytes : 0)}, at::kByte, device);
+  Tensor block = empty({4 * n + (a.E + 1) * 4 + (bytes > 0 ? bytes : 0)}, at::kByte, device, stream);
   Tensor index = part(block, at::kInt, {a.T, k}, 0);
   Tensor weight = part(block, at::kFloat, {a.T, k}, n);
   Tensor slot = part(block, at::kInt, {a.T, k}, 2 * n);
@@ -714,7 +752,7 @@ Tensor route_bwd(const Tensor& logits, const Tensor& index, const Tensor& d_weig
   pairs(index, "index", at::kInt, device, a.T, k);
   pairs(d_weight, "d_weight", at::kFloat, device, a.T, k);
   int64_t ld = 0;
-  Tensor out = output(out_, "out", a.T, a.E, logits.scalar_type(), device, &ld);
+  Tensor out = output(out_, "out", a.T, a.E, logits.scalar_type(), device, &ld, stream);
   run("gemm_route_bwd", device, stream, [&](void* s) {
     return gemm_route_bwd(&a, ptr<int32_t>(index), ptr<float>(d_weight), ptr(out), ld, s);
   });
@@ -758,7 +796,7 @@ Tensor combine(const Tensor& rows, const Tensor& slot, const Tensor& weight, con
                                           x ? x->scalar_type() : rows.scalar_type()),
                    out_);
   int64_t ld = 0;
-  Tensor out = output(out_, "out", a.T, a.D, type, device, &ld);
+  Tensor out = output(out_, "out", a.T, a.D, type, device, &ld, stream);
   run("gemm_combine", device, stream,
       [&](void* s) { return gemm_combine(&a, ptr(out), ld, abi_type(type), s); });
   return out;
@@ -772,10 +810,10 @@ std::tuple<Tensor, Tensor> combine_bwd(const Tensor& d_out, const Tensor& rows, 
   const int64_t ld_d =
       matrix(d_out, "d_out", {at::kFloat, at::kBFloat16}, device, a.T, a.D);
   int64_t ld = 0;
-  Tensor d_rows = output(d_rows_, "d_rows", a.R, a.D, rows.scalar_type(), device, &ld);
+  Tensor d_rows = output(d_rows_, "d_rows", a.R, a.D, rows.scalar_type(), device, &ld, stream);
   // Only the device knows which rows no slot names: theirs is the gradient of nothing.
   if (!d_rows_ && d_rows.numel() > 0) on_stream(device, stream, [&] { d_rows.zero_(); });
-  Tensor d_weight = empty({a.T, a.k}, at::kFloat, device);
+  Tensor d_weight = empty({a.T, a.k}, at::kFloat, device, stream);
   run("gemm_combine_bwd", device, stream, [&](void* s) {
     return gemm_combine_bwd(&a, ptr(d_out), ld_d, type_of(d_out), ptr(d_rows), ld,
                             ptr<float>(d_weight), s);

@@ -5,6 +5,8 @@ import itertools
 import pytest
 import torch
 
+from torch.utils._python_dispatch import TorchDispatchMode
+
 import dense_gemm_07_gb300 as g7
 from test_gpu_experts import BF16, F32, INF, NAN, _check_route, _gen, _randn
 
@@ -152,3 +154,81 @@ def test_combine_gradient_of_rows_without_a_slot(D, dtype):
     _leave(NAN, ((120, D), dtype))
     got, _ = g7.gemm_combine_bwd(d, rows, empty, empty.float())
     assert torch.equal(got, torch.zeros_like(got))
+
+
+class _Seen(TorchDispatchMode):
+    def __init__(self):
+        super().__init__()
+        self.names = []
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        self.names.append(str(func))
+        return func(*args, **(kwargs or {}))
+
+
+def _calls(stream=None):
+    """What makes its own tensors, of the operators with rows that a call leaves alone
+    first: their names and outputs."""
+    g = _gen(9)
+    x, rows = _randn(g, 50, 256, dtype=BF16), _randn(g, 150, 64)
+    logits = _randn(g, 50, 8)
+    logits[40:] = -INF
+    r = g7.gemm_route(logits, 3)
+    a = g7.gemm_fp8_quantize(x, index=r.source)
+    w = g7.gemm_fp8_quantize(_randn(g, 8, 96, 256), square=True)
+    few = g7.gemm_fp8_quantize(_randn(g, 96, 256), square=True)
+    n = int(r.offsets[-1])
+    torch.cuda.synchronize()
+
+    def experts():
+        out = g7.gemm_fp8_experts(a, w, r.offsets, stream=stream)
+        return out[:n], out[n:]
+
+    return experts, dict(
+        route=lambda: g7.gemm_route(logits, 3, stream=stream),
+        quantize=lambda: g7.gemm_fp8_quantize(x, transpose=True, stream=stream)[:2],
+        fp8=lambda: (g7.gemm_fp8(a, few, stream=stream),),
+        route_bwd=lambda: (g7.gemm_route_bwd(logits, r.index, r.weight, stream=stream),),
+        combine=lambda: (g7.gemm_combine(rows, r.slot, r.weight, stream=stream),),
+        combine_bwd=lambda: g7.gemm_combine_bwd(rows[:50], rows, r.slot, r.weight, stream=stream),
+        norm=lambda: (g7.gemm_norm_gate(x, x, stream=stream)[0],),
+        ckpt8=lambda: g7.gemm_ckpt8_pack(x.float(), activation="gelu", stream=stream)[1:])
+
+
+def _same(u, v):
+    as_bytes = lambda t: t.contiguous().view(torch.uint8)  # noqa: E731
+    return torch.equal(as_bytes(u), as_bytes(v))
+
+
+@pytest.mark.parametrize("other", [False, True])
+def test_new_tensors_are_filled_in_deterministic_mode(other):
+    """torch's deterministic mode fills memory that nothing has been written to, on the
+    stream that the call runs on; what a call writes is the same."""
+    stream = torch.cuda.Stream() if other else None
+    experts, calls = _calls(stream)
+    want = {name: f() for name, f in calls.items()}
+    written = experts()[0]
+    torch.cuda.synchronize()
+    torch.use_deterministic_algorithms(True)
+    try:
+        for _ in range(5):
+            _leave(0.0, ((150, 96), F32))
+            got, rest = experts()
+            torch.cuda.synchronize()
+            assert torch.equal(got, written) and rest.numel() > 0 and bool(rest.isnan().all())
+            for name, f in calls.items():
+                out = f()
+                torch.cuda.synchronize()
+                assert all(_same(u, v) for u, v in zip(out, want[name])), name
+    finally:
+        torch.use_deterministic_algorithms(False)
+
+
+def test_new_tensors_are_seen_by_dispatch_modes():
+    experts, calls = _calls()
+    for name, f in [("experts", experts), *calls.items()]:
+        want = f()
+        with _Seen() as seen:
+            got = f()
+        assert any(n.startswith("aten.empty") for n in seen.names), (name, seen.names)
+        assert all(_same(u, v) for u, v in zip(got, want) if u.numel() and name != "experts"), name
