@@ -146,9 +146,11 @@ def _compile_binding(torch_dir: str) -> str:
 
 def _link_binding(torch_dir: str, obj: str) -> None:
     libs = os.path.join(torch_dir, "lib")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
     tmp = BINDING_PATH + f".tmp{os.getpid()}"
     _run(["g++", "-shared", "-o", tmp, obj, f"-L{LIB_DIR}", "-lgemm07", f"-L{libs}", "-lc10",
-          "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN",
+          "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
+          f"-L{os.path.join(cuda, 'lib64')}", "-lcudart", "-Wl,-rpath,$ORIGIN",
           f"-Wl,-rpath,{libs}"], "linking layer_binding.so")
     os.replace(tmp, BINDING_PATH)
     with open(BINDING_STAMP, "w") as f:

@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <initializer_list>
@@ -811,10 +812,14 @@ std::tuple<Tensor, Tensor> combine_bwd(const Tensor& d_out, const Tensor& rows, 
       matrix(d_out, "d_out", {at::kFloat, at::kBFloat16}, device, a.T, a.D);
   int64_t ld = 0;
   Tensor d_rows = output(d_rows_, "d_rows", a.R, a.D, rows.scalar_type(), device, &ld, stream);
-  // Only the device knows which rows no slot names: theirs is the gradient of nothing.
-  if (!d_rows_ && d_rows.numel() > 0) on_stream(device, stream, [&] { d_rows.zero_(); });
   Tensor d_weight = empty({a.T, a.k}, at::kFloat, device, stream);
   run("gemm_combine_bwd", device, stream, [&](void* s) {
+    // Only the device knows which rows no slot names: theirs is the gradient of nothing.
+    // (Tensor::zero_ takes 5 us more of the host's time.)
+    if (!d_rows_ && d_rows.numel() > 0 &&
+        cudaMemsetAsync(d_rows.data_ptr(), 0, d_rows.nbytes(), static_cast<cudaStream_t>(s)) !=
+            cudaSuccess)
+      return GEMM_ERR_LAUNCH;
     return gemm_combine_bwd(&a, ptr(d_out), ld_d, type_of(d_out), ptr(d_rows), ld,
                             ptr<float>(d_weight), s);
   });
