@@ -409,21 +409,34 @@ std::atomic<uint64_t> g_allowed, g_registers;
 
 }  // namespace
 
+// The most units of 128 rows there are (experts: only the device knows their rows).
+int units_of(const Fp8GemmArgs& a) {
+  return a.E == 0 ? (a.M + TILE_M - 1) / TILE_M : a.M / TILE_M + (a.E < a.M ? a.E : a.M);
+}
+
 // Many rows, for which a thread of fp8_wide has one scale of A for 128 columns, where
-// one of fp8_few reads the scales of its columns: measured, in us one after another (few,
-// wide): 256 x 4096 x 4096 15, 21 (M x N x K, 32 tiles); 384 x 4096 x 4096 20.8, 21.2 (48);
-// 512 x 4096 x 4096 21.0, 21.3 (64); 700 x 3000 x 2000 16, 14 (72); 2048^3 19, 14; 4096 x
-// 11008 x 4096 260, 191.  Experts, by their average number of rows: 64: 512 rows of 8,
-// 4096 x 4096, 31.4, 30.5 and 4096 rows of 64, 2048 x 4096, 110, 105; 100: 6000 rows of 60,
-// 2000 x 500, 40, 29; 125: 1500 rows of 12, 700 x 2000, 16.4, 15.2; 256: 226, 187; 2048:
-// 197, 142.  Where B's rows have scales of their own, both have to be read per column, and
-// fp8_few's narrower tiles are faster (4096 x 11008 x 4096: 306, 318 with an L2 flush).
+// one of fp8_few reads the scales of its columns, and enough tiles, of which fp8_wide does
+// not share K: measured, in us one after another (few, wide), M x N x K.
+// By tiles: 256 x 4096 x 4096 15, 21 (32); 384 x 4096 x 4096 22.0, 22.0 (48); 512 x 4096 x
+// 4096 22.2, 22.1 (64); 700 x 3000 x 2000 16.7, 13.9 (72); 300 x 8192 x 4096 30.6, 22.3
+// (96); 2048^3 18.8, 14.1; 4096 x 11008 x 4096 260, 191.  By rows, where the tiles are
+// enough: 1 x 16384 x 4096 16.1, 21.8; 16 x 32000 x 4096 26.6, 36.0; 32 x 128256 x 4096
+// 92.5, 100.6; 64 x 16384 x 4096 18.1, 22.4; 64 x 32000 x 4096 28.0, 28.7; 65 x 32000 x
+// 4096 29.0, 28.6; 128 x 16384 x 4096 22.8, 22.9; 128 x 32000 x 4096 33.0, 29.7; 129 x
+// 16384 x 4096 31.2, 23.2.  Experts, by their average number of rows: 48 rows of 8, 4096 x
+// 4096, 29.2, 30.0 and of 64, 4096 x 2048, 111.7, 100.4; 64 rows of 8, 4096 x 4096, 31.8,
+// 30.1 and of 64, 4096 x 2048, 119, 109; 128 rows of 16, 2048 x 4096, 53, 47; 2048 rows of
+// 8, 2048 x 4096, 197, 142; by tiles: 64 rows of 1, 4096 x 4096, 9.6, 21.0 (16); 1000 rows
+// of 1, 1024 x 2048, 12.6, 13.7 (32); 256 rows of 8, 512 x 4096, 21.5, 21.8 (48); 128 rows
+// of 8, 1024 x 1024, 10.5, 10.1 (64).  Where B's rows have scales of their own, both have
+// to be read per column, and fp8_few's narrower tiles are faster (4096 x 11008 x 4096: 306,
+// 318 with an L2 flush).
 bool fp8_takes_wide(const Fp8GemmArgs& a, const LayerDevice& dev) {
   if (a.K == 0 || !a.b_square) return false;
-  if (a.E > 0) return a.M / a.E >= TILE_M / 2;
-  const int64_t tiles = (static_cast<int64_t>(a.M) + TILE_M - 1) / TILE_M *
+  const int64_t tiles = static_cast<int64_t>(units_of(a)) *
                         ((static_cast<int64_t>(a.N) + TILE_N - 1) / TILE_N);
-  return 5 * tiles >= 2 * dev.sms;
+  const bool rows = a.E > 0 ? a.M / a.E >= TILE_M / 2 : a.M > TILE_M / 2;
+  return rows && 5 * tiles >= 2 * dev.sms;
 }
 
 cudaError_t launch_fp8_wide(const CUtensorMap& tmA, const CUtensorMap& tmB, const Fp8GemmArgs& a,
@@ -432,9 +445,7 @@ cudaError_t launch_fp8_wide(const CUtensorMap& tmA, const CUtensorMap& tmB, cons
   // The roles' register shares are drawn from what the block is launched with.
   if (e == cudaSuccess) e = check_registers(fp8_wide_kernel, kRegsBlock, THREADS, &g_registers);
   if (e != cudaSuccess) return e;
-  WideArgs p = {a, (a.N + TILE_N - 1) / TILE_N, 0, dev.status};
-  // (experts: at most this many units, of rows that only the device knows)
-  p.units = a.E == 0 ? (a.M + TILE_M - 1) / TILE_M : a.M / TILE_M + (a.E < a.M ? a.E : a.M);
+  const WideArgs p = {a, (a.N + TILE_N - 1) / TILE_N, units_of(a), dev.status};
   const int64_t tiles = static_cast<int64_t>(p.units) * p.n_tiles;
   if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};

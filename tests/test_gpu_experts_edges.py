@@ -4,11 +4,13 @@ import itertools
 
 import pytest
 import torch
-
 from torch.utils._python_dispatch import TorchDispatchMode
 
 import dense_gemm_07_gb300 as g7
-from test_gpu_experts import BF16, F32, INF, NAN, _check_route, _gen, _randn
+import experts_reference as ref
+from layer_reference import EPS32
+from test_gpu_experts import (BF16, F32, INF, NAN, STEP, _check_route, _close, _experts_case, _gen,
+                              _product_tol, _randn, _status)
 
 pytestmark = pytest.mark.gpu
 
@@ -232,3 +234,59 @@ def test_new_tensors_are_seen_by_dispatch_modes():
             got = f()
         assert any(n.startswith("aten.empty") for n in seen.names), (name, seen.names)
         assert all(_same(u, v) for u, v in zip(got, want) if u.numel() and name != "experts"), name
+
+
+# ---------------------------------------------------------------- products
+
+# rows an expert and columns on each side of the rules that choose the tiles
+SEGMENTS = [([10, 20, 6], 200, 256), ([3] * 70, 130, 640), ([40, 2, 60], 257, 1024),
+            ([100, 200, 60], 4100, 256), ([70] * 40, 300, 200), ([128, 1, 129, 0, 256], 2100, 385),
+            ([300, 20, 0, 700, 1], 1300, 640), ([1000], 2200, 300), ([257, 255, 511, 513, 2, 90], 1100, 300)]
+
+
+@pytest.mark.parametrize("lengths,N,K", SEGMENTS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_outside_the_offsets_stay(lengths, N, K, dtype):
+    """Rows that no expert has are left as they were, and offsets that make no sense are
+    held to the rows there are and to their running maximum."""
+    E, M = len(lengths), sum(lengths)
+    g, a, b, offsets = _experts_case(E + K, lengths, N, K)
+    va, vb = ref.values(*a), ref.values(*b)
+    good = offsets.tolist()
+    inner = [good[1], *good[1:-1], good[-2]]            # rows before and behind the experts'
+    wild = [-7, *good[1:]]
+    wild[E // 2] = wild[max(E // 2 - 1, 0)] - 1         # one goes back
+    wild[-1] = 2 ** 31 - 1
+    back = [v if i % 2 else -2 ** 31 for i, v in enumerate(good)]
+    for given in (good, inner, wild, back, [M + 9] * (E + 1), [0] * (E + 1), [M] + [0] * E):
+        held, top = [], 0
+        for v in given:
+            top = max(top, min(max(v, 0), M))
+            held.append(top)
+        old = _randn(g, M, N, dtype=dtype)
+        out = g7.gemm_fp8_experts(a, b, torch.tensor(given, dtype=torch.int32, device="cuda"),
+                                  out=old.clone(), alpha=2.0, beta=0.5)
+        want, tol = old.double(), torch.zeros((M, N), dtype=torch.float64, device="cuda")
+        for e in range(E):
+            r = slice(held[e], held[e + 1])
+            v = va[r] @ vb[e].t()
+            want[r] = 2.0 * v + 0.5 * old[r].double()
+            size = 2.0 * _product_tol(va[r], vb[e], K) + 4 * EPS32 * (2 * v.abs() + old[r].double().abs())
+            tol[r] = size + STEP[dtype] * (want[r].abs() + size)
+        _close(out, want, tol, str(given[:8]))
+    _status()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 16400, 640), (16, 16384, 512), (64, 16385, 300), (65, 15700, 300),
+                                   (128, 15500, 256)])
+def test_few_rows_of_many_columns(M, N, K):
+    """On each side of the rule by rows; one expert with all rows is the same product."""
+    g, a, b, offsets = _experts_case(M, [M], N, K)
+    va, vb = ref.values(*a), ref.values(*b)[0]
+    bias = _randn(g, 1, N)
+    want, tol = va @ vb.t() + bias.double(), _product_tol(va, vb, K)
+    tol = tol + 4 * EPS32 * ((va @ vb.t()).abs() + bias.double().abs())
+    dense = g7.gemm_fp8(a, g7.Fp8(b.codes[0], b.scales[0], True), bias=bias[0])
+    _close(dense, want, tol, "dense")
+    _close(g7.gemm_fp8_experts(a, b, offsets, bias=bias), want, tol, "experts")
+    _status()
