@@ -57,7 +57,7 @@ def gemm_fp8_experts(a, b, offsets, out=None, alpha=1.0, beta=0.0, bias=None, ac
     (an Fp8, M x K) with the e-th matrix of b (an Fp8 of E x N x K, square).
 
     offsets: int32, E + 1, on the device (Routing.offsets); rows outside of them are
-    not written.  bias: float32, E x N."""
+    not written, and hold anything in an out that the call makes.  bias: float32, E x N."""
     return _binding().fp8_experts(*a, *b, offsets, out, alpha, beta, bias, activation, out_dtype,
                                   _handle(stream))
 

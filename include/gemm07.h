@@ -127,7 +127,7 @@ GEMM07_API gemm_status_t gemm_bf16_f32acc(int64_t M, int64_t N, int64_t K,
  */
 typedef enum gemm_activation {
     GEMM_ACT_NONE = 0,
-    GEMM_ACT_RELU = 1,     /* max(x, 0) */
+    GEMM_ACT_RELU = 1,     /* max(x, 0); 0 for a NaN */
     GEMM_ACT_GELU = 2      /* x * Phi(x) = 0.5 x (1 + erf(x / sqrt 2)), FP32 erff;
                               the element-wise GELU of "GEMM Optimization" */
 } gemm_activation_t;
@@ -703,6 +703,9 @@ GEMM07_API gemm_status_t gemm_fp8_quantize(const gemm_fp8_quantize_args_t *args,
  * epilogue as for gemm_bf16_f32acc_ex (NULL: the product).
  *   The products of codes of a block of 128 k are added on the tensor cores, their
  *   sum times both scales in FP32; C is rounded once.
+ *   GELU is that of gemm_bf16_f32acc_ex for some sizes and a published polynomial for
+ *   others, each within 2^-20 |x| of x * Phi(x) in FP32.  NaN codes give NaN, which ReLU
+ *   turns into 0.
  *   Gradients are the same operator: dA from dC quantised by rows and B transposed
  *   (gemm_fp8_quantize with square and transpose); dB from dC and A both transposed.
  */
@@ -733,7 +736,7 @@ GEMM07_API gemm_status_t gemm_fp8_experts(int64_t E, int64_t M, int64_t N, int64
  *   lowest expert.  With groups_kept < groups, only from the groups_kept groups (of
  *   E / groups consecutive experts) whose group_top (1 or 2) largest s + bias have
  *   the largest sum, ties to the lowest group.  Comparisons are decided as in 64
- *   bits; without a bias those of experts by the logits.
+ *   bits; without a bias those of experts, and of groups with group_top 1, by the logits.
  *   An expert with the logit -infinity, or with s + bias of -infinity or NaN, is not
  *   chosen.  A token with fewer than k others has the index -1 and the weight 0 in
  *   the places left (a token of padding: all logits -infinity).  A token with a logit

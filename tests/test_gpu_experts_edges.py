@@ -8,7 +8,7 @@ from torch.utils._python_dispatch import TorchDispatchMode
 
 import dense_gemm_07_gb300 as g7
 import experts_reference as ref
-from layer_reference import EPS32
+from layer_reference import EPS32, act
 from test_gpu_experts import (BF16, F32, INF, NAN, STEP, _check_route, _close, _experts_case, _gen,
                               _product_tol, _randn, _status)
 
@@ -83,6 +83,21 @@ def test_route_all_places_taken():
         for b in (bias, torch.zeros_like(bias), near):
             _check_route(logits, 32, score="sigmoid", bias=b)
             _check_route(logits[:1] + 1e-7 * _randn(g, 200, E), 32, score="sigmoid", bias=b)
+
+
+def test_route_logits_whose_scores_are_equal():
+    """Sigmoids that are 1, and softmax scores that are 0, in 64 bits too: without a bias
+    the logits tell experts, and groups of one expert each, apart."""
+    up = torch.tensor([[40.0, 50.0, 41.0, 60.0, -1.0, 70.0]], device="cuda")
+    down = torch.tensor([[-900.0, -950.0, -990.0, -800.0, 3.0, -801.0]], device="cuda")
+    for logits, score in ((up, "sigmoid"), (down, "softmax"), (down, "sigmoid")):
+        want = logits.sort(dim=1, descending=True).indices
+        r = g7.gemm_route(logits, 4, score=score)
+        assert r.index.tolist() == want[:, :4].tolist(), score
+        best = logits.view(3, 2).amax(1).sort(descending=True).indices[:2].tolist()
+        inside = [e for e in want[0].tolist() if e // 2 in best]
+        r = g7.gemm_route(logits, 4, score=score, groups=3, groups_kept=2, group_top=1)
+        assert r.index[0].tolist() == inside, score
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
@@ -290,3 +305,43 @@ def test_few_rows_of_many_columns(M, N, K):
     _close(dense, want, tol, "dense")
     _close(g7.gemm_fp8_experts(a, b, offsets, bias=bias), want, tol, "experts")
     _status()
+
+
+@pytest.mark.parametrize("M,N,K", [(8, 300, 2000), (16, 128, 640), (600, 4100, 300)])
+def test_one_expert_with_all_rows_is_the_dense_product(M, N, K):
+    """On the same tiles with the same parts of K, so bit for bit."""
+    g, a, b, offsets = _experts_case(M, [M], N, K)
+    bias = _randn(g, 1, N)
+    dense = g7.gemm_fp8(a, g7.Fp8(b.codes[0], b.scales[0], True), bias=bias[0], activation="gelu")
+    assert torch.equal(g7.gemm_fp8_experts(a, b, offsets, bias=bias, activation="gelu"), dense)
+
+
+@pytest.mark.parametrize("M,N", [(5, 3000), (200, 16400)])
+@pytest.mark.parametrize("size", [2.0 ** -12, 2.0 ** -6, 1.0])
+def test_gelu_of_both_kernels(M, N, size):
+    """K = 1: a product of two codes is exact and its sum with the bias one rounding, so
+    that the activation's argument is known; 2^-20 of it is allowed."""
+    g = _gen(M)
+    a = g7.gemm_fp8_quantize(_randn(g, M, 1))
+    b = g7.gemm_fp8_quantize(_randn(g, N, 1), square=True)
+    bias = _randn(g, N, scale=3.0 * size)
+    b = g7.Fp8(b.codes, b.scales * size, True)
+    v = (ref.values(*a) @ ref.values(*b).t()).float() + bias
+    got = g7.gemm_fp8(a, b, bias=bias, activation="gelu")
+    _close(got, act(v.double(), "gelu"), 2.0 ** -20 * v.double().abs() + 1e-40)
+
+
+@pytest.mark.parametrize("M,N", [(5, 300), (200, 16400)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_activations_of_nan(M, N, dtype):
+    """A block that was not finite is NaN, through GELU too; ReLU gives 0."""
+    g = _gen(N)
+    x = _randn(g, M, 200)
+    x[1, 150], x[4, 3] = INF, NAN
+    a, b = g7.gemm_fp8_quantize(x), g7.gemm_fp8_quantize(_randn(g, N, 200), square=True)
+    rest = [i for i in range(M) if i not in (1, 4)]
+    for kind in ("none", "gelu", "relu"):
+        out = g7.gemm_fp8(a, b, activation=kind, out_dtype=dtype)
+        bad = out[[1, 4]]
+        assert bool((bad == 0).all() if kind == "relu" else bad.isnan().all()), kind
+        assert not bool(out[rest].isnan().any())
