@@ -15,9 +15,9 @@
 //
 // What bounds it is the turn of an accumulator, MMAs, signal, reading, signal, which the
 // two hide only in part: four MMAs of 128 x 256 x 32 take 641 clocks back to back (of
-// 128 x 128 x 32 404), a block of K about 1040 (1024 x 4864 x 8192 less 1024 x 4864 x 4096,
-// one tile an SM: 534 ns at 2.0 GHz).  4096 x 4096 x 11008: 195 us, 1.89
-// PFLOP/s, 49 % of twice the measured BF16 rate; 226 with bias and GELU, whose
+// 128 x 128 x 32 404; timed apart, by a program that is not kept), a block of K about 1040
+// (1024 x 4864 x 8192 less 1024 x 4864 x 4096, one tile an SM: 534 ns at 2.0 GHz).  4096 x
+// 4096 x 11008: 195 us, 1.89 PFLOP/s, 49 % of twice the measured BF16 rate; 226 with bias and GELU, whose
 // exponentials and quotients keep the sum warps from the next tile; 16384 rows of 64
 // experts, 4096 x 2048, 197 us.  The last of ten waves has 8 tiles of 152.
 //
