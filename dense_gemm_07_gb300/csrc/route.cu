@@ -223,6 +223,18 @@ __device__ __forceinline__ float sigmoid_over(float l, float shift) {
   return top / (1.0f + e);
 }
 
+// The logit of this lane's expert e (0 for -1), from the token's.
+template <int V>
+__device__ __forceinline__ float logit_of(const float (&l)[V], int e) {
+  float v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float x = __shfl_sync(kAll, l[i], e & 31);
+    if (i == e >> 5) v = x;
+  }
+  return v;
+}
+
 // The choice in 64 bits, from the definition: the token's logits, and in `score` the
 // sigmoid of each, or its exponential for softmax.
 template <int V>
@@ -255,6 +267,11 @@ __device__ __forceinline__ int choose_64(const RouteArgs& a, const float (&l)[V]
   const int first = pick<V>(key, a.k).index;
   const int at = lane < a.k ? first : -1;
   double w = at < 0 ? 0.0 : a.sigmoid ? score[at] : score[at] / total;
+  if (a.renorm && !a.sigmoid) {  // over the chosen alone, as FP32 does: theirs may all be 0
+    const float chosen = logit_of<V>(l, first);
+    const float most = value_of(warp_max(at >= 0 ? key_of(plain_zero(chosen)) : 0u));
+    if (at >= 0) w = exp(static_cast<double>(chosen) - static_cast<double>(most));
+  }
   if (a.renorm) {
     const double sum = warp_sum(w);
     w = sum > 0.0 ? w / sum : 0.0;
@@ -356,17 +373,8 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, const float (&l)[
     for (int i = 0; i < V; ++i) key[i] = key_of(plain_zero(l[i]));
   }
 
-  auto logit = [&](int e) {  // of this lane's expert e
-    float v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float x = __shfl_sync(kAll, l[i], e & 31);
-      if (i == e >> 5) v = x;
-    }
-    return v;
-  };
   const Choice<uint32_t> c = pick<V>(key, a.k);
-  float chosen = logit(c.index);
+  const float chosen = logit_of<V>(l, c.index);
   const int at = lane < a.k ? c.index : -1;
   if (a.bias) {
     // every two that follow each other have to be told apart, or equal in everything

@@ -741,8 +741,9 @@ GEMM07_API gemm_status_t gemm_fp8_experts(int64_t E, int64_t M, int64_t N, int64
  *   chosen.  A token with fewer than k others has the index -1 and the weight 0 in
  *   the places left (a token of padding: all logits -infinity).  A token with a logit
  *   that is NaN (for softmax also +infinity) has no expert, and NaN weights.
- *   Weights: scale * s of the chosen, divided by their sum when renormalize is set
- *   (0 where that sum is 0).
+ *   Weights: scale * s of the chosen, divided by their sum when renormalize is set (for
+ *   softmax a softmax over the chosen alone, also where their s leave 64 bits; for sigmoid
+ *   0 where that sum is 0).
  * Outputs: index (T x k, in the order of the choice), weight (T x k), and the chosen
  * pairs sorted by expert, then by token: slot (T x k): a pair's row in that order, -1
  * without an expert; source (T * k): the token of each row, -1 past the last;

@@ -100,6 +100,27 @@ def test_route_logits_whose_scores_are_equal():
         assert r.index[0].tolist() == inside, score
 
 
+@pytest.mark.parametrize("low", [-30.0, -900.0, torch.finfo(F32).min])
+def test_route_chosen_scores_that_leave_64_bits(low):
+    """Renormalised softmax weights are a softmax over the chosen, however far below the
+    largest logit they are, whichever precision chose them; their gradient is that's."""
+    logits = torch.full((6, 4), low, device="cuda")
+    logits[:, 0] = 1.0
+    logits[:, 2] -= 1.0
+    want = torch.softmax(logits[:, 1:3].double(), 1)
+    d = torch.tensor([[1.0, -2.0]], device="cuda").repeat(6, 1)
+    for near in (0.5, 0.25):            # (equal biases: scores of 0 that FP32 cannot tell)
+        bias = torch.tensor([-INF, 0.5, near, -4.0], device="cuda")
+        r = g7.gemm_route(logits, 2, bias=bias)
+        assert r.index.tolist() == [[1, 2]] * 6
+        _close(r.weight, want, 8 * EPS32 * want, near)
+        got = g7.gemm_route_bwd(logits, r.index, d)
+        grad = want * (d.double() - (d.double() * want).sum(1, keepdim=True))
+        full = torch.zeros(6, 4, dtype=torch.float64, device="cuda")
+        full[:, 1:3] = grad
+        _close(got, full, 16 * EPS32 * full.abs(), near)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_route_gradient_of_closed_experts(score, dtype):
