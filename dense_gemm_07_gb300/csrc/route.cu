@@ -16,11 +16,12 @@
 // The instructions of the choice bound it, about 1500 a token of 256 experts at 2.9 a
 // clock, on 128 of 152 SMs (a block for each 128 tokens), and then the block with the
 // most tokens that need 64 bits: 16384 x 256, sigmoid, bias, 4 of 8 groups, 8 chosen, 54
-// to 60 us a call by the inputs (the logits are 17 MB, 2.5 us), 68000 clocks of an average block and 99000 of
-// the busiest.  128 x 256 is one block and takes 32 us.  Loops that are not written out
-// matter: a choice's code written out does not stay in the instruction cache (74 against
-// 58 us under the profiler).  So do the tokens that need 64 bits: chosen by a warp alone,
-// with the other warps waiting, 70 us with an L2 flush, by all warps together 62.
+// to 60 us a call by the inputs (the logits are 17 MB, 2.5 us), 68000 clocks of an
+// average block and 99000 of the busiest.  128 x 256 is one block and takes 32 us.  Loops
+// that are not written out matter: a choice's code written out does not stay in the
+// instruction cache (74 against 58 us under the profiler).  So do the tokens that need 64
+// bits: chosen by a warp alone, with the other warps waiting, 70 us with an L2 flush, by
+// all warps together 62.
 #include <cfloat>
 
 #include "experts.h"
